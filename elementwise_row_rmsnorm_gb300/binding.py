@@ -75,6 +75,11 @@ def lib() -> ctypes.CDLL:
                 "gbe_sample": [vp, vp, vp, i64, i64, i32, f32, i64, f32, i32, vp],
                 "gbe_sample_seeded": [vp, vp, i64, i64, i32, f32, i64, f32, u64, u64, i32, vp],
                 "gbe_pcg64_uniforms": [vp, i64, u64, u64, vp],
+                "gbe_kv_write": [vp, i64, vp, i64, vp, i64, vp, vp, i32, vp],
+                "gbe_kv_read": [vp, i64, vp, i64, vp, i64, vp, vp, i32, vp],
+                "gbe_attn_decode": [vp, i64, vp, i64, i64, i64, vp, vp, i64, vp, f32, vp, i64, i32, vp],
+                "gbe_attn_decode_workspace": [i64, i64, i64, i64, i64, i64],
+                "gbe_attn_prompt": [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, f32, i32, vp],
                 "gbe_version": [],
                 "gbe_last_cuda_error": [],
                 "gbe_status_string": [i32],
@@ -82,7 +87,8 @@ def lib() -> ctypes.CDLL:
             for name, args in sigs.items():
                 fn = getattr(L, name)
                 fn.argtypes = args
-                fn.restype = ctypes.c_char_p if name == "gbe_status_string" else ctypes.c_int
+                fn.restype = {"gbe_status_string": ctypes.c_char_p,
+                              "gbe_attn_decode_workspace": i64}.get(name, ctypes.c_int)
             _lib = L
     return _lib
 
@@ -425,7 +431,176 @@ def gbe_pcg64_uniforms(u, seed: int, offset: int = 0, stream=None) -> None:
     _check("gbe_pcg64_uniforms", lib().gbe_pcg64_uniforms(_ptr(u), u.numel(), seed, offset, _stream(stream)))
 
 
+class _KvCacheStruct(ctypes.Structure):
+    """gbe_kv_cache of the C header."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("Hkv", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("D", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
+
+
+_KV_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2}
+
+
+class KvCache:
+    """A paged key-value cache of one layer: k and v are [n_pages, Hkv,
+    page_size, D] tensors (float32, bfloat16 or float8_e4m3fn) whose pages are
+    contiguous and share a stride (the halves k = kv[:, 0], v = kv[:, 1] of one
+    [n_pages, 2, Hkv, page_size, D] tensor will do); a float8_e4m3fn cache also
+    has k_scale and v_scale, uint8 [n_pages, Hkv, page_size].  Holds the
+    tensors and their description; no state of its own."""
+    __slots__ = ("k", "v", "k_scale", "v_scale", "shape", "desc", "ptr")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        shape, st = k.shape, k.stride()
+        if len(shape) != 4 or v.shape != shape or k.dtype not in _KV_DTYPES or v.dtype != k.dtype:
+            raise ValueError("KvCache: k and v are [n_pages, Hkv, page_size, D], float32, bfloat16 or float8_e4m3fn")
+        N, H, P, D = shape
+        if N > 1:
+            if v.stride() != st or st[1:] != (P * D, D, 1):
+                raise ValueError("KvCache: the pages of k and v are contiguous and share a stride")
+        elif not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("KvCache: the pages of k and v are contiguous and share a stride")
+        scales = (k_scale, v_scale)
+        if k.dtype == torch.float8_e4m3fn:
+            for s in scales:
+                if s is None or s.dtype != torch.uint8 or s.shape != (N, H, P) or not s.is_contiguous():
+                    raise ValueError("KvCache: a float8_e4m3fn cache has uint8 scales [n_pages, Hkv, page_size]")
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("KvCache: only a float8_e4m3fn cache has scales")
+        for t in (k, v, *scales):
+            if t is not None and not _on_device(t):
+                raise ValueError("tensors must be on the CUDA device or in pinned host memory")
+        self.k, self.v, self.k_scale, self.v_scale, self.shape = k, v, k_scale, v_scale, shape
+        self.desc = _KvCacheStruct(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), N, H, P, D,
+                                   st[0] if N > 1 else H * P * D, _KV_DTYPES[k.dtype])
+        self.ptr = ctypes.addressof(self.desc)
+
+
+def _kv_sides(what, k, v, cache, slots, bad):
+    T, H, sk = _rows_view(k, cache.shape[3])
+    Tv, Hv, sv = _rows_view(v, cache.shape[3])
+    if Tv != T or H != cache.shape[1] or Hv != H:
+        raise ValueError(f"{what}: k and v are [T, Hkv, D] with the cache's Hkv and D")
+    if slots.dtype != torch.int32 or slots.numel() != T or not slots.is_contiguous():
+        raise ValueError(f"{what}: slots is int32[T]")
+    if bad is not None and (bad.dtype != torch.int32 or bad.numel() != 1):
+        raise ValueError(f"{what}: bad_slot_count is one int32")
+    for t in (k, v, slots, bad):
+        if t is not None and not _on_device(t):
+            raise ValueError("tensors must be on the CUDA device or in pinned host memory")
+    return k.data_ptr(), sk, v.data_ptr(), sv, slots.data_ptr(), T, cache.ptr, _ptr(bad), _dt(k, v)
+
+
+def gbe_kv_write(k, v, slots, cache: KvCache, bad_slot_count=None, stream=None) -> None:
+    """k, v: [T, Hkv, D] views with contiguous heads (slices of a QKV buffer will do); slots: int32[T], page *
+    page_size + row, -1 for a token that is not stored."""
+    _check("gbe_kv_write", lib().gbe_kv_write(*_kv_sides("kv_write", k, v, cache, slots, bad_slot_count),
+                                              _stream(stream)))
+
+
+def gbe_kv_read(k, v, slots, cache: KvCache, bad_slot_count=None, stream=None) -> None:
+    """k, v: [T, Hkv, D] outputs of the model's dtype, views with contiguous heads; slots as for gbe_kv_write."""
+    _check("gbe_kv_read", lib().gbe_kv_read(*_kv_sides("kv_read", k, v, cache, slots, bad_slot_count),
+                                            _stream(stream)))
+
+
+def attn_decode_workspace(B: int, Hq: int, cache: KvCache, max_pages: int) -> int:
+    """Bytes of workspace of gbe_attn_decode for B sequences of at most max_pages pages."""
+    _, H, P, D = cache.shape
+    n = lib().gbe_attn_decode_workspace(B, Hq, H, D, P, max_pages)
+    if n < 0:
+        raise ValueError("attn_decode: sizes out of range (Hq a multiple of Hkv, D a multiple of 8 up to 256, ...)")
+    return n
+
+
+def gbe_attn_decode(q, out, cache: KvCache, table, lens, scale: float, workspace=None, stream=None) -> None:
+    """q, out: [B, Hq, D]; table: int32[B, max_pages]; lens: int32[B], the new token included; workspace: any tensor
+    of attn_decode_workspace bytes (None when that is 0)."""
+    B, Hq, sq = _rows_view(q, cache.shape[3])
+    _, _, so = _rows_view(out, cache.shape[3])
+    if out.shape != q.shape:
+        raise ValueError("attn_decode: out has q's shape")
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B or not table.is_contiguous():
+        raise ValueError("attn_decode: table is int32[B, max_pages]")
+    if lens.dtype != torch.int32 or lens.numel() != B or not lens.is_contiguous():
+        raise ValueError("attn_decode: lens is int32[B]")
+    for t in (q, out, table, lens, workspace):
+        if t is not None and not _on_device(t):
+            raise ValueError("tensors must be on the CUDA device or in pinned host memory")
+    room = 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        room = workspace.numel() * workspace.element_size()
+    _check("gbe_attn_decode", lib().gbe_attn_decode(
+        q.data_ptr(), sq, out.data_ptr(), so, B, Hq, cache.ptr, table.data_ptr(), table.shape[1], lens.data_ptr(),
+        scale, _ptr(workspace), room, _dt(q, out), _stream(stream)))
+
+
+def gbe_attn_prompt(q, k, v, out, starts, scale: float, stream=None) -> None:
+    """q, out: [T, Hq, D], k, v: [T, Hkv, D] views with contiguous heads; starts: int32[n_seqs + 1]; rows outside
+    [starts[0], starts[-1]) of out are left as they were."""
+    D = q.shape[-1]
+    T, Hq, sq = _rows_view(q, D)
+    Tk, Hkv, sk = _rows_view(k, D)
+    Tv, Hv, sv = _rows_view(v, D)
+    _, _, so = _rows_view(out, D)
+    if Tk != T or Tv != T or Hv != Hkv or out.shape != q.shape:
+        raise ValueError("attn_prompt: q and out are [T, Hq, D], k and v [T, Hkv, D]")
+    if starts.dtype != torch.int32 or starts.numel() < 1 or not starts.is_contiguous():
+        raise ValueError("attn_prompt: starts is int32[n_seqs + 1]")
+    for t in (q, k, v, out, starts):
+        if not _on_device(t):
+            raise ValueError("tensors must be on the CUDA device or in pinned host memory")
+    _check("gbe_attn_prompt", lib().gbe_attn_prompt(
+        q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, out.data_ptr(), so, starts.data_ptr(),
+        starts.numel() - 1, T, Hq, Hkv, D, scale, _dt(q, k, v, out), _stream(stream)))
+
+
 # ---- conveniences that allocate the outputs -------------------------------------------
+
+def kv_cache(n_pages: int, Hkv: int, page_size: int, D: int, dtype=torch.bfloat16, device="cuda") -> KvCache:
+    """A zeroed cache; dtype torch.float8_e4m3fn for the 8-bit one."""
+    k, v = (torch.zeros((n_pages, Hkv, page_size, D), dtype=dtype, device=device) for _ in range(2))
+    if dtype != torch.float8_e4m3fn:
+        return KvCache(k, v)
+    ks, vs = (torch.zeros((n_pages, Hkv, page_size), dtype=torch.uint8, device=device) for _ in range(2))
+    return KvCache(k, v, ks, vs)
+
+
+def kv_read(cache: KvCache, slots, dtype=None, stream=None):
+    """(k, v), each [T, Hkv, D], of the slots; dtype: the cache's own unless it is 8-bit (then bfloat16)."""
+    if dtype is None:
+        dtype = torch.bfloat16 if cache.k.dtype == torch.float8_e4m3fn else cache.k.dtype
+    k, v = (torch.empty((slots.numel(), cache.shape[1], cache.shape[3]), dtype=dtype, device=slots.device)
+            for _ in range(2))
+    gbe_kv_read(k, v, slots, cache, None, stream)
+    return k, v
+
+
+def attn_decode(q, cache: KvCache, table, lens, scale: float | None = None, workspace=None, stream=None):
+    """[B, Hq, D]; allocates the workspace unless one is given."""
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if workspace is None:
+        n = attn_decode_workspace(q.shape[0], q.shape[1], cache, table.shape[1])
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+            if stream is not None and workspace.is_cuda:  # it is released on return, while `stream` may still use it
+                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                        else torch.cuda.ExternalStream(_stream(stream)))
+    gbe_attn_decode(q, out, cache, table, lens, 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale, workspace,
+                    stream)
+    return out
+
+
+def attn_prompt(q, k, v, starts, scale: float | None = None, stream=None):
+    """[T, Hq, D]; rows outside [starts[0], starts[-1]) are not written."""
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    gbe_attn_prompt(q, k, v, out, starts, 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale, stream)
+    return out
+
 
 def rmsnorm(x, w, eps: float = 1e-5, out=None, stream=None):
     y = torch.empty_like(x) if out is None else out

@@ -256,6 +256,8 @@ const char* gbe_status_string(int status) {
         case GBE_ERR_POINTER: return "a pointer is not memory of the current device, or its extent exceeds its allocation";
         case GBE_ERR_CUDA: return "the CUDA runtime reported an error at launch";
         case GBE_ERR_SAMPLING: return "a sampling method or parameter is out of range";
+        case GBE_ERR_SCALE: return "the softmax scale is not finite";
+        case GBE_ERR_WORKSPACE: return "the workspace is smaller than the call needs";
         default: return "unknown status";
     }
 }
@@ -660,6 +662,184 @@ int gbe_pcg64_uniforms(float* u, int64_t n, uint64_t seed, uint64_t offset, gbe_
     if (st != GBE_OK) return st;
     return finish(gbe::launch_pcg64_uniforms(u, n, (unsigned long long)seed, (unsigned long long)offset,
                                              as_stream(stream)));
+}
+
+// ---- the paged cache and attention ------------------------------------------------
+
+// A cache's description checked without the driver; bufs: 0, 1 = k, v and
+// 2, 3 = their scales (empty unless e4m3).
+static int cache_form(const gbe_kv_cache* c, int dtype, gbe::KvCacheArgs* out, Rows (&pages)[2], Buf (&bufs)[4]) {
+    if (c == nullptr) return GBE_ERR_NULL;
+    const bool e4m3 = c->dtype == GBE_KV_E4M3;
+    if (!e4m3 && c->dtype != dtype) return GBE_ERR_DTYPE;  // GBE_KV_F32 and GBE_KV_BF16 are the storage types' values
+    const int es = e4m3 ? 1 : elem_size(dtype);
+    if (c->D < 8 || c->D > 256 || c->D % 8) return GBE_ERR_SHAPE;
+    if (c->n_pages < 0 || c->Hkv < 1 || c->Hkv > 4096 || c->page_size < 1 || c->page_size > (1 << 20))
+        return GBE_ERR_SHAPE;
+    if (c->n_pages > INT32_MAX / c->page_size) return GBE_ERR_SHAPE;  // slots are int32
+    const int64_t page = c->Hkv * c->page_size * c->D;
+    if (c->page_stride < page || c->page_stride > INT64_MAX / es / (c->n_pages > 0 ? c->n_pages : 1))
+        return GBE_ERR_SHAPE;
+    if (c->page_stride % 8) return GBE_ERR_ALIGN;
+    const uint64_t scales = e4m3 ? (uint64_t)(c->n_pages * c->Hkv * c->page_size) : 0u;
+    void* kv[2] = {c->k, c->v};
+    for (int i = 0; i < 2; ++i) {
+        pages[i] = {kv[i], c->n_pages, c->page_stride * es, page * es};
+        bufs[i] = pages[i].extent();
+        bufs[i].align = 16;
+    }
+    bufs[2] = {c->k_scale, scales, 1};
+    bufs[3] = {c->v_scale, scales, 1};
+    *out = {c->k, c->v, c->k_scale, c->v_scale, c->n_pages, c->page_stride, (int)c->page_size, (int)c->Hkv, (int)c->D,
+            c->dtype};
+    return GBE_OK;
+}
+
+// Row operands [T, H, D] with a token stride.
+static int rows_form(int64_t T, int64_t H, int64_t D, int64_t stride, int es) {
+    if (stride < H * D || stride > INT64_MAX / (T > 0 ? T : 1) / es) return GBE_ERR_SHAPE;
+    return GBE_OK;
+}
+
+static int kv_rows(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int32_t* slots, int64_t T,
+                   const gbe_kv_cache* cache, int32_t* bad, int dtype, gbe_stream stream, bool write) {
+    const int es = elem_size(dtype);
+    if (!es) return GBE_ERR_DTYPE;
+    gbe::KvCacheArgs c;
+    Rows pages[2];
+    Buf cb[4];
+    int st = cache_form(cache, dtype, &c, pages, cb);
+    if (st != GBE_OK) return st;
+    if (T < 0 || T > (1LL << 30) / c.Hkv) return GBE_ERR_SHAPE;
+    if ((st = rows_form(T, c.Hkv, c.D, k_stride, es)) || (st = rows_form(T, c.Hkv, c.D, v_stride, es))) return st;
+    if (T == 0) return GBE_OK;
+    const int64_t width = (int64_t)c.Hkv * c.D * es;
+    const Rows rows[2] = {{k, T, k_stride * es, width}, {v, T, v_stride * es, width}};
+    // 0, 1 = the rows; 2 .. 5 = the cache; 6 = slots; 7 = the counter
+    Buf bufs[8] = {rows[0].extent(), rows[1].extent(), cb[0], cb[1], cb[2], cb[3], {slots, (uint64_t)T * 4, 4},
+                   {bad, bad ? 4u : 0u, 4}};
+    bufs[0].align = bufs[1].align = (uint64_t)es;
+    for (const Buf& b : bufs)
+        if ((st = check_form(b)) != GBE_OK) return st;
+    // what is written shares no byte with anything else; k and v may
+    // interleave row by row (columns of one buffer, halves of one page)
+    if (write ? rows_overlap(pages[0], pages[1]) : rows_overlap(rows[0], rows[1])) return GBE_ERR_ALIAS;
+    for (int i = 0; i < 8; ++i)
+        for (int j = 0; j < i; ++j) {
+            const bool out_i = i == 7 || (write ? i >= 2 && i < 6 : i < 2), out_j = write ? j >= 2 && j < 6 : j < 2;
+            if (!(out_i || out_j) || (i == 1 && j == 0) || (i == 3 && j == 2)) continue;
+            if (overlaps(bufs[i], bufs[j])) return GBE_ERR_ALIAS;
+        }
+    Checker chk;
+    if ((st = chk.begin()) != GBE_OK) return st;
+    for (const Buf& b : bufs)
+        if ((st = chk.check(b)) != GBE_OK) return st;
+    const bool vec = aligned16(k) && aligned16(v) && (k_stride * es) % 16 == 0 && (v_stride * es) % 16 == 0;
+    return finish(write ? gbe::launch_kv_write(k, k_stride, v, v_stride, slots, T, c, bad, dtype, vec,
+                                               as_stream(stream))
+                        : gbe::launch_kv_read(const_cast<void*>(k), k_stride, const_cast<void*>(v), v_stride, slots, T,
+                                              c, bad, dtype, vec, as_stream(stream)));
+}
+
+int gbe_kv_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int32_t* slots, int64_t T,
+                 const gbe_kv_cache* cache, int32_t* bad_slot_count, int dtype, gbe_stream stream) {
+    return kv_rows(k, k_stride, v, v_stride, slots, T, cache, bad_slot_count, dtype, stream, true);
+}
+
+int gbe_kv_read(void* k, int64_t k_stride, void* v, int64_t v_stride, const int32_t* slots, int64_t T,
+                const gbe_kv_cache* cache, int32_t* bad_slot_count, int dtype, gbe_stream stream) {
+    return kv_rows(k, k_stride, v, v_stride, slots, T, cache, bad_slot_count, dtype, stream, false);
+}
+
+// The sizes of a decode call that decide its workspace.
+static bool decode_sizes_ok(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size, int64_t max_pages) {
+    if (B < 0 || B > (1 << 20) || Hkv < 1 || Hkv > 4096 || Hq < Hkv || Hq > 65536 || Hq % Hkv) return false;
+    if (D < 8 || D > 256 || D % 8 || page_size < 1 || page_size > (1 << 20) || max_pages < 0) return false;
+    if (max_pages > (1 << 30) / page_size) return false;
+    return B * gbe::decode_split(Hkv, page_size, max_pages).split <= INT32_MAX / Hq;
+}
+
+static uint64_t decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size, int64_t max_pages) {
+    const int64_t split = gbe::decode_split(Hkv, page_size, max_pages).split;
+    return split == 1 ? 0u : (uint64_t)B * Hq * split * (D + 2) * 4;
+}
+
+int64_t gbe_attn_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,
+                                  int64_t max_pages) {
+    if (!decode_sizes_ok(B, Hq, Hkv, D, page_size, max_pages)) return -1;
+    return (int64_t)decode_workspace(B, Hq, Hkv, D, page_size, max_pages);
+}
+
+int gbe_attn_decode(const void* q, int64_t q_stride, void* out, int64_t out_stride, int64_t B, int64_t Hq,
+                    const gbe_kv_cache* cache, const int32_t* table, int64_t max_pages, const int32_t* lens,
+                    float scale, void* workspace, int64_t workspace_bytes, int dtype, gbe_stream stream) {
+    const int es = elem_size(dtype);
+    if (!es) return GBE_ERR_DTYPE;
+    gbe::KvCacheArgs c;
+    Rows pages[2];
+    Buf cb[4];
+    int st = cache_form(cache, dtype, &c, pages, cb);
+    if (st != GBE_OK) return st;
+    if (!decode_sizes_ok(B, Hq, c.Hkv, c.D, c.page_size, max_pages)) return GBE_ERR_SHAPE;
+    if ((st = rows_form(B, Hq, c.D, q_stride, es)) || (st = rows_form(B, Hq, c.D, out_stride, es))) return st;
+    if (!std::isfinite(scale)) return GBE_ERR_SCALE;
+    if (B == 0) return GBE_OK;
+    const uint64_t need = decode_workspace(B, Hq, c.Hkv, c.D, c.page_size, max_pages);
+    if (workspace_bytes < 0 || (uint64_t)workspace_bytes < need) return GBE_ERR_WORKSPACE;
+    const Rows qr = {q, B, q_stride * es, Hq * c.D * es}, orow = {out, B, out_stride * es, Hq * c.D * es};
+    Buf bufs[9] = {orow.extent(), {workspace, need, 16}, qr.extent(), cb[0], cb[1], cb[2], cb[3],
+                   {table, (uint64_t)(B * max_pages) * 4, 4}, {lens, (uint64_t)B * 4, 4}};
+    bufs[0].align = bufs[2].align = (uint64_t)es;
+    for (const Buf& b : bufs)
+        if ((st = check_form(b)) != GBE_OK) return st;
+    for (int o = 0; o < 2; ++o)
+        for (int j = o + 1; j < 9; ++j) {
+            if (o == 0 && j == 2 ? rows_overlap(orow, qr) : overlaps(bufs[o], bufs[j])) return GBE_ERR_ALIAS;
+        }
+    Checker chk;
+    if ((st = chk.begin()) != GBE_OK) return st;
+    for (const Buf& b : bufs)
+        if ((st = chk.check(b)) != GBE_OK) return st;
+    const gbe::DecodeArgs a = {q, out, q_stride, out_stride, c, table, lens, B, Hq, max_pages, scale, workspace};
+    return finish(gbe::launch_attn_decode(a, dtype, as_stream(stream)));
+}
+
+int gbe_attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                    void* out, int64_t out_stride, const int32_t* starts, int64_t n_seqs, int64_t T, int64_t Hq,
+                    int64_t Hkv, int64_t D, float scale, int dtype, gbe_stream stream) {
+    const int es = elem_size(dtype);
+    if (!es) return GBE_ERR_DTYPE;
+    if (n_seqs < 0 || n_seqs > (1 << 24) || T < 0 || T > (1 << 28) || Hkv < 1 || Hq < Hkv || Hq > 65536 || Hq % Hkv)
+        return GBE_ERR_SHAPE;
+    if (D < 8 || D > 256 || D % 8) return GBE_ERR_SHAPE;
+    if (T / 64 + n_seqs > INT32_MAX / Hq) return GBE_ERR_SHAPE;
+    if (rows_form(T, Hq, D, q_stride, es) || rows_form(T, Hkv, D, k_stride, es) ||
+        rows_form(T, Hkv, D, v_stride, es) || rows_form(T, Hq, D, out_stride, es))
+        return GBE_ERR_SHAPE;
+    if (!std::isfinite(scale)) return GBE_ERR_SCALE;
+    if (T == 0 || n_seqs == 0) return GBE_OK;
+    const Rows r[4] = {{out, T, out_stride * es, Hq * D * es},
+                       {q, T, q_stride * es, Hq * D * es},
+                       {k, T, k_stride * es, Hkv * D * es},
+                       {v, T, v_stride * es, Hkv * D * es}};
+    Buf bufs[5] = {r[0].extent(), r[1].extent(), r[2].extent(), r[3].extent(), {starts, (uint64_t)(n_seqs + 1) * 4, 4}};
+    int st;
+    for (int i = 0; i < 5; ++i) {
+        if (i < 4) bufs[i].align = (uint64_t)es;
+        if ((st = check_form(bufs[i])) != GBE_OK) return st;
+    }
+    for (int i = 1; i < 4; ++i)
+        if (rows_overlap(r[0], r[i])) return GBE_ERR_ALIAS;
+    if (overlaps(bufs[0], bufs[4])) return GBE_ERR_ALIAS;
+    Checker chk;
+    if ((st = chk.begin()) != GBE_OK) return st;
+    for (const Buf& b : bufs)
+        if ((st = chk.check(b)) != GBE_OK) return st;
+    bool vec = true;
+    for (const Rows& x : r) vec = vec && aligned16(x.p) && x.stride % 16 == 0;
+    const gbe::PromptArgs a = {q, k, v, out, q_stride, k_stride, v_stride, out_stride, starts, n_seqs, T, Hq, Hkv, D,
+                               scale};
+    return finish(gbe::launch_attn_prompt(a, dtype, vec, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,298 @@
+// attn_decode.cu -- attention of one new token per sequence over the paged
+// key-value cache, split over the cache's length and joined.
+//
+//   out[b, h] = sum_j p_j v_j,  p = softmax_j(scale * q[b, h] . k_j),  j < lens[b]
+//
+// with k_j, v_j the cached rows of kv head h / (Hq / Hkv).  One CTA takes one
+// chunk of one sequence's tokens for one kv head and up to H of its query
+// heads; the chunk's length is a function of the sequence's length alone
+// (chunk_tokens below), so a sequence's result has the same bits in a batch
+// of any size.  Each CTA leaves the unnormalised sum, the running maximum and
+// the running sum of its chunk in the workspace, and attn_join adds the
+// chunks of a row in order.  A sequence of one chunk is written at once.
+#include "common.cuh"
+#include "gbe_elementwise.h"
+#include "kv_cache.cuh"
+#include "launch.h"
+
+namespace gbe {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A partial softmax's weight when its maximum m moves to m2: 0 while nothing
+// has been seen (m = -inf).
+__device__ __forceinline__ float rescale(float m, float m2) { return m == -INFINITY ? 0.0f : ex2(m - m2); }
+
+// Tokens of a chunk for a sequence of n tokens: n / split of them in units
+// of 64, at least `least`.
+__device__ __forceinline__ int chunk_tokens(int n, int split, int least) {
+    const int c = ((n + split - 1) / split + 63) & ~63;
+    return c < least ? least : c;
+}
+
+struct Args {
+    const void* q;
+    void* out;
+    int64_t q_stride, out_stride;
+    KvCacheArgs c;
+    const int32_t* table;
+    const int32_t* lens;
+    int Hq, group, max_pages;
+    int split, least;     // chunks at most, tokens a chunk at least
+    int parts;            // query-head parts of a kv head: ceil(group / H)
+    float scale;          // times log2(e)
+    float* part_o;        // [B * Hq, split, D]
+    float2* part_ml;      // [B * Hq, split]: running maximum (base 2), running sum
+};
+
+// One 8-value piece of a cached row, widened to f32.
+template <int KV>
+struct Piece;
+template <>
+struct Piece<GBE_KV_F32> {
+    Vec16 a, b;
+    __device__ __forceinline__ void load(const void* base, int64_t i) {
+        const float* p = static_cast<const float*>(base) + i;
+        a = ld_stream(p), b = ld_stream(p + 4);
+    }
+    __device__ __forceinline__ void widen(float (&f)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(a.w[e]), f[4 + e] = __uint_as_float(b.w[e]);
+    }
+};
+template <>
+struct Piece<GBE_KV_BF16> {
+    Vec16 a;
+    __device__ __forceinline__ void load(const void* base, int64_t i) {
+        a = ld_stream(static_cast<const uint16_t*>(base) + i);
+    }
+    __device__ __forceinline__ void widen(float (&f)[8]) const { Store<kBF16>::unpack(a, f); }
+};
+template <>
+struct Piece<GBE_KV_E4M3> {
+    uint2 a;
+    __device__ __forceinline__ void load(const void* base, int64_t i) {
+        a = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + i);
+    }
+    __device__ __forceinline__ void widen(float (&f)[8]) const {
+        e4m3x4_to_f32(a.x, f);
+        e4m3x4_to_f32(a.y, f + 4);
+    }
+};
+
+// The CUDA-core form: G lanes (the power of two at or above D / 8) hold one
+// token's row, eight values each, so a warp walks 32 / G tokens at a time
+// and each lane keeps the query heads' pieces and the output's in registers.
+template <int DT, int KV, int H>
+__global__ void __launch_bounds__(kThreads) decode_rows(Args a, int lanes_log2) {
+    extern __shared__ float sm[];  // [kThreads / G][H][D + 2]
+    pdl_begin();
+    const KvCacheArgs& c = a.c;
+    const int G = 1 << lanes_log2, D = c.D;
+    uint32_t id = blockIdx.x;
+    const int part = id % a.parts;
+    id /= a.parts;
+    const int kvh = id % c.Hkv;
+    id /= c.Hkv;
+    const int chunk = id % a.split, b = id / a.split;
+
+    const int64_t capacity = (int64_t)a.max_pages * c.page_size;
+    const int32_t len = a.lens[b];
+    const int n = len < 0 ? 0 : (int)(len < capacity ? len : capacity);
+    const int C = chunk_tokens(n, a.split, a.least);
+    const int t0 = chunk * C, t1 = min(n, t0 + C);
+    if (t0 >= t1 && chunk > 0) return;
+    const int h0 = kvh * a.group + part * H;              // first query head
+    const int heads = min(H, a.group - part * H);
+
+    const int sub = threadIdx.x & (G - 1), d0 = sub * 8;
+    const bool mine = d0 < D;
+    const int stream = threadIdx.x >> lanes_log2, streams = kThreads >> lanes_log2;
+
+    float q[H][8], acc[H][8], m[H], l[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        m[h] = -INFINITY;
+        l[h] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            acc[h][e] = 0.0f;
+            q[h][e] = 0.0f;
+            if (mine && h < heads)
+                q[h][e] = Store<DT>::load1(a.q, b * a.q_stride + (int64_t)(h0 + h) * D + d0 + e) * a.scale;
+        }
+    }
+    const int32_t* pages = a.table + (int64_t)b * a.max_pages;
+    // all streams of a warp take the same number of steps, so that its
+    // shuffles meet
+    for (int base = t0; base < t1; base += streams) {
+        const int t = base + stream;
+        const bool live = t < t1;
+        const int page_i = live ? t / c.page_size : 0;
+        const int32_t page = live ? pages[page_i] : -1;
+        const bool good = page >= 0 && page < c.n_pages;
+        Piece<KV> kp = {}, vp = {};
+        float ks = 1.0f, vs = 1.0f;
+        if (good) {
+            const int row = t - page_i * c.page_size;
+            const int64_t i = page * c.page_stride + ((int64_t)kvh * c.page_size + row) * D + d0;
+            if (mine) kp.load(c.k, i), vp.load(c.v, i);
+            if (KV == GBE_KV_E4M3) {
+                const int64_t si = ((int64_t)page * c.Hkv + kvh) * c.page_size + row;
+                ks = __uint_as_float((uint32_t)c.k_scale[si] << 23);
+                vs = __uint_as_float((uint32_t)c.v_scale[si] << 23);
+            }
+        }
+        float k[8], v[8];
+        kp.widen(k);
+        vp.widen(v);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(q[h][e], k[e], s);
+            for (int x = G >> 1; x >= 1; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
+            if (KV == GBE_KV_E4M3) s *= ks;
+            if (good) {
+                // a NaN logit leaves a finite maximum, so that its NaN weight reaches the result
+                const float m2 = fmaxf(m[h], s == s ? s : -3.0e38f);
+                const float r = rescale(m[h], m2);
+                const float p = s == -INFINITY ? 0.0f : ex2(s - m2);
+                l[h] = fmaf(l[h], r, p);
+                const float pv = KV == GBE_KV_E4M3 ? p * vs : p;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[h][e] = fmaf(pv, v[e], acc[h][e] * r);
+                m[h] = m2;
+            }
+        }
+    }
+    // join the streams in order, in shared memory
+    const int W = D + 2;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        float* o = sm + (stream * H + h) * W;
+        if (mine)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[d0 + e] = acc[h][e];
+        if (sub == 0) o[D] = m[h], o[D + 1] = l[h];
+    }
+    __syncthreads();
+    const bool whole = C >= n;
+    for (int i = threadIdx.x; i < heads * D; i += kThreads) {
+        const int h = i / D, d = i - h * D;
+        float mx = -INFINITY;
+        for (int s = 0; s < streams; ++s) mx = fmaxf(mx, sm[(s * H + h) * W + D]);
+        float sum = 0.0f, o = 0.0f;
+        for (int s = 0; s < streams; ++s) {
+            const float* x = sm + (s * H + h) * W;
+            const float r = rescale(x[D], mx);
+            if (r != 0.0f) sum = fmaf(x[D + 1], r, sum), o = fmaf(x[d], r, o);
+        }
+        if (whole) {
+            Store<DT>::store1(a.out, b * a.out_stride + (int64_t)(h0 + h) * D + d,
+                              mx == -INFINITY ? 0.0f : o / sum);
+        } else {
+            const int64_t row = ((int64_t)b * a.Hq + h0 + h) * a.split + chunk;
+            a.part_o[row * D + d] = o;
+            if (d == 0) a.part_ml[row] = make_float2(mx, sum);
+        }
+    }
+}
+
+// The chunks of one row added in order: one warp a (sequence, query head).
+template <int DT>
+__global__ void __launch_bounds__(kThreads) attn_join(Args a, int64_t rows) {
+    pdl_begin();
+    const int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    const int lane = threadIdx.x & 31, D = a.c.D;
+    const int64_t b = r / a.Hq, h = r - b * a.Hq;
+    const int64_t capacity = (int64_t)a.max_pages * a.c.page_size;
+    const int32_t len = a.lens[b];
+    const int n = len < 0 ? 0 : (int)(len < capacity ? len : capacity);
+    const int C = chunk_tokens(n, a.split, a.least);
+    if (C >= n) return;  // one chunk: already written
+    const int chunks = (n + C - 1) / C;
+    const float2* ml = a.part_ml + r * a.split;
+    float mx = -INFINITY;
+    for (int s = lane; s < chunks; s += 32) mx = fmaxf(mx, ml[s].x);
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+    float sum = 0.0f, o[8] = {};
+    for (int s = 0; s < chunks; ++s) {
+        const float2 v = ml[s];
+        const float w = rescale(v.x, mx);
+        if (w == 0.0f) continue;
+        sum = fmaf(v.y, w, sum);
+        const float* p = a.part_o + (r * a.split + s) * D;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (lane + 32 * e < D) o[e] = fmaf(p[lane + 32 * e], w, o[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (lane + 32 * e < D)
+            Store<DT>::store1(a.out, b * a.out_stride + h * D + lane + 32 * e, mx == -INFINITY ? 0.0f : o[e] / sum);
+}
+
+template <int DT, int KV, int H>
+cudaError_t go(Args a, int64_t B, cudaStream_t st) {
+    int lg = 0;
+    while ((8 << lg) < a.c.D) ++lg;
+    a.parts = (a.group + H - 1) / H;
+    const size_t smem = (size_t)(kThreads >> lg) * H * (a.c.D + 2) * 4;
+    const dim3 grid((unsigned)(B * a.split * a.c.Hkv * a.parts));
+    return launch(decode_rows<DT, KV, H>, grid, dim3(kThreads), smem, st, a, lg);
+}
+
+template <int DT, int KV>
+cudaError_t pick(const Args& a, int64_t B, cudaStream_t st) {
+    if (a.group == 1) return go<DT, KV, 1>(a, B, st);
+    if (a.group == 2) return go<DT, KV, 2>(a, B, st);
+    return go<DT, KV, 4>(a, B, st);
+}
+
+}  // namespace
+
+DecodeSplit decode_split(int64_t Hkv, int64_t page_size, int64_t max_pages) {
+    DecodeSplit s;
+    s.least = 128;
+    int64_t want = (304 + Hkv - 1) / Hkv;
+    want = want < 16 ? 16 : want > 128 ? 128 : want;
+    const int64_t most = (page_size * max_pages + s.least - 1) / s.least;
+    s.split = (int)(want < most ? want : most < 1 ? 1 : most);
+    return s;
+}
+
+cudaError_t launch_attn_decode(const DecodeArgs& d, int dtype, cudaStream_t st) {
+    Args a = {};
+    const DecodeSplit s = decode_split(d.c.Hkv, d.c.page_size, d.max_pages);
+    a.q = d.q, a.out = d.out, a.q_stride = d.q_stride, a.out_stride = d.out_stride;
+    a.c = d.c, a.table = d.table, a.lens = d.lens;
+    a.Hq = (int)d.Hq, a.group = (int)(d.Hq / d.c.Hkv), a.max_pages = (int)d.max_pages;
+    a.split = s.split, a.least = s.least;
+    a.scale = d.scale * kLog2e;
+    a.part_ml = static_cast<float2*>(d.workspace);
+    a.part_o = reinterpret_cast<float*>(a.part_ml + d.B * d.Hq * s.split);
+    cudaError_t e;
+    if (dtype == GBE_F32)
+        e = d.c.dtype == GBE_KV_E4M3 ? pick<kF32, GBE_KV_E4M3>(a, d.B, st) : pick<kF32, GBE_KV_F32>(a, d.B, st);
+    else
+        e = d.c.dtype == GBE_KV_E4M3 ? pick<kBF16, GBE_KV_E4M3>(a, d.B, st) : pick<kBF16, GBE_KV_BF16>(a, d.B, st);
+    if (e != cudaSuccess || s.split == 1) return e;
+    const int64_t rows = d.B * d.Hq;
+    const dim3 grid(ceil_div_i(rows, kWarps));
+    return dtype == GBE_F32 ? launch(attn_join<kF32>, grid, dim3(kThreads), 0, st, a, rows)
+                            : launch(attn_join<kBF16>, grid, dim3(kThreads), 0, st, a, rows);
+}
+
+}  // namespace gbe

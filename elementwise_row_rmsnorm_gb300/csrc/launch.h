@@ -101,4 +101,54 @@ cudaError_t launch_sample(const void* x, int32_t* out, int64_t rows, int64_t n, 
 cudaError_t launch_pcg64_uniforms(float* u, int64_t n, unsigned long long seed, unsigned long long offset,
                                   cudaStream_t st);
 
+// A paged key-value cache as the kernels see it (gbe_kv_cache, checked).
+struct KvCacheArgs {
+    void* k;
+    void* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    int64_t n_pages, page_stride;
+    int page_size, Hkv, D, dtype;
+};
+
+cudaError_t launch_kv_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int32_t* slots,
+                            int64_t T, const KvCacheArgs& c, int32_t* bad, int dtype, bool vec, cudaStream_t st);
+
+cudaError_t launch_kv_read(void* k, int64_t k_stride, void* v, int64_t v_stride, const int32_t* slots, int64_t T,
+                           const KvCacheArgs& c, int32_t* bad, int dtype, bool vec, cudaStream_t st);
+
+// How a sequence's tokens are cut into chunks that are attended to apart:
+// at most `split` chunks of at least `least` tokens.
+struct DecodeSplit {
+    int split, least;
+};
+DecodeSplit decode_split(int64_t Hkv, int64_t page_size, int64_t max_pages);
+
+struct DecodeArgs {
+    const void* q;
+    void* out;
+    int64_t q_stride, out_stride;
+    KvCacheArgs c;
+    const int32_t* table;
+    const int32_t* lens;
+    int64_t B, Hq, max_pages;
+    float scale;
+    void* workspace;
+};
+
+cudaError_t launch_attn_decode(const DecodeArgs& a, int dtype, cudaStream_t st);
+
+struct PromptArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    int64_t q_stride, k_stride, v_stride, out_stride;
+    const int32_t* starts;
+    int64_t n_seqs, T, Hq, Hkv, D;
+    float scale;
+};
+
+cudaError_t launch_attn_prompt(const PromptArgs& a, int dtype, bool vec, cudaStream_t st);
+
 }  // namespace gbe

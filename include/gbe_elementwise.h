@@ -1,7 +1,9 @@
 /*
  * gbe_elementwise.h -- C ABI of the GB300 (sm_103a) elementwise and
  * row-wise transformer ops: RMSNorm, fused residual add + RMSNorm, RoPE,
- * SiLU-mul, embedding gather, residual add and greedy argmax.
+ * SiLU-mul, embedding gather, residual add, greedy argmax and sampling, and
+ * the attention between them: the paged key-value cache and causal attention
+ * over prompts and over that cache.
  *
  * Sources of the definitions (cited per entry point below):
  *   "Operations" -- the op math spec of the glia runtime (sections 1 to 10);
@@ -67,7 +69,9 @@ typedef enum gbe_status {
     GBE_ERR_ALIGN = 9,   /* a pointer is not aligned to its element size */
     GBE_ERR_POINTER = 10, /* not device memory of the current device, or the extent exceeds its allocation */
     GBE_ERR_CUDA = 11,   /* the CUDA runtime reported an error at launch */
-    GBE_ERR_SAMPLING = 12 /* a sampling method or parameter is out of range */
+    GBE_ERR_SAMPLING = 12, /* a sampling method or parameter is out of range */
+    GBE_ERR_SCALE = 13,    /* the softmax scale is not finite */
+    GBE_ERR_WORKSPACE = 14 /* the workspace is smaller than the call needs */
 } gbe_status;
 
 /* The stream type; the same type as cudaStream_t, so either may be passed. */
@@ -372,6 +376,134 @@ int gbe_sample_seeded(const void *x, int32_t *out, int64_t rows, int64_t n, int 
  *     n - 1 (the stream continues past 2^64).  n >= 0.
  */
 int gbe_pcg64_uniforms(float *u, int64_t n, uint64_t seed, uint64_t offset, gbe_stream stream);
+
+/* What a paged cache holds. */
+typedef enum gbe_kv_dtype { GBE_KV_F32 = 0, GBE_KV_BF16 = 1, GBE_KV_E4M3 = 2 } gbe_kv_dtype;
+
+/*
+ * A paged key-value cache of one layer, described to the entry points below
+ * by a HOST pointer that is read during the call; the memory is the caller's,
+ * device memory like every other buffer.
+ *   "Operations" (KvCache: k and v of [kv_heads, tokens, head_dim] per
+ *   layer, appended to as tokens arrive), cut into pages so that sequences
+ *   of any length share one pool.
+ * Row r of page p holds one token: slot p * page_size + r.
+ */
+typedef struct gbe_kv_cache {
+    void *k, *v;              /* [n_pages, Hkv, page_size, D], 16-byte aligned; within a page contiguous */
+    uint8_t *k_scale;         /* GBE_KV_E4M3: [n_pages, Hkv, page_size], one byte a row, contiguous; */
+    uint8_t *v_scale;         /*   else not read (NULL) */
+    int64_t n_pages, Hkv, page_size, D;
+    int64_t page_stride;      /* elements from one page of k (and of v) to the next, >= Hkv * page_size * D, a
+                                 multiple of 8; k and v may be the halves of one [n_pages, 2, ...] buffer */
+    int dtype;                /* the call's dtype (GBE_KV_F32, GBE_KV_BF16), or GBE_KV_E4M3 */
+} gbe_kv_cache;
+/*
+ * D is a multiple of 8 from 8 to 256; Hkv at most 4096; page_size at most
+ * 2^20; n_pages * page_size below 2^31.
+ *
+ * GBE_KV_E4M3: value = code * 2^(byte - 127), the code an e4m3 number (4
+ * exponent and 3 mantissa bits, no infinities, largest 448), the byte one of
+ * 1 .. 254; a row whose byte is 0 stands for zeros.
+ */
+
+/*
+ * gbe_kv_write -- store the k and v rows of T tokens into their slots.
+ *   "Operations" (KvCache append).
+ *   f32 and bf16 caches: the rows as they are, bit for bit.  GBE_KV_E4M3:
+ *   each row of D values (a token, a head, k or v) gets the least scale 2^e,
+ *   e >= -126, at which its largest finite magnitude is at most 448, and
+ *   its codes are x * 2^-e rounded to e4m3, nearest, ties to even (one
+ *   rounding: the product is exact).  Infinities and NaN are stored as NaN;
+ *   at e = 120 codes stop at 240, so that no finite value is read as infinite.
+ * k, v  : [T, Hkv, D] with token strides k_stride, v_stride (elements, >=
+ *         Hkv * D): column slices of a fused QKV buffer, as gbe_rope_qk
+ *         leaves them.  dtype.
+ * slots : device int32[T].  -1: the token (padding) is not stored.  Any other
+ *         slot outside [0, n_pages * page_size) is not stored either and,
+ *         when bad_slot_count (NULL, or a device int32 that the caller
+ *         zeroes) is given, counted.  The other slots must differ from one
+ *         another: a slot that occurs twice holds bytes of either row.
+ * Rows of the cache that no slot names are left as they were.
+ * T * Hkv is at most 2^30.  Alias: none (k and v may interleave in one buffer).
+ */
+int gbe_kv_write(const void *k, int64_t k_stride, const void *v, int64_t v_stride, const int32_t *slots, int64_t T,
+                 const gbe_kv_cache *cache, int32_t *bad_slot_count, int dtype, gbe_stream stream);
+
+/*
+ * gbe_kv_read -- gather the k and v rows of T slots, the inverse of
+ * gbe_kv_write: for reuse of a cached prefix by gbe_attn_prompt, for moving a
+ * sequence, for inspection.
+ *   f32 and bf16 caches: bit for bit.  GBE_KV_E4M3: code * 2^(byte - 127),
+ *   exact in f32 and, from 2^-126 on, in bf16.
+ * k, v (outputs), strides, slots, T, bad_slot_count, dtype, cache : as for
+ *   gbe_kv_write; a slot may occur any number of times, and a slot that is
+ *   not in the cache (-1 among them) gives zeros.
+ */
+int gbe_kv_read(void *k, int64_t k_stride, void *v, int64_t v_stride, const int32_t *slots, int64_t T,
+                const gbe_kv_cache *cache, int32_t *bad_slot_count, int dtype, gbe_stream stream);
+
+/*
+ * gbe_attn_decode -- attention of one new token of each of B sequences over
+ * the paged cache.
+ *   "Operations" (Sdpa with grouped heads), for one query token:
+ *   out[b, h] = sum_j p_j v_j,  p = softmax over j < lens[b] of
+ *   scale * (q[b, h] . k_j), k_j and v_j the rows of kv head h / (Hq / Hkv)
+ *   at token j of sequence b: row j % page_size of page
+ *   table[b, j / page_size].  The new token's own k and v are in the cache
+ *   already (gbe_kv_write ahead of the call) and counted in lens.
+ * q     : [B, Hq, D], sequences q_stride elements apart (>= Hq * D); dtype.
+ * out   : likewise with out_stride; overlaps nothing.
+ * table : device int32[B, max_pages].  A token on a page outside [0, n_pages)
+ *         takes no part.  Entries past a sequence's last page are not read.
+ * lens  : device int32[B].  0 or less: the row is zeros.  A length above
+ *         max_pages * page_size counts as that.
+ * scale : finite, usually 1 / sqrt(D).
+ * workspace : device memory of gbe_attn_decode_workspace bytes at least, 16-byte
+ *         aligned, of any content, used until the call's work on `stream` is
+ *         done: calls in flight on other streams need their own.  May be NULL
+ *         when 0 bytes are needed.
+ * Sums, maxima and the softmax are f32; results are rounded once at the end.
+ * What lies in the cache behind a sequence's last token is not looked at
+ * (infinities and NaN there stay there).  A NaN in an attended place gives
+ * NaN; a row with nothing to attend to is zeros.
+ * A row's bits depend on its own q, cache rows and length, and on Hq, Hkv, D,
+ * page_size, max_pages: the same in a batch of any size.
+ * Hq is a multiple of Hkv, at most 65536; max_pages * page_size at most 2^30;
+ * B at most 2^20.
+ */
+int gbe_attn_decode(const void *q, int64_t q_stride, void *out, int64_t out_stride, int64_t B, int64_t Hq,
+                    const gbe_kv_cache *cache, const int32_t *table, int64_t max_pages, const int32_t *lens,
+                    float scale, void *workspace, int64_t workspace_bytes, int dtype, gbe_stream stream);
+
+/* The bytes of workspace that gbe_attn_decode needs (0 for short tables);
+ * -1 when it would refuse the sizes. */
+int64_t gbe_attn_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,
+                                  int64_t max_pages);
+
+/*
+ * gbe_attn_prompt -- causal attention over whole prompts, packed one behind
+ * the other.
+ *   "Operations" (Sdpa, causal mask, grouped heads): for row i of a
+ *   sequence, out[i, h] = sum_j p_j v_j, p = softmax over the sequence's
+ *   rows j <= i of scale * (q[i, h] . k_j), k and v of kv head
+ *   h / (Hq / Hkv).  Masked places take no part at all (an infinity or a
+ *   NaN in a later row, or in another sequence, stays there).
+ * q, out : [T, Hq, D], k, v : [T, Hkv, D], each with its token stride in
+ *          elements (column slices of a fused QKV buffer).  dtype for all.
+ * starts : device int32[n_seqs + 1], not decreasing: sequence s holds rows
+ *          starts[s] .. starts[s + 1] - 1 (none is allowed).  Rows before
+ *          starts[0] and from starts[n_seqs] on are left as they were.
+ *          Entries are brought into [0, T] before use.
+ * scale  : finite, usually 1 / sqrt(D).  D : a multiple of 8, 8 to 256.
+ * Sums, maxima and the softmax are f32; results are rounded once at the end.
+ * Alias : out overlaps nothing; q, k and v may interleave in one buffer.
+ * A row's bits depend on its sequence alone, not on its place in the packing.
+ * Hq is a multiple of Hkv, at most 65536; T at most 2^28, n_seqs at most 2^24.
+ */
+int gbe_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                    void *out, int64_t out_stride, const int32_t *starts, int64_t n_seqs, int64_t T, int64_t Hq,
+                    int64_t Hkv, int64_t D, float scale, int dtype, gbe_stream stream);
 
 #ifdef __cplusplus
 }

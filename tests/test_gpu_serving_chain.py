@@ -1,0 +1,79 @@
+"""The serving operators as a layer runs them: rotate q and k in the fused
+projection's buffer, store k and v, attend over the prompt, then one token at
+a time over the cache -- each against the definition on what the cache holds,
+and the two attentions against each other."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import attn_ref
+import elementwise_row_rmsnorm_gb300 as gbe
+from synth import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+Hq, H, D, P = 8, 2, 128, 16
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _rotated(fused, pos, om):
+    q, k, v = fused[:, :Hq], fused[:, Hq:Hq + H], fused[:, Hq + H:]
+    gbe.gbe_rope_qk(q, q, k, k, pos, om, D, 1.0, 0)
+    return q, k, v
+
+
+@pytest.mark.parametrize("dtype,kind", [(F32, F32), (F32, F8), (BF, BF), (BF, F8)])
+def test_prompt_then_decode(dtype, kind):
+    lens, steps = [70, 1, 200], 4
+    scale = 1.0 / math.sqrt(D)
+    om = torch.from_numpy(W.inv_freq(500000.0, D, D // 2)).cuda()
+    cache = gbe.kv_cache(40, H, P, D, kind)
+    room = [-(-(n + steps) // P) for n in lens]
+    table = torch.full((3, max(room)), -1, dtype=torch.int32)
+    order = torch.randperm(40, generator=torch.Generator().manual_seed(4)).tolist()
+    for b, m in enumerate(room):
+        table[b, :m] = torch.tensor([order.pop() for _ in range(m)], dtype=torch.int32)
+
+    def slot(b, t): return int(table[b, t // P]) * P + t % P
+
+    g = torch.Generator(device="cuda").manual_seed(5)
+    starts = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    fused = torch.randn(starts[-1], Hq + 2 * H, D, generator=g, device="cuda").to(dtype)
+    pos = _i32([t for n in lens for t in range(n)])
+    q, k, v = _rotated(fused, pos, om)
+    slots = _i32([slot(b, t) for b, n in enumerate(lens) for t in range(n)])
+    gbe.gbe_kv_write(k, v, slots, cache)
+    ctx = gbe.attn_prompt(q, k, v, _i32(starts))
+    want, tol, _ = attn_ref.prompt(q, k, v, starts, scale, dtype == BF)
+    attn_ref.assert_within(ctx, want, tol, "prompt")
+
+    # the prompt's last row again, over the cache: the same but for what the cache's 8 bits cost
+    last = q[[z - 1 for z in starts[1:]]]
+    dec = gbe.attn_decode(last, cache, table.cuda(), _i32(lens))
+    want_d, tol_d = attn_ref.decode(last, cache, table.cuda(), lens, scale, dtype == BF)
+    attn_ref.assert_within(dec, want_d, tol_d, "last rows over the cache")
+    if kind != F8:
+        ends = [z - 1 for z in starts[1:]]
+        attn_ref.assert_within(dec, want[ends], tol[ends] + tol_d, "prompt and decode agree")
+
+    # the cached prefix read back and attended to as a prompt: what the cache holds, no more
+    rk, rv = gbe.kv_read(cache, slots, dtype)
+    again = gbe.attn_prompt(q, rk, rv, _i32(starts))
+    want_r, tol_r, _ = attn_ref.prompt(q, rk, rv, starts, scale, dtype == BF)
+    attn_ref.assert_within(again, want_r, tol_r, "over the cache read back")
+
+    n = list(lens)
+    for step in range(steps):
+        fused = torch.randn(3, Hq + 2 * H, D, generator=g, device="cuda").to(dtype)
+        q, k, v = _rotated(fused, _i32(n), om)
+        gbe.gbe_kv_write(k, v, _i32([slot(b, n[b]) for b in range(3)]), cache)
+        n = [x + 1 for x in n]
+        out = gbe.attn_decode(q, cache, table.cuda(), _i32(n))
+        want, tol = attn_ref.decode(q, cache, table.cuda(), n, scale, dtype == BF)
+        attn_ref.assert_within(out, want, tol, f"step {step}")
