@@ -214,6 +214,9 @@ cudaError_t pick(const PromptArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attn_prompt(const PromptArgs& a, int dtype, bool vec, cudaStream_t st) {
+    constexpr int64_t kFar = 1LL << 38;  // strides that a tensor copy can describe
+    if (dtype == GBE_BF16 && vec && a.D <= 128 && a.q_stride < kFar && a.k_stride < kFar && a.v_stride < kFar)
+        return launch_attn_prompt_tc(a, st);
     if (dtype == GBE_F32) return vec ? pick<kF32, true>(a, st) : pick<kF32, false>(a, st);
     return vec ? pick<kBF16, true>(a, st) : pick<kBF16, false>(a, st);
 }

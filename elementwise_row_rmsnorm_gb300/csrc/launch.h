@@ -149,6 +149,9 @@ struct PromptArgs {
     float scale;
 };
 
+// vec: rows on the 16-byte grid.
 cudaError_t launch_attn_prompt(const PromptArgs& a, int dtype, bool vec, cudaStream_t st);
+// bf16 on the tensor cores: D <= 128, rows on the 16-byte grid.
+cudaError_t launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t st);
 
 }  // namespace gbe
