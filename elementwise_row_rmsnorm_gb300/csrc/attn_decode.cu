@@ -10,49 +10,16 @@
 // of any size.  Each CTA leaves the unnormalised sum, the running maximum and
 // the running sum of its chunk in the workspace, and attn_join adds the
 // chunks of a row in order.  A sequence of one chunk is written at once.
-#include "common.cuh"
+#include "attn_decode.cuh"
 #include "gbe_elementwise.h"
 #include "kv_cache.cuh"
-#include "launch.h"
 
 namespace gbe {
 namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// A partial softmax's weight when its maximum m moves to m2: 0 while nothing
-// has been seen (m = -inf).
-__device__ __forceinline__ float rescale(float m, float m2) { return m == -INFINITY ? 0.0f : ex2(m - m2); }
-
-// Tokens of a chunk for a sequence of n tokens: n / split of them in units
-// of 64, at least `least`.
-__device__ __forceinline__ int chunk_tokens(int n, int split, int least) {
-    const int c = ((n + split - 1) / split + 63) & ~63;
-    return c < least ? least : c;
-}
-
-struct Args {
-    const void* q;
-    void* out;
-    int64_t q_stride, out_stride;
-    KvCacheArgs c;
-    const int32_t* table;
-    const int32_t* lens;
-    int Hq, group, max_pages;
-    int split, least;     // chunks at most, tokens a chunk at least
-    int parts;            // query-head parts of a kv head: ceil(group / H)
-    float scale;          // times log2(e)
-    float* part_o;        // [B * Hq, split, D]
-    float2* part_ml;      // [B * Hq, split]: running maximum (base 2), running sum
-};
+using namespace decode;
 
 // One 8-value piece of a cached row, widened to f32.
 template <int KV>
@@ -98,21 +65,11 @@ __global__ void __launch_bounds__(kThreads) decode_rows(Args a, int lanes_log2) 
     pdl_begin();
     const KvCacheArgs& c = a.c;
     const int G = 1 << lanes_log2, D = c.D;
-    uint32_t id = blockIdx.x;
-    const int part = id % a.parts;
-    id /= a.parts;
-    const int kvh = id % c.Hkv;
-    id /= c.Hkv;
-    const int chunk = id % a.split, b = id / a.split;
-
-    const int64_t capacity = (int64_t)a.max_pages * c.page_size;
-    const int32_t len = a.lens[b];
-    const int n = len < 0 ? 0 : (int)(len < capacity ? len : capacity);
-    const int C = chunk_tokens(n, a.split, a.least);
-    const int t0 = chunk * C, t1 = min(n, t0 + C);
-    if (t0 >= t1 && chunk > 0) return;
-    const int h0 = kvh * a.group + part * H;              // first query head
-    const int heads = min(H, a.group - part * H);
+    const Part p = find_part(a, blockIdx.x);
+    if (p.t0 >= p.t1 && p.chunk > 0) return;
+    const int b = p.b, kvh = p.kvh, t0 = p.t0, t1 = p.t1;
+    const int h0 = kvh * a.group + p.part * H;            // first query head
+    const int heads = min(H, a.group - p.part * H);
 
     const int sub = threadIdx.x & (G - 1), d0 = sub * 8;
     const bool mine = d0 < D;
@@ -166,9 +123,9 @@ __global__ void __launch_bounds__(kThreads) decode_rows(Args a, int lanes_log2) 
                 // a NaN logit leaves a finite maximum, so that its NaN weight reaches the result
                 const float m2 = fmaxf(m[h], s == s ? s : -3.0e38f);
                 const float r = rescale(m[h], m2);
-                const float p = s == -INFINITY ? 0.0f : ex2(s - m2);
-                l[h] = fmaf(l[h], r, p);
-                const float pv = KV == GBE_KV_E4M3 ? p * vs : p;
+                const float w = s == -INFINITY ? 0.0f : ex2(s - m2);
+                l[h] = fmaf(l[h], r, w);
+                const float pv = KV == GBE_KV_E4M3 ? w * vs : w;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[h][e] = fmaf(pv, v[e], acc[h][e] * r);
                 m[h] = m2;
@@ -186,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) decode_rows(Args a, int lanes_log2) 
         if (sub == 0) o[D] = m[h], o[D + 1] = l[h];
     }
     __syncthreads();
-    const bool whole = C >= n;
+    const bool whole = p.C >= p.n;
     for (int i = threadIdx.x; i < heads * D; i += kThreads) {
         const int h = i / D, d = i - h * D;
         float mx = -INFINITY;
@@ -194,14 +151,15 @@ __global__ void __launch_bounds__(kThreads) decode_rows(Args a, int lanes_log2) 
         float sum = 0.0f, o = 0.0f;
         for (int s = 0; s < streams; ++s) {
             const float* x = sm + (s * H + h) * W;
-            const float r = rescale(x[D], mx);
-            if (r != 0.0f) sum = fmaf(x[D + 1], r, sum), o = fmaf(x[d], r, o);
+            if (x[D] == -INFINITY) continue;  // nothing seen; a weight of 0 still carries NaN on
+            const float r = ex2(x[D] - mx);
+            sum = fmaf(x[D + 1], r, sum), o = fmaf(x[d], r, o);
         }
         if (whole) {
             Store<DT>::store1(a.out, b * a.out_stride + (int64_t)(h0 + h) * D + d,
                               mx == -INFINITY ? 0.0f : o / sum);
         } else {
-            const int64_t row = ((int64_t)b * a.Hq + h0 + h) * a.split + chunk;
+            const int64_t row = ((int64_t)b * a.Hq + h0 + h) * a.split + p.chunk;
             a.part_o[row * D + d] = o;
             if (d == 0) a.part_ml[row] = make_float2(mx, sum);
         }
@@ -230,8 +188,8 @@ __global__ void __launch_bounds__(kThreads) attn_join(Args a, int64_t rows) {
     float sum = 0.0f, o[8] = {};
     for (int s = 0; s < chunks; ++s) {
         const float2 v = ml[s];
-        const float w = rescale(v.x, mx);
-        if (w == 0.0f) continue;
+        if (v.x == -INFINITY) continue;  // nothing seen; a weight of 0 still carries NaN on
+        const float w = ex2(v.x - mx);
         sum = fmaf(v.y, w, sum);
         const float* p = a.part_o + (r * a.split + s) * D;
 #pragma unroll
@@ -263,9 +221,13 @@ cudaError_t pick(const Args& a, int64_t B, cudaStream_t st) {
 
 }  // namespace
 
+// Chunks of 512 tokens and more: shorter ones cost more in fixed work and in
+// partial results (4 * Hq / Hkv bytes written and read for every token and kv
+// head) than the SMs they bring in are worth.  At most as many chunks as
+// bring two CTAs to each of the 152 SMs from one sequence alone.
 DecodeSplit decode_split(int64_t Hkv, int64_t page_size, int64_t max_pages) {
     DecodeSplit s;
-    s.least = 128;
+    s.least = 512;
     int64_t want = (304 + Hkv - 1) / Hkv;
     want = want < 16 ? 16 : want > 128 ? 128 : want;
     const int64_t most = (page_size * max_pages + s.least - 1) / s.least;
@@ -284,10 +246,10 @@ cudaError_t launch_attn_decode(const DecodeArgs& d, int dtype, cudaStream_t st) 
     a.part_ml = static_cast<float2*>(d.workspace);
     a.part_o = reinterpret_cast<float*>(a.part_ml + d.B * d.Hq * s.split);
     cudaError_t e;
-    if (dtype == GBE_F32)
-        e = d.c.dtype == GBE_KV_E4M3 ? pick<kF32, GBE_KV_E4M3>(a, d.B, st) : pick<kF32, GBE_KV_F32>(a, d.B, st);
+    if (dtype == GBE_BF16)
+        e = decode::launch_mma(a, d.B, st);
     else
-        e = d.c.dtype == GBE_KV_E4M3 ? pick<kBF16, GBE_KV_E4M3>(a, d.B, st) : pick<kBF16, GBE_KV_BF16>(a, d.B, st);
+        e = d.c.dtype == GBE_KV_E4M3 ? pick<kF32, GBE_KV_E4M3>(a, d.B, st) : pick<kF32, GBE_KV_F32>(a, d.B, st);
     if (e != cudaSuccess || s.split == 1) return e;
     const int64_t rows = d.B * d.Hq;
     const dim3 grid(ceil_div_i(rows, kWarps));
