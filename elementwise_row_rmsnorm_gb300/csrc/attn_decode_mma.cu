@@ -19,8 +19,8 @@
 // tokens are put together by byte permutes.  P changes from the layout of a
 // result to that of B by movmatrix.
 //
-// A CTA is eight warps, each with tokens of its own (16 of every 128) and its
-// own running maximum, joined at the end in shared memory.  The maximum in use
+// A CTA is four warps, each with steps of tokens of its own and its own
+// running maximum, joined at the end in shared memory.  The maximum in use
 // lags behind by up to 2^8 (as weights, floats all of them, may), so that a
 // step costs one vote instead of a reduction.
 //
@@ -32,6 +32,8 @@
 // itself, as bf16 would, down to 2^-29 of the row's largest, and to 2^-37 of
 // that one below; a step with a scale more than 2^8 under E takes bf16 weights
 // and values instead.
+#include <type_traits>
+
 #include "attn_decode.cuh"
 #include "gbe_elementwise.h"
 #include "kv_cache.cuh"
@@ -40,8 +42,7 @@ namespace gbe {
 namespace decode {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kStep = 16;           // tokens a warp takes at a time
+constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kHeads = 8;           // query heads of a CTA
 constexpr int kScaleGrowth = 1, kScaleDrop = 8;
 
@@ -103,11 +104,13 @@ struct Eight {
 };
 
 template <int KV, int DP>
-__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) decode_mma(Args a) {
+__global__ void __launch_bounds__(kThreads, DP <= 128 ? 4 : 2) decode_mma(Args a) {
     constexpr bool E4 = KV == GBE_KV_E4M3;
     constexpr float kGrowth = E4 ? 2.0f : 8.0f;  // powers of two that the maximum in use may lag
-    constexpr int KC = DP / 32, VC = DP / 64;  // pieces of a K row, of a V row
-    extern __shared__ float sm[];              // [kWarps][kHeads][DP + 2]
+    constexpr int KC = DP / 32, VC = DP / 64;    // pieces of a K row, of a V row
+    constexpr int SUB = E4 ? 2 : 1;              // groups of 16 tokens a step: as many bytes for either cache
+    constexpr int kStep = 16 * SUB, kStride = kStep * kWarps;
+    extern __shared__ float sm[];                // [kWarps][kHeads][DP + 2]
     pdl_begin();
     const KvCacheArgs& c = a.c;
     const Part p = find_part(a, blockIdx.x);
@@ -115,6 +118,64 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) decode_mma(Args a
     const int D = c.D, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int h0 = p.kvh * a.group + p.part * kHeads;
     const int heads = min(kHeads, a.group - p.part * kHeads);
+
+    // where token base + lane % kStep lies: its page (-1: none) ...
+    const int32_t* pages = a.table + (int64_t)p.b * a.max_pages;
+    const int mine = lane & (kStep - 1);
+    auto page_of = [&](int base) {
+        const int tok = base + mine;
+        return tok < p.t1 ? pages[tok / c.page_size] : -1;
+    };
+    // ... and its row's first element in k and v (-1: none) and scales
+    struct Place {
+        int64_t at;
+        uint32_t scales;
+    };
+    auto place = [&](int base, int32_t page) {
+        Place w = {-1, 0};
+        if (page >= 0 && page < c.n_pages) {
+            const int row = (base + mine) % c.page_size;
+            w.at = page * c.page_stride + ((int64_t)p.kvh * c.page_size + row) * D;
+            if constexpr (E4) {
+                const int64_t si = ((int64_t)page * c.Hkv + p.kvh) * c.page_size + row;
+                w.scales = (uint32_t)c.k_scale[si] | (uint32_t)c.v_scale[si] << 8;
+            }
+        }
+        return w;
+    };
+    Eight<KV> k[SUB][2][KC], v[SUB][4][VC];
+    auto load_k = [&](const Place& w) {
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int64_t at = __shfl_sync(0xFFFFFFFFu, w.at, 16 * u + g + 8 * i);
+#pragma unroll
+                for (int x = 0; x < KC; ++x) {
+                    const int d = x * 32 + t * 8;
+                    k[u][i][x].load(c.k, at + d, at >= 0 && d < D);
+                }
+            }
+    };
+    auto load_v = [&](const Place& w) {
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t at = __shfl_sync(0xFFFFFFFFu, w.at, 16 * u + 2 * t + (i & 1) + 8 * (i >> 1));
+#pragma unroll
+                for (int x = 0; x < VC; ++x) {
+                    const int d = x * 64 + g * 8;
+                    v[u][i][x].load(c.v, at + d, at >= 0 && d < D);
+                }
+            }
+    };
+
+    int base = p.t0 + warp * kStep;
+    Place now = place(base, page_of(base));
+    load_k(now);
+    load_v(now);
+    int32_t page1 = page_of(base + kStride);
 
     // q of head g, the inner index of the first product as above
     uint32_t q[KC][4];
@@ -159,88 +220,38 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) decode_mma(Args a
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
     int E = -1000;
 
-    // where token base + lane % 16 lies: its page (-1: none) ...
-    const int32_t* pages = a.table + (int64_t)p.b * a.max_pages;
-    const int r16 = lane & 15;
-    auto page_of = [&](int base) {
-        const int tok = base + r16;
-        return tok < p.t1 ? pages[tok / c.page_size] : -1;
-    };
-    // ... and its row's first element in k and v (-1: none) and scales
-    struct Place {
-        int64_t at;
-        uint32_t scales;
-    };
-    auto place = [&](int base, int32_t page) {
-        Place w = {-1, 0};
-        if (page >= 0 && page < c.n_pages) {
-            const int row = (base + r16) % c.page_size;
-            w.at = page * c.page_stride + ((int64_t)p.kvh * c.page_size + row) * D;
-            if constexpr (E4) {
-                const int64_t si = ((int64_t)page * c.Hkv + p.kvh) * c.page_size + row;
-                w.scales = (uint32_t)c.k_scale[si] | (uint32_t)c.v_scale[si] << 8;
-            }
-        }
-        return w;
-    };
-    Eight<KV> k[2][KC], v[4][VC];
-    auto load_k = [&](const Place& w) {
+    for (; base < p.t1; base += kStride) {
+        float s[SUB][4];  // tokens g (heads 2 t, 2 t + 1) and g + 8 of each group
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t at = __shfl_sync(0xFFFFFFFFu, w.at, g + 8 * i);
+        for (int u = 0; u < SUB; ++u) {
+            s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.0f;
 #pragma unroll
-            for (int x = 0; x < KC; ++x) {
-                const int d = x * 32 + t * 8;
-                k[i][x].load(c.k, at + d, at >= 0 && d < D);
-            }
-        }
-    };
-    auto load_v = [&](const Place& w) {
+            for (int x = 0; x < KC; ++x)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t at = __shfl_sync(0xFFFFFFFFu, w.at, 2 * t + (i & 1) + 8 * (i >> 1));
-#pragma unroll
-            for (int x = 0; x < VC; ++x) {
-                const int d = x * 64 + g * 8;
-                v[i][x].load(c.v, at + d, at >= 0 && d < D);
-            }
-        }
-    };
-
-    int base = p.t0 + warp * kStep;
-    Place now = place(base, page_of(base));
-    load_k(now);
-    load_v(now);
-    int32_t page1 = page_of(base + kStep * kWarps);
-    for (; base < p.t1; base += kStep * kWarps) {
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // tokens g (heads 2 t, 2 t + 1) and g + 8
-#pragma unroll
-        for (int x = 0; x < KC; ++x) {
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                if constexpr (E4) {
-                    const uint32_t f[4] = {e4m3x2_f16x2<0>(k[0][x].w[y]), e4m3x2_f16x2<0>(k[1][x].w[y]),
-                                           e4m3x2_f16x2<1>(k[0][x].w[y]), e4m3x2_f16x2<1>(k[1][x].w[y])};
-                    mma_f16(s, f, q[x][2 * y], q[x][2 * y + 1]);
-                } else {
-                    const uint32_t f[4] = {k[0][x].w[2 * y], k[1][x].w[2 * y], k[0][x].w[2 * y + 1],
-                                           k[1][x].w[2 * y + 1]};
-                    mma_bf16(s, f, q[x][2 * y], q[x][2 * y + 1]);
+                for (int y = 0; y < 2; ++y) {
+                    if constexpr (E4) {
+                        const uint32_t f[4] = {e4m3x2_f16x2<0>(k[u][0][x].w[y]), e4m3x2_f16x2<0>(k[u][1][x].w[y]),
+                                               e4m3x2_f16x2<1>(k[u][0][x].w[y]), e4m3x2_f16x2<1>(k[u][1][x].w[y])};
+                        mma_f16(s[u], f, q[x][2 * y], q[x][2 * y + 1]);
+                    } else {
+                        const uint32_t f[4] = {k[u][0][x].w[2 * y], k[u][1][x].w[2 * y], k[u][0][x].w[2 * y + 1],
+                                               k[u][1][x].w[2 * y + 1]};
+                        mma_bf16(s[u], f, q[x][2 * y], q[x][2 * y + 1]);
+                    }
                 }
-            }
         }
         // the next step's K, and the page after it
-        const Place next = place(base + kStep * kWarps, page1);
+        const Place next = place(base + kStride, page1);
         load_k(next);
-        page1 = page_of(base + 2 * kStep * kWarps);
+        page1 = page_of(base + 2 * kStride);
 
-        float ks[2] = {1.0f, 1.0f}, vf[2];  // k's scales of tokens g, g + 8, and 2^(byte - E + 12) of v's
+        const uint32_t live = __ballot_sync(0xFFFFFFFFu, now.at >= 0);
         bool wide = false;
         if constexpr (E4) {
-            const bool live = now.at >= 0;
+            const bool here = now.at >= 0;
             const int e = (int)(now.scales >> 8);
-            if (__any_sync(0xFFFFFFFFu, live && e - E > kScaleGrowth)) {
-                const int top = __reduce_max_sync(0xFFFFFFFFu, live ? e : 0);
+            if (__any_sync(0xFFFFFFFFu, here && e - E > kScaleGrowth)) {
+                const int top = __reduce_max_sync(0xFFFFFFFFu, here ? e : 0);
                 const int by = min(max(E, 0) - top, 0);
                 const float r = by < -126 ? 0.0f : __uint_as_float((uint32_t)(127 + by) << 23);
                 if (E >= 0) {
@@ -251,28 +262,31 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) decode_mma(Args a
                 }
                 E = max(E, top);
             }
-            wide = __any_sync(0xFFFFFFFFu, live && e > 0 && E - e > kScaleDrop);
+            wide = __any_sync(0xFFFFFFFFu, here && e > 0 && E - e > kScaleDrop);
+        }
+        float vf[SUB][2];  // 2^(byte - E + 12) of v's scales
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t w = __shfl_sync(0xFFFFFFFFu, now.scales, g + 8 * i);
-                ks[i] = __uint_as_float((w & 255u) << 23);
-                const int by = (int)(w >> 8) - E + 12;
-                vf[i] = (w >> 8) == 0 || by < -126 ? 0.0f : __uint_as_float((uint32_t)(127 + by) << 23);
+                const bool here = live >> (16 * u + g + 8 * i) & 1u;
+                float ks = 1.0f;
+                if constexpr (E4) {
+                    const uint32_t w = __shfl_sync(0xFFFFFFFFu, now.scales, 16 * u + g + 8 * i);
+                    ks = __uint_as_float((w & 255u) << 23);
+                    const int by = (int)(w >> 8) - E + 12;
+                    vf[u][i] = (w >> 8) == 0 || by < -126 ? 0.0f : __uint_as_float((uint32_t)(127 + by) << 23);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float& x = s[u][2 * i + h];
+                    x = E4 ? x * cs[h] * ks : x * cs[h];
+                    x = here ? x : -INFINITY;
+                    // a NaN logit leaves a finite maximum, so that its NaN weight reaches the result
+                    top[h] = fmaxf(top[h], x == x ? x : -3.0e38f);
+                }
             }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const bool live = __shfl_sync(0xFFFFFFFFu, now.at, g + 8 * i) >= 0;
-            s[2 * i] = live ? s[2 * i] * cs[0] * ks[i] : -INFINITY;
-            s[2 * i + 1] = live ? s[2 * i + 1] * cs[1] * ks[i] : -INFINITY;
-        }
-        float top[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            // a NaN logit leaves a finite maximum, so that its NaN weight reaches the result
-            const float x = s[h] == s[h] ? s[h] : -3.0e38f, y = s[2 + h] == s[2 + h] ? s[2 + h] : -3.0e38f;
-            top[h] = fmaxf(x, y);
-        }
         if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + kGrowth || top[1] > m[1] + kGrowth)) {
             float r[2];
 #pragma unroll
@@ -292,53 +306,63 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) decode_mma(Args a
                 o[x][3] *= r[1];
             }
         }
-        float w[4];
+        const float shift[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float x = m[i & 1] == -INFINITY ? 0.0f : m[i & 1];
-            w[i] = ex2(s[i] - x);
-            l[i & 1] += w[i];
-            if constexpr (E4) w[i] *= vf[i >> 1];
-        }
-        const bool half = E4 && !wide;
-        uint32_t b0, b1;
-        if (half) {
-            b0 = transpose8(f16x2(w[0], w[1])), b1 = transpose8(f16x2(w[2], w[3]));
-        } else {
-            b0 = transpose8(f32x2_to_bf16x2_bits(w[0], w[1])), b1 = transpose8(f32x2_to_bf16x2_bits(w[2], w[3]));
-        }
+        for (int u = 0; u < SUB; ++u)
 #pragma unroll
-        for (int x = 0; x < VC; ++x)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                // rows: entries 64 x + 8 g + 2 y (lanes' first) and + 2 y + 1
-                uint32_t f[4];
-                if constexpr (E4) {
-                    const uint32_t sel = y & 1 ? 0x7362u : 0x5140u;  // the two tokens' codes of both entries
-                    const uint32_t u = __byte_perm(v[0][x].w[y >> 1], v[1][x].w[y >> 1], sel);
-                    const uint32_t z = __byte_perm(v[2][x].w[y >> 1], v[3][x].w[y >> 1], sel);
-                    f[0] = e4m3x2_f16x2<0>(u), f[1] = e4m3x2_f16x2<1>(u);
-                    f[2] = e4m3x2_f16x2<0>(z), f[3] = e4m3x2_f16x2<1>(z);
-                    if (half) {
-                        mma_f16(o[x * 4 + y], f, b0, b1);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) f[i] = f16x2_bf16x2(f[i]);
-                        mma_bf16(o[x * 4 + y], f, b0, b1);
-                    }
-                } else {
-                    f[0] = __byte_perm(v[0][x].w[y], v[1][x].w[y], 0x5410);
-                    f[1] = __byte_perm(v[0][x].w[y], v[1][x].w[y], 0x7632);
-                    f[2] = __byte_perm(v[2][x].w[y], v[3][x].w[y], 0x5410);
-                    f[3] = __byte_perm(v[2][x].w[y], v[3][x].w[y], 0x7632);
-                    mma_bf16(o[x * 4 + y], f, b0, b1);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float w = ex2(s[u][i] - shift[i & 1]);
+                l[i & 1] += w;
+                s[u][i] = E4 ? w * vf[u][i >> 1] : w;
             }
+        // o += V^T P^T; rows of the product: entries 64 x + 8 g + 2 y and + 2 y + 1
+        auto weigh = [&](auto half) {
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                uint32_t b0, b1;
+                if constexpr (decltype(half)::value) {
+                    b0 = transpose8(f16x2(s[u][0], s[u][1])), b1 = transpose8(f16x2(s[u][2], s[u][3]));
+                } else {
+                    b0 = transpose8(f32x2_to_bf16x2_bits(s[u][0], s[u][1]));
+                    b1 = transpose8(f32x2_to_bf16x2_bits(s[u][2], s[u][3]));
+                }
+#pragma unroll
+                for (int x = 0; x < VC; ++x)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        uint32_t f[4];
+                        if constexpr (E4) {
+                            const uint32_t sel = y & 1 ? 0x7362u : 0x5140u;  // the two tokens' codes of both entries
+                            const uint32_t w = __byte_perm(v[u][0][x].w[y >> 1], v[u][1][x].w[y >> 1], sel);
+                            const uint32_t z = __byte_perm(v[u][2][x].w[y >> 1], v[u][3][x].w[y >> 1], sel);
+                            f[0] = e4m3x2_f16x2<0>(w), f[1] = e4m3x2_f16x2<1>(w);
+                            f[2] = e4m3x2_f16x2<0>(z), f[3] = e4m3x2_f16x2<1>(z);
+                            if constexpr (decltype(half)::value) {
+                                mma_f16(o[x * 4 + y], f, b0, b1);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) f[i] = f16x2_bf16x2(f[i]);
+                                mma_bf16(o[x * 4 + y], f, b0, b1);
+                            }
+                        } else {
+                            f[0] = __byte_perm(v[u][0][x].w[y], v[u][1][x].w[y], 0x5410);
+                            f[1] = __byte_perm(v[u][0][x].w[y], v[u][1][x].w[y], 0x7632);
+                            f[2] = __byte_perm(v[u][2][x].w[y], v[u][3][x].w[y], 0x5410);
+                            f[3] = __byte_perm(v[u][2][x].w[y], v[u][3][x].w[y], 0x7632);
+                            mma_bf16(o[x * 4 + y], f, b0, b1);
+                        }
+                    }
+            }
+        };
+        if (E4 && !wide)
+            weigh(std::bool_constant<E4>{});
+        else
+            weigh(std::false_type{});
         load_v(next);
         now = next;
     }
 
-    // the eight warps' sums, joined in order
+    // the warps' sums, joined in order
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
