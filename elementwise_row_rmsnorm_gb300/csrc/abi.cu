@@ -756,11 +756,11 @@ static bool decode_sizes_ok(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64
     if (B < 0 || B > (1 << 20) || Hkv < 1 || Hkv > 4096 || Hq < Hkv || Hq > 65536 || Hq % Hkv) return false;
     if (D < 8 || D > 256 || D % 8 || page_size < 1 || page_size > (1 << 20) || max_pages < 0) return false;
     if (max_pages > (1 << 30) / page_size) return false;
-    return B * gbe::decode_split(Hkv, page_size, max_pages).split <= INT32_MAX / Hq;
+    return B * gbe::decode_split(page_size, max_pages).split <= INT32_MAX / Hq;
 }
 
 static uint64_t decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size, int64_t max_pages) {
-    const int64_t split = gbe::decode_split(Hkv, page_size, max_pages).split;
+    const int64_t split = gbe::decode_split(page_size, max_pages).split;
     return split == 1 ? 0u : (uint64_t)B * Hq * split * (D + 2) * 4;
 }
 

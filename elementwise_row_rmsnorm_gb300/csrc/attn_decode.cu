@@ -18,7 +18,6 @@ namespace gbe {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
 using namespace decode;
 
 // One 8-value piece of a cached row, widened to f32.
@@ -166,13 +165,18 @@ __global__ void __launch_bounds__(kThreads) decode_rows(Args a, int lanes_log2) 
     }
 }
 
-// The chunks of one row added in order: one warp a (sequence, query head).
+// The chunks of one row added: one CTA a (sequence, query head).  Warp w adds
+// chunks w, w + 8, ... in order, four entries a lane, and the warps' sums are
+// added in order.  The loads of a warp's chunks do not wait on one another: one
+// warp walking all 128 chunks of a long row took over 100 us.
+constexpr int kJoinWarps = 8, kMostChunks = 128;
 template <int DT>
-__global__ void __launch_bounds__(kThreads) attn_join(Args a, int64_t rows) {
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join(Args a) {
+    __shared__ float weight[kMostChunks], sums[kJoinWarps];
+    __shared__ float4 part[kJoinWarps][64];
     pdl_begin();
-    const int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (r >= rows) return;
-    const int lane = threadIdx.x & 31, D = a.c.D;
+    const int64_t r = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.c.D;
     const int64_t b = r / a.Hq, h = r - b * a.Hq;
     const int64_t capacity = (int64_t)a.max_pages * a.c.page_size;
     const int32_t len = a.lens[b];
@@ -180,26 +184,53 @@ __global__ void __launch_bounds__(kThreads) attn_join(Args a, int64_t rows) {
     const int C = chunk_tokens(n, a.split, a.least);
     if (C >= n) return;  // one chunk: already written
     const int chunks = (n + C - 1) / C;
+    // every warp finds the maximum for itself
     const float2* ml = a.part_ml + r * a.split;
     float mx = -INFINITY;
     for (int s = lane; s < chunks; s += 32) mx = fmaxf(mx, ml[s].x);
 #pragma unroll
     for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
-    float sum = 0.0f, o[8] = {};
-    for (int s = 0; s < chunks; ++s) {
+    // -1 marks a chunk in which nothing was seen; a weight of 0 still carries NaN on
+    float l = 0.0f;
+    for (int s = threadIdx.x; s < chunks; s += kJoinWarps * 32) {
         const float2 v = ml[s];
-        if (v.x == -INFINITY) continue;  // nothing seen; a weight of 0 still carries NaN on
-        const float w = ex2(v.x - mx);
-        sum = fmaf(v.y, w, sum);
-        const float* p = a.part_o + (r * a.split + s) * D;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (lane + 32 * e < D) o[e] = fmaf(p[lane + 32 * e], w, o[e]);
+        const float w = v.x == -INFINITY ? -1.0f : ex2(v.x - mx);
+        weight[s] = w;
+        if (w >= 0.0f) l = fmaf(v.y, w, l);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (lane + 32 * e < D)
-            Store<DT>::store1(a.out, b * a.out_stride + h * D + lane + 32 * e, mx == -INFINITY ? 0.0f : o[e] / sum);
+    for (int x = 16; x >= 1; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+    if (lane == 0) sums[warp] = l;
+    __syncthreads();
+    float4 o[2] = {};
+    const float* from = a.part_o + r * a.split * D + lane * 4;
+#pragma unroll 4
+    for (int s = warp; s < chunks; s += kJoinWarps) {
+        const float w = weight[s];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (lane * 4 + x * 128 >= D) continue;
+            const float4 v = *reinterpret_cast<const float4*>(from + (int64_t)s * D + x * 128);
+            if (w >= 0.0f) {
+                o[x].x = fmaf(v.x, w, o[x].x);
+                o[x].y = fmaf(v.y, w, o[x].y);
+                o[x].z = fmaf(v.z, w, o[x].z);
+                o[x].w = fmaf(v.w, w, o[x].w);
+            }
+        }
+    }
+    part[warp][lane] = o[0];
+    part[warp][32 + lane] = o[1];
+    __syncthreads();
+    float sum = 0.0f;
+#pragma unroll
+    for (int x = 0; x < kJoinWarps; ++x) sum += sums[x];
+    if (threadIdx.x < D) {
+        float y = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kJoinWarps; ++x) y += reinterpret_cast<const float*>(part[x])[threadIdx.x];
+        Store<DT>::store1(a.out, b * a.out_stride + h * D + threadIdx.x, mx == -INFINITY ? 0.0f : y / sum);
+    }
 }
 
 template <int DT, int KV, int H>
@@ -223,38 +254,35 @@ cudaError_t pick(const Args& a, int64_t B, cudaStream_t st) {
 
 // Chunks of 512 tokens and more: shorter ones cost more in fixed work and in
 // partial results (4 * Hq / Hkv bytes written and read for every token and kv
-// head) than the SMs they bring in are worth.  At most as many chunks as
-// bring two CTAs to each of the 152 SMs from one sequence alone.
-DecodeSplit decode_split(int64_t Hkv, int64_t page_size, int64_t max_pages) {
+// head) than the SMs they bring in are worth.  128 chunks at most, so that two
+// sequences of 131072 tokens make 2048 CTAs.
+DecodeSplit decode_split(int64_t page_size, int64_t max_pages) {
     DecodeSplit s;
     s.least = 512;
-    int64_t want = (304 + Hkv - 1) / Hkv;
-    want = want < 16 ? 16 : want > 128 ? 128 : want;
     const int64_t most = (page_size * max_pages + s.least - 1) / s.least;
-    s.split = (int)(want < most ? want : most < 1 ? 1 : most);
+    s.split = (int)(most < 1 ? 1 : most > kMostChunks ? kMostChunks : most);
     return s;
 }
 
 cudaError_t launch_attn_decode(const DecodeArgs& d, int dtype, cudaStream_t st) {
     Args a = {};
-    const DecodeSplit s = decode_split(d.c.Hkv, d.c.page_size, d.max_pages);
+    const DecodeSplit s = decode_split(d.c.page_size, d.max_pages);
     a.q = d.q, a.out = d.out, a.q_stride = d.q_stride, a.out_stride = d.out_stride;
     a.c = d.c, a.table = d.table, a.lens = d.lens;
     a.Hq = (int)d.Hq, a.group = (int)(d.Hq / d.c.Hkv), a.max_pages = (int)d.max_pages;
-    a.split = s.split, a.least = s.least;
+    a.split = s.split, a.least = s.least, a.run = 1;
     a.scale = d.scale * kLog2e;
-    a.part_ml = static_cast<float2*>(d.workspace);
-    a.part_o = reinterpret_cast<float*>(a.part_ml + d.B * d.Hq * s.split);
+    a.part_o = static_cast<float*>(d.workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + d.B * d.Hq * s.split * d.c.D);
     cudaError_t e;
     if (dtype == GBE_BF16)
         e = decode::launch_mma(a, d.B, st);
     else
         e = d.c.dtype == GBE_KV_E4M3 ? pick<kF32, GBE_KV_E4M3>(a, d.B, st) : pick<kF32, GBE_KV_F32>(a, d.B, st);
     if (e != cudaSuccess || s.split == 1) return e;
-    const int64_t rows = d.B * d.Hq;
-    const dim3 grid(ceil_div_i(rows, kWarps));
-    return dtype == GBE_F32 ? launch(attn_join<kF32>, grid, dim3(kThreads), 0, st, a, rows)
-                            : launch(attn_join<kBF16>, grid, dim3(kThreads), 0, st, a, rows);
+    const dim3 rows((unsigned)(d.B * d.Hq)), threads(kJoinWarps * 32);
+    return dtype == GBE_F32 ? launch(attn_join<kF32>, rows, threads, 0, st, a)
+                            : launch(attn_join<kBF16>, rows, threads, 0, st, a);
 }
 
 }  // namespace gbe

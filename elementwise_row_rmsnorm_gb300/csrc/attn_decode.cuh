@@ -22,9 +22,9 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float rescale(float m, float m2) { return m == -INFINITY ? 0.0f : ex2(m - m2); }
 
 // Tokens of a chunk for a sequence of n tokens: n / split of them in units
-// of 64, at least `least`.
+// of 128, at least `least`.
 __device__ __forceinline__ int chunk_tokens(int n, int split, int least) {
-    const int c = ((n + split - 1) / split + 63) & ~63;
+    const int c = ((n + split - 1) / split + 127) & ~127;
     return c < least ? least : c;
 }
 
@@ -38,16 +38,17 @@ struct Args {
     int Hq, group, max_pages;
     int split, least;     // chunks at most, tokens a chunk at least
     int parts;            // query-head parts of a kv head: ceil(group / H)
+    int run;              // chunks that one CTA takes one after another
     float scale;          // times log2(e)
     float* part_o;        // [B * Hq, split, D]
     float2* part_ml;      // [B * Hq, split]: running maximum (base 2), running sum
 };
 
 // The CTA's part of the work, from its index: query-head part innermost, then
-// kv head, then chunk.
+// kv head, then chunks.
 struct Part {
-    int b, kvh, chunk, part;
-    int n, C, t0, t1;  // the sequence's tokens, tokens a chunk, and this chunk's
+    int b, kvh, chunk, part;  // chunk: the first of a.run
+    int n, C, t0, t1;         // the sequence's tokens, tokens a chunk, and those of this CTA
 };
 __device__ __forceinline__ Part find_part(const Args& a, uint32_t id) {
     Part p;
@@ -55,14 +56,16 @@ __device__ __forceinline__ Part find_part(const Args& a, uint32_t id) {
     id /= (uint32_t)a.parts;
     p.kvh = (int)(id % (uint32_t)a.c.Hkv);
     id /= (uint32_t)a.c.Hkv;
-    p.chunk = (int)(id % (uint32_t)a.split);
-    p.b = (int)(id / (uint32_t)a.split);
+    const uint32_t runs = (uint32_t)((a.split + a.run - 1) / a.run);
+    p.chunk = (int)(id % runs) * a.run;
+    p.b = (int)(id / runs);
     const int64_t capacity = (int64_t)a.max_pages * a.c.page_size;
     const int32_t len = a.lens[p.b];
     p.n = len < 0 ? 0 : (int)(len < capacity ? len : capacity);
     p.C = chunk_tokens(p.n, a.split, a.least);
+    // (chunk, run at most 128 and C at most 2^30 / split + 127: no overflow)
     p.t0 = p.chunk * p.C;
-    p.t1 = min(p.n, p.t0 + p.C);
+    p.t1 = (int)min((int64_t)p.n, p.t0 + (int64_t)a.run * p.C);
     return p;
 }
 

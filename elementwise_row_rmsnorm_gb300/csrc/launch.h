@@ -122,7 +122,7 @@ cudaError_t launch_kv_read(void* k, int64_t k_stride, void* v, int64_t v_stride,
 struct DecodeSplit {
     int split, least;
 };
-DecodeSplit decode_split(int64_t Hkv, int64_t page_size, int64_t max_pages);
+DecodeSplit decode_split(int64_t page_size, int64_t max_pages);
 
 struct DecodeArgs {
     const void* q;
