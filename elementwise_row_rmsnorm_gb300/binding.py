@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 
 import torch
@@ -439,6 +440,7 @@ class _KvCacheStruct(ctypes.Structure):
                 ("dtype", ctypes.c_int)]
 
 
+_pack_cache = struct.Struct("@PPPPqqqqqi4x").pack
 _KV_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2}
 
 
@@ -449,33 +451,38 @@ class KvCache:
     [n_pages, 2, Hkv, page_size, D] tensor will do); a float8_e4m3fn cache also
     has k_scale and v_scale, uint8 [n_pages, Hkv, page_size].  Holds the
     tensors and their description; no state of its own."""
-    __slots__ = ("k", "v", "k_scale", "v_scale", "shape", "desc", "ptr")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "shape", "desc")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
                  v_scale: torch.Tensor | None = None):
-        shape, st = k.shape, k.stride()
-        if len(shape) != 4 or v.shape != shape or k.dtype not in _KV_DTYPES or v.dtype != k.dtype:
+        shape, kind = k.shape, _KV_DTYPES.get(k.dtype)
+        if len(shape) != 4 or v.shape != shape or kind is None or v.dtype != k.dtype:
             raise ValueError("KvCache: k and v are [n_pages, Hkv, page_size, D], float32, bfloat16 or float8_e4m3fn")
         N, H, P, D = shape
-        if N > 1:
-            if v.stride() != st or st[1:] != (P * D, D, 1):
+        stride = H * P * D
+        if not (k.is_contiguous() and v.is_contiguous()):
+            st = k.stride()
+            if N <= 1 or v.stride() != st or st[1:] != (P * D, D, 1):
                 raise ValueError("KvCache: the pages of k and v are contiguous and share a stride")
-        elif not (k.is_contiguous() and v.is_contiguous()):
-            raise ValueError("KvCache: the pages of k and v are contiguous and share a stride")
-        scales = (k_scale, v_scale)
-        if k.dtype == torch.float8_e4m3fn:
-            for s in scales:
+            stride = st[0]
+        if kind == 2:
+            for s in (k_scale, v_scale):
                 if s is None or s.dtype != torch.uint8 or s.shape != (N, H, P) or not s.is_contiguous():
                     raise ValueError("KvCache: a float8_e4m3fn cache has uint8 scales [n_pages, Hkv, page_size]")
         elif k_scale is not None or v_scale is not None:
             raise ValueError("KvCache: only a float8_e4m3fn cache has scales")
-        for t in (k, v, *scales):
-            if t is not None and not _on_device(t):
-                raise ValueError("tensors must be on the CUDA device or in pinned host memory")
+        _where(k, v, k_scale, v_scale)
         self.k, self.v, self.k_scale, self.v_scale, self.shape = k, v, k_scale, v_scale, shape
-        self.desc = _KvCacheStruct(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), N, H, P, D,
-                                   st[0] if N > 1 else H * P * D, _KV_DTYPES[k.dtype])
-        self.ptr = ctypes.addressof(self.desc)
+        # the bytes of a gbe_kv_cache, which the library reads during the call
+        self.desc = _pack_cache(k.data_ptr(), v.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
+                                0 if v_scale is None else v_scale.data_ptr(), N, H, P, D, stride, kind)
+
+
+def _where(*ts):
+    """Every tensor given is one that the device can address."""
+    for t in ts:
+        if t is not None and not (t.is_cuda or t.is_pinned()):
+            raise ValueError("tensors must be on the CUDA device or in pinned host memory")
 
 
 def _kv_sides(what, k, v, cache, slots, bad):
@@ -487,10 +494,9 @@ def _kv_sides(what, k, v, cache, slots, bad):
         raise ValueError(f"{what}: slots is int32[T]")
     if bad is not None and (bad.dtype != torch.int32 or bad.numel() != 1):
         raise ValueError(f"{what}: bad_slot_count is one int32")
-    for t in (k, v, slots, bad):
-        if t is not None and not _on_device(t):
-            raise ValueError("tensors must be on the CUDA device or in pinned host memory")
-    return k.data_ptr(), sk, v.data_ptr(), sv, slots.data_ptr(), T, cache.ptr, _ptr(bad), _dt(k, v)
+    _where(k, v, slots, bad)
+    return (k.data_ptr(), sk, v.data_ptr(), sv, slots.data_ptr(), T, cache.desc, None if bad is None else bad.data_ptr(),
+            _dt(k, v))
 
 
 def gbe_kv_write(k, v, slots, cache: KvCache, bad_slot_count=None, stream=None) -> None:
@@ -518,25 +524,25 @@ def attn_decode_workspace(B: int, Hq: int, cache: KvCache, max_pages: int) -> in
 def gbe_attn_decode(q, out, cache: KvCache, table, lens, scale: float, workspace=None, stream=None) -> None:
     """q, out: [B, Hq, D]; table: int32[B, max_pages]; lens: int32[B], the new token included; workspace: any tensor
     of attn_decode_workspace bytes (None when that is 0)."""
-    B, Hq, sq = _rows_view(q, cache.shape[3])
-    _, _, so = _rows_view(out, cache.shape[3])
-    if out.shape != q.shape:
+    D = cache.shape[3]
+    B, Hq, sq = _rows_view(q, D)
+    Bo, Ho, so = _rows_view(out, D)
+    if Bo != B or Ho != Hq:
         raise ValueError("attn_decode: out has q's shape")
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B or not table.is_contiguous():
+    rows = table.shape
+    if table.dtype != torch.int32 or len(rows) != 2 or rows[0] != B or not table.is_contiguous():
         raise ValueError("attn_decode: table is int32[B, max_pages]")
     if lens.dtype != torch.int32 or lens.numel() != B or not lens.is_contiguous():
         raise ValueError("attn_decode: lens is int32[B]")
-    for t in (q, out, table, lens, workspace):
-        if t is not None and not _on_device(t):
-            raise ValueError("tensors must be on the CUDA device or in pinned host memory")
+    _where(q, out, table, lens, workspace)
     room = 0
     if workspace is not None:
         if not workspace.is_contiguous():
             raise ValueError("tensors must be contiguous")
         room = workspace.numel() * workspace.element_size()
     _check("gbe_attn_decode", lib().gbe_attn_decode(
-        q.data_ptr(), sq, out.data_ptr(), so, B, Hq, cache.ptr, table.data_ptr(), table.shape[1], lens.data_ptr(),
-        scale, _ptr(workspace), room, _dt(q, out), _stream(stream)))
+        q.data_ptr(), sq, out.data_ptr(), so, B, Hq, cache.desc, table.data_ptr(), rows[1], lens.data_ptr(), scale,
+        None if workspace is None else workspace.data_ptr(), room, _dt(q, out), _stream(stream)))
 
 
 def gbe_attn_prompt(q, k, v, out, starts, scale: float, stream=None) -> None:
@@ -551,9 +557,7 @@ def gbe_attn_prompt(q, k, v, out, starts, scale: float, stream=None) -> None:
         raise ValueError("attn_prompt: q and out are [T, Hq, D], k and v [T, Hkv, D]")
     if starts.dtype != torch.int32 or starts.numel() < 1 or not starts.is_contiguous():
         raise ValueError("attn_prompt: starts is int32[n_seqs + 1]")
-    for t in (q, k, v, out, starts):
-        if not _on_device(t):
-            raise ValueError("tensors must be on the CUDA device or in pinned host memory")
+    _where(q, k, v, out, starts)
     _check("gbe_attn_prompt", lib().gbe_attn_prompt(
         q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, out.data_ptr(), so, starts.data_ptr(),
         starts.numel() - 1, T, Hq, Hkv, D, scale, _dt(q, k, v, out), _stream(stream)))
@@ -574,15 +578,16 @@ def kv_read(cache: KvCache, slots, dtype=None, stream=None):
     """(k, v), each [T, Hkv, D], of the slots; dtype: the cache's own unless it is 8-bit (then bfloat16)."""
     if dtype is None:
         dtype = torch.bfloat16 if cache.k.dtype == torch.float8_e4m3fn else cache.k.dtype
-    k, v = (torch.empty((slots.numel(), cache.shape[1], cache.shape[3]), dtype=dtype, device=slots.device)
-            for _ in range(2))
+    shape = (slots.numel(), cache.shape[1], cache.shape[3])
+    k = torch.empty(shape, dtype=dtype, device=slots.device)
+    v = torch.empty_like(k)
     gbe_kv_read(k, v, slots, cache, None, stream)
     return k, v
 
 
 def attn_decode(q, cache: KvCache, table, lens, scale: float | None = None, workspace=None, stream=None):
     """[B, Hq, D]; allocates the workspace unless one is given."""
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if workspace is None:
         n = attn_decode_workspace(q.shape[0], q.shape[1], cache, table.shape[1])
         if n:
@@ -597,7 +602,7 @@ def attn_decode(q, cache: KvCache, table, lens, scale: float | None = None, work
 
 def attn_prompt(q, k, v, starts, scale: float | None = None, stream=None):
     """[T, Hq, D]; rows outside [starts[0], starts[-1]) are not written."""
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    out = torch.empty_like(q, memory_format=torch.contiguous_format)
     gbe_attn_prompt(q, k, v, out, starts, 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale, stream)
     return out
 

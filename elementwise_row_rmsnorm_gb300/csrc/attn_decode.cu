@@ -17,7 +17,7 @@
 namespace gbe {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 using namespace decode;
 
 // One 8-value piece of a cached row, widened to f32.
@@ -55,12 +55,16 @@ struct Piece<GBE_KV_E4M3> {
     }
 };
 
-// The CUDA-core form: G lanes (the power of two at or above D / 8) hold one
-// token's row, eight values each, so a warp walks 32 / G tokens at a time
-// and each lane keeps the query heads' pieces and the output's in registers.
+// The CUDA-core form, for f32 queries: G lanes (the power of two at or above
+// D / 8) hold one token's row, eight values each, so a warp walks 32 / G
+// streams of tokens and each lane keeps the query heads' pieces and the
+// output's in registers.  A stream takes four tokens at a time: their loads are
+// on their way together (64 KB for a CTA's f32 rows, enough to cover HBM's
+// latency from one CTA an SM), and the running maximum moves once for the four.
 template <int DT, int KV, int H>
-__global__ void __launch_bounds__(kThreads) decode_rows(Args a, int lanes_log2) {
-    extern __shared__ float sm[];  // [kThreads / G][H][D + 2]
+__global__ void __launch_bounds__(kThreads, 1) decode_rows(Args a, int lanes_log2) {
+    constexpr int U = 4;
+    extern __shared__ float sm[];  // [kWarps][H][D + 2]
     pdl_begin();
     const KvCacheArgs& c = a.c;
     const int G = 1 << lanes_log2, D = c.D;
@@ -90,65 +94,112 @@ __global__ void __launch_bounds__(kThreads) decode_rows(Args a, int lanes_log2) 
     const int32_t* pages = a.table + (int64_t)b * a.max_pages;
     // all streams of a warp take the same number of steps, so that its
     // shuffles meet
-    for (int base = t0; base < t1; base += streams) {
-        const int t = base + stream;
-        const bool live = t < t1;
-        const int page_i = live ? t / c.page_size : 0;
-        const int32_t page = live ? pages[page_i] : -1;
-        const bool good = page >= 0 && page < c.n_pages;
-        Piece<KV> kp = {}, vp = {};
-        float ks = 1.0f, vs = 1.0f;
-        if (good) {
+    for (int base = t0; base < t1; base += U * streams) {
+        Piece<KV> kp[U], vp[U];
+        float ks[U], vs[U];
+        bool good[U];
+        int64_t at[U], si[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = base + u * streams + stream;
+            const bool live = t < t1;
+            const int page_i = live ? t / c.page_size : 0;
+            const int32_t page = live ? pages[page_i] : -1;
             const int row = t - page_i * c.page_size;
-            const int64_t i = page * c.page_stride + ((int64_t)kvh * c.page_size + row) * D + d0;
-            if (mine) kp.load(c.k, i), vp.load(c.v, i);
-            if (KV == GBE_KV_E4M3) {
-                const int64_t si = ((int64_t)page * c.Hkv + kvh) * c.page_size + row;
-                ks = __uint_as_float((uint32_t)c.k_scale[si] << 23);
-                vs = __uint_as_float((uint32_t)c.v_scale[si] << 23);
+            good[u] = page >= 0 && page < c.n_pages;
+            at[u] = page * c.page_stride + ((int64_t)kvh * c.page_size + row) * D + d0;
+            si[u] = ((int64_t)page * c.Hkv + kvh) * c.page_size + row;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            kp[u] = {}, vp[u] = {};
+            ks[u] = vs[u] = 1.0f;
+            if (good[u] && mine) kp[u].load(c.k, at[u]), vp[u].load(c.v, at[u]);
+            if (KV == GBE_KV_E4M3 && good[u]) {
+                ks[u] = __uint_as_float((uint32_t)c.k_scale[si[u]] << 23);
+                vs[u] = __uint_as_float((uint32_t)c.v_scale[si[u]] << 23);
             }
         }
-        float k[8], v[8];
-        kp.widen(k);
-        vp.widen(v);
+        float s[U][H];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float k[8];
+            kp[u].widen(k);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                float x = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x = fmaf(q[h][e], k[e], x);
+                for (int y = G >> 1; y >= 1; y >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, y);
+                s[u][h] = good[u] ? (KV == GBE_KV_E4M3 ? x * ks[u] : x) : -INFINITY;
+            }
+        }
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-            float s = 0.0f;
+            float m2 = m[h];
+            // a NaN logit leaves a finite maximum, so that its NaN weight reaches the result
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s = fmaf(q[h][e], k[e], s);
-            for (int x = G >> 1; x >= 1; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-            if (KV == GBE_KV_E4M3) s *= ks;
-            if (good) {
-                // a NaN logit leaves a finite maximum, so that its NaN weight reaches the result
-                const float m2 = fmaxf(m[h], s == s ? s : -3.0e38f);
-                const float r = rescale(m[h], m2);
-                const float w = s == -INFINITY ? 0.0f : ex2(s - m2);
-                l[h] = fmaf(l[h], r, w);
-                const float pv = KV == GBE_KV_E4M3 ? w * vs : w;
+            for (int u = 0; u < U; ++u) m2 = fmaxf(m2, s[u][h] == s[u][h] ? s[u][h] : -3.0e38f);
+            const float r = rescale(m[h], m2);
+            m[h] = m2;
+            l[h] *= r;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[h][e] = fmaf(pv, v[e], acc[h][e] * r);
-                m[h] = m2;
+            for (int e = 0; e < 8; ++e) acc[h][e] *= r;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                s[u][h] = s[u][h] == -INFINITY ? 0.0f : ex2(s[u][h] - m2);
+                l[h] += s[u][h];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float v[8];
+            vp[u].widen(v);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const float w = KV == GBE_KV_E4M3 ? s[u][h] * vs[u] : s[u][h];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[h][e] = fmaf(w, v[e], acc[h][e]);
             }
         }
     }
-    // join the streams in order, in shared memory
-    const int W = D + 2;
+    // the warp's streams joined, pair by pair: both sides compute the same sums
+    for (int x = G; x < 32; x <<= 1) {
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-        float* o = sm + (stream * H + h) * W;
-        if (mine)
+        for (int h = 0; h < H; ++h) {
+            const float mo = __shfl_xor_sync(0xFFFFFFFFu, m[h], x), lo = __shfl_xor_sync(0xFFFFFFFFu, l[h], x);
+            const float m2 = fmaxf(m[h], mo), r = rescale(m[h], m2), ro = rescale(mo, m2);
+            l[h] = l[h] * r + lo * ro;
+            m[h] = m2;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[d0 + e] = acc[h][e];
-        if (sub == 0) o[D] = m[h], o[D + 1] = l[h];
+            for (int e = 0; e < 8; ++e) {
+                const float o = __shfl_xor_sync(0xFFFFFFFFu, acc[h][e], x);
+                acc[h][e] = __fadd_rn(__fmul_rn(acc[h][e], r), __fmul_rn(o, ro));
+            }
+        }
+    }
+    // and the warps in order, in shared memory
+    const int W = D + 2, warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) < G) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            float* o = sm + (warp * H + h) * W;
+            if (mine)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[d0 + e] = acc[h][e];
+            if (sub == 0) o[D] = m[h], o[D + 1] = l[h];
+        }
     }
     __syncthreads();
     const bool whole = p.C >= p.n;
     for (int i = threadIdx.x; i < heads * D; i += kThreads) {
         const int h = i / D, d = i - h * D;
         float mx = -INFINITY;
-        for (int s = 0; s < streams; ++s) mx = fmaxf(mx, sm[(s * H + h) * W + D]);
+#pragma unroll
+        for (int s = 0; s < kWarps; ++s) mx = fmaxf(mx, sm[(s * H + h) * W + D]);
         float sum = 0.0f, o = 0.0f;
-        for (int s = 0; s < streams; ++s) {
+#pragma unroll
+        for (int s = 0; s < kWarps; ++s) {
             const float* x = sm + (s * H + h) * W;
             if (x[D] == -INFINITY) continue;  // nothing seen; a weight of 0 still carries NaN on
             const float r = ex2(x[D] - mx);
@@ -238,7 +289,10 @@ cudaError_t go(Args a, int64_t B, cudaStream_t st) {
     int lg = 0;
     while ((8 << lg) < a.c.D) ++lg;
     a.parts = (a.group + H - 1) / H;
-    const size_t smem = (size_t)(kThreads >> lg) * H * (a.c.D + 2) * 4;
+    const size_t smem = (size_t)kWarps * H * (a.c.D + 2) * 4;
+    static FunctionLimit limit;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(decode_rows<DT, KV, H>), kWarps * H * 258 * 4);
+    if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(B * a.split * a.c.Hkv * a.parts));
     return launch(decode_rows<DT, KV, H>, grid, dim3(kThreads), smem, st, a, lg);
 }
@@ -247,7 +301,8 @@ template <int DT, int KV>
 cudaError_t pick(const Args& a, int64_t B, cudaStream_t st) {
     if (a.group == 1) return go<DT, KV, 1>(a, B, st);
     if (a.group == 2) return go<DT, KV, 2>(a, B, st);
-    return go<DT, KV, 4>(a, B, st);
+    if (a.group <= 4) return go<DT, KV, 4>(a, B, st);
+    return go<DT, KV, 8>(a, B, st);
 }
 
 }  // namespace

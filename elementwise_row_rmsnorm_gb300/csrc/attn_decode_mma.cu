@@ -494,11 +494,9 @@ cudaError_t go(Args a, int64_t B, cudaStream_t st) {
     const int heads = a.group < kHeads ? a.group : kHeads;
     const int smem = S::kRing + kWarps * heads * (DP + 2) * 4;
     constexpr int most = S::kRing + kWarps * kHeads * (DP + 2) * 4;
-    const cudaError_t e = cudaFuncSetAttribute(decode_mma<KV, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return e;
-    }
+    static FunctionLimit limit;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(decode_mma<KV, DP>), most);
+    if (e != cudaSuccess) return e;
     a.parts = (a.group + kHeads - 1) / kHeads;
     // Several chunks to a CTA while that leaves eight waves of CTAs.
     const int64_t rows = B * a.c.Hkv * a.parts, want = rows * a.split / (8 * 3 * (int64_t)sm_count());

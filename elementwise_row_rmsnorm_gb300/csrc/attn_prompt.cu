@@ -193,13 +193,9 @@ __global__ void __launch_bounds__(kThreads) prompt_rows(PromptArgs a) {
 template <int DT, int DP, bool VEC>
 cudaError_t go(const PromptArgs& a, cudaStream_t st) {
     constexpr int smem = ((kM + 2 * kN) * (DP + 4) + kM * (kN + 4)) * 4;
-    // a property of the function on the current device, the same value every time
-    const cudaError_t e = cudaFuncSetAttribute(prompt_rows<DT, DP, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               smem);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return e;
-    }
+    static FunctionLimit limit;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(prompt_rows<DT, DP, VEC>), smem);
+    if (e != cudaSuccess) return e;
     const int64_t tiles = a.T / kM + (a.n_seqs < a.T ? a.n_seqs : a.T);
     return launch(prompt_rows<DT, DP, VEC>, dim3((unsigned)(tiles * a.Hq)), dim3(kThreads), smem, st, a);
 }

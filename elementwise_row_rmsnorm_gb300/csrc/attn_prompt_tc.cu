@@ -453,11 +453,9 @@ cudaError_t go(const PromptArgs& a, cudaStream_t st) {
         !encode(&mv, a.v, a.T, a.Hkv, a.D, a.v_stride))
         return cudaErrorNotSupported;
     constexpr int smem = Shape<DP>::kBytes;
-    const cudaError_t e = cudaFuncSetAttribute(prompt_tc<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return e;
-    }
+    static FunctionLimit limit;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(prompt_tc<DP>), smem);
+    if (e != cudaSuccess) return e;
     const int64_t group = a.Hq / a.Hkv, seqs = a.n_seqs < a.T ? a.n_seqs : a.T;
     const int64_t pairs = ((a.T / kM + seqs) * group + (group & 1 ? seqs : 0)) / 2;
     return launch(prompt_tc<DP>, dim3((unsigned)(pairs * a.Hkv)), dim3(kThreads), smem, st, mq, mk, mv, a);

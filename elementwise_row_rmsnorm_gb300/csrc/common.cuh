@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 namespace gbe {
@@ -107,6 +108,27 @@ inline cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
     if (e != cudaSuccess) cudaGetLastError();  // clear it; the caller reports e
     return e;
 }
+
+// Dynamic shared memory past 48 KB is granted to a kernel once a device; one of
+// these for each kernel remembers on which devices that has been done.
+class FunctionLimit {
+  public:
+    cudaError_t raise(const void* kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) {
+            const unsigned long long bit = 1ull << (dev & 63);
+            if (dev < 64 && (done_.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            if (e == cudaSuccess && dev < 64) done_.fetch_or(bit, std::memory_order_release);
+        }
+        if (e != cudaSuccess) cudaGetLastError();  // clear it; the caller reports e
+        return e;
+    }
+
+  private:
+    std::atomic<unsigned long long> done_{0};
+};
 
 // ---- RoPE angles ------------------------------------------------------------------
 

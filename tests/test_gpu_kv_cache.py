@@ -221,3 +221,36 @@ def test_many_rows(kind):
             assert torch.equal(got.cpu().double(), y)
     else:
         assert torch.equal(gk, k) and torch.equal(gv, v)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_a_cache_of_the_rows_type_holds_every_bit(dtype, pad):
+    """Infinities, signed zeros and NaN of any payload, on and off the 16-byte grid."""
+    T, H, D, P = 40, 2, 64, 16
+    es = torch.empty((), dtype=dtype).element_size()
+    raw = torch.randint(0, 256, (T, (2 * H * D + pad) * es), generator=torch.Generator().manual_seed(3),
+                        dtype=torch.uint8).cuda().view(dtype)
+    raw[:, ::7] = float("nan")
+    raw.view(torch.uint8)[:, 1::13] = 0xFF
+    k, v = raw[:, :H * D].unflatten(1, (H, D)), raw[:, H * D:2 * H * D].unflatten(1, (H, D))
+    cache = gbe.kv_cache(4, H, P, D, dtype)
+    slots = torch.randperm(4 * P, generator=torch.Generator().manual_seed(4))[:T].to(torch.int32).cuda()
+    gbe.gbe_kv_write(k, v, slots, cache)
+    out = torch.zeros_like(raw)
+    ok, ov = out[:, :H * D].unflatten(1, (H, D)), out[:, H * D:2 * H * D].unflatten(1, (H, D))
+    gbe.gbe_kv_read(ok, ov, slots, cache)
+    assert torch.equal(_bytes(ok), _bytes(k)) and torch.equal(_bytes(ov), _bytes(v))
+
+
+@pytest.mark.parametrize("H,P", [(7, 11), (1, 1), (12, 100), (64, 16), (3, 4096)])
+def test_odd_heads_and_pages(H, P):
+    """Counts that are no powers of two, and pages larger than the batch."""
+    T, D = 333, 32
+    pages = -(-T // P) + 1
+    cache = gbe.kv_cache(pages, H, P, D, torch.bfloat16)
+    k, v = _rand((T, H, D), torch.bfloat16, 21), _rand((T, H, D), torch.bfloat16, 22)
+    slots = torch.randperm(pages * P, generator=torch.Generator().manual_seed(2))[:T].to(torch.int32).cuda()
+    _check_write(cache, k, v, slots)
+    gk, gv = gbe.kv_read(cache, slots)
+    assert torch.equal(gk, k) and torch.equal(gv, v)
