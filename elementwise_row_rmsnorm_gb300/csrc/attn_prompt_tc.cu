@@ -33,7 +33,7 @@ namespace gbe {
 namespace {
 
 constexpr int kM = 128, kN = 128;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;  // three warpgroups: softmax of each tile, and the issuing warps
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrowth = 8.0f;  // a maximum may lag this many powers of two
@@ -53,7 +53,7 @@ struct Shape {
 };
 
 struct Control {
-    uint64_t q_full, kv_full[9], kv_empty[9], s_full[2], p_ready[2], o_full[2], drained;
+    uint64_t q_full, kv_full[9], kv_empty[9], s_full[2], p_ready[2][2], o_full[2], drained;
     uint32_t tmem;
     int abort;
     int begin, len, unit0, units;  // the sequence and its first tile here; how many tiles
@@ -183,7 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_addr(&ctl.s_full[t]), 1);
-            mbar_init(smem_addr(&ctl.p_ready[t]), 128);
+            mbar_init(smem_addr(&ctl.p_ready[t][0]), 128);
+            mbar_init(smem_addr(&ctl.p_ready[t][1]), 128);
             mbar_init(smem_addr(&ctl.o_full[t]), 1);
         }
         mbar_init(smem_addr(&ctl.drained), 1);
@@ -214,6 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int most = max(blocks[0], blocks[1]);
 
+    // Registers: 384 threads were launched with 168 each (64512); the softmax
+    // warpgroups take 208, the issuing one keeps 80 (63488 in all).
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == kLoadWarp) {
         if (lane == 0 && units > 0) {
             const uint32_t qb = smem_addr(&ctl.q_full);
@@ -260,12 +265,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 mma_commit(smem_addr(&ctl.s_full[t]));
             };
-            auto weigh = [&](int t, int st, bool add) {
+            auto weigh = [&](int t, int st, int half, bool add) {
                 const uint32_t v0 = kv_smem + st * S::kTile;
 #pragma unroll
-                for (int x = 0; x < kN / 16; ++x)
+                for (int y = 0; y < kN / 32; ++y) {
+                    const int x = half * (kN / 32) + y;
                     mma_ts(tmem + 256 + t * 128, tmem + t * 128 + x * 8, smem_desc(v0 + x * 2048, S::kPanel, 1024),
                            idesc_o, add || x > 0);
+                }
             };
             ok = ok && mbar_wait(smem_addr(&ctl.kv_full[stage]), phase, abort);
             if (ok) {
@@ -286,10 +293,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (!ok || j >= blocks[t]) continue;
-                    ok = mbar_wait(smem_addr(&ctl.p_ready[t]), j & 1, abort);
+                    ok = mbar_wait(smem_addr(&ctl.p_ready[t][0]), j & 1, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    weigh(t, vs, j > 0);
+                    weigh(t, vs, 0, j > 0);
+                    ok = mbar_wait(smem_addr(&ctl.p_ready[t][1]), j & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    weigh(t, vs, 1, j > 0);
                     if (j + 1 == blocks[t]) mma_commit(smem_addr(&ctl.o_full[t]));
                     if (t == 1 || j >= blocks[1]) mma_commit(smem_addr(&ctl.kv_empty[vs]));
                     if (j + 1 < blocks[t]) {
@@ -307,7 +318,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             int none = 0;
             mbar_wait(smem_addr(&ctl.drained), 0, &none);
         }
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = warp >> 2;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
         const uint32_t ts = tmem + t * 128 + lanes, to = tmem + 256 + t * 128 + lanes;
@@ -328,17 +341,43 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int x = 0; x < 128; ++x) s[x] = x <= seen ? s[x] : 0xFF800000u;
             }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            auto maximum = [&] {
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int x = 0; x < 128; x += 4)
+                for (int x = 0; x < 128; x += 8)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[x + e]));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const bool grow = m == -INFINITY || (top - m) * c > kGrowth;
-            const float m2 = grow ? fmaxf(m, top) : m;
-            const float r = m == -INFINITY ? 0.0f : ex2((m - m2) * c);
-            m = m2;
-            if (j > 0 && __any_sync(0xFFFFFFFFu, r != 1.0f)) {
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[x + e]), __uint_as_float(s[x + 4 + e])));
+                return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            };
+            // half a row's weights, packed, and their sum
+            float2 sum[2];
+            auto weights = [&](int half, uint32_t (&w)[32]) {
+                const float shift = m == -INFINITY ? 0.0f : -m * c;
+                const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+                sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    float2 x = fma2_rn(make_float2(__uint_as_float(s[64 * half + 2 * e]),
+                                                   __uint_as_float(s[64 * half + 2 * e + 1])), c2, shift2);
+                    x.x = ex2(x.x), x.y = ex2(x.y);
+                    sum[e & 1] = add2_rn(sum[e & 1], x);
+                    w[e] = f32x2_to_bf16x2_bits(x.x, x.y);
+                }
+                return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            };
+            // The first half is weighed with the maximum of the blocks before,
+            // while this block's is being found; only where that has grown too
+            // much are O and the sum rescaled and the half weighed again.
+            if (j == 0) m = maximum();
+            uint32_t w[32];
+            float add = weights(0, w);
+            const float top = maximum();
+            const bool grow = m == -INFINITY ? top > m : (top - m) * c > kGrowth;
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+                const float m2 = grow ? top : m;
+                const float r = m == -INFINITY ? 0.0f : ex2((m - m2) * c);
+                m = m2;
                 l *= r;
 #pragma unroll
                 for (int x = 0; x < DP / 32; ++x) {
@@ -349,26 +388,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
                     tmem_st32(to + x * 32, o);
                 }
+                add = weights(0, w);
             }
-            const float shift = m == -INFINITY ? 0.0f : -m * c;
-            float sum[4] = {};
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                uint32_t w[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float p0 = ex2(fmaf(__uint_as_float(s[64 * x + 2 * e]), c, shift));
-                    const float p1 = ex2(fmaf(__uint_as_float(s[64 * x + 2 * e + 1]), c, shift));
-                    sum[(2 * e) & 3] += p0;
-                    sum[(2 * e + 1) & 3] += p1;
-                    w[e] = f32x2_to_bf16x2_bits(p0, p1);
-                }
-                tmem_st32(ts + x * 32, w);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            l += add;
+            tmem_st32(ts, w);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(smem_addr(&ctl.p_ready[t]));
+            mbar_arrive(smem_addr(&ctl.p_ready[t][0]));
+            l += weights(1, w);
+            tmem_st32(ts + 32, w);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(smem_addr(&ctl.p_ready[t][1]));
         }
         if (n > 0) {
             ok = ok && mbar_wait(smem_addr(&ctl.o_full[t]), 0, abort);
