@@ -6,19 +6,26 @@
 //
 // A CTA works on two tiles of 128 query rows that share one kv head -- two
 // heads of its group at the same rows, or neighbouring row tiles -- and walks
-// the keys in blocks of 128 that a ring of shared-memory stages holds.  Ten
-// warps: four of softmax for each tile (a thread owns a row), one that issues
-// the tensor copies, one that issues the products.  Tensor memory (512
-// columns): S and O of both tiles; the weights, rounded to bf16, overwrite
-// their tile's S and are the A operand of the second product.  While one
-// tile's softmax runs, the tensor cores do the other's two products.
+// the keys in blocks of 128 that a ring of shared-memory stages holds.  Three
+// warpgroups: one of softmax for each tile (a thread owns a row), and one of
+// which a warp issues the tensor copies and another the products.
 //
-// The products of one CTA execute in the order of their issue, so "S of block
-// j + 1 is there" also says that block j's product with v is done: O may be
-// rescaled then without a further wait.  It is rescaled only when a row's
-// maximum has grown by more than 2^8 over the one in use; until then weights
-// go up to 2^8, which costs nothing in bf16 or f32 (both floats) and keeps
-// sums far from overflow.
+// Tensor memory (512 columns): one S for both tiles, O of each, and the
+// weights of each, rounded to bf16, which are the A operand of the second
+// product.  A block of 128 keys costs a tile 512 clocks of either product and
+// its warpgroup some 1400 clocks of softmax, so the products of a tile must not
+// wait for its softmax: they are issued in the order
+//
+//   S0 = q0 k(j+1)^T, O0 += p0 v(j), S1 = q1 k(j+1)^T, O1 += p1 v(j)
+//
+// S is handed over as soon as a warpgroup has it in registers, and each
+// softmax then has 1500 clocks until its weights are asked for.  (With an S
+// for each tile, overwritten by its weights, the next S had to wait for the
+// product with v, and a round of both tiles took 3300 clocks, not 2048.)
+//
+// O is rescaled only when a row's maximum has grown by more than 2^8 over the
+// one in use; until then weights go up to 2^8, which costs nothing in bf16 or
+// f32 (both floats) and keeps sums far from overflow.
 //
 // Masked weights are exact zeros, but zero times an infinity or a NaN in a
 // later row of v would reach the sum; a row that ends up not finite is
@@ -53,7 +60,7 @@ struct Shape {
 };
 
 struct Control {
-    uint64_t q_full, kv_full[9], kv_empty[9], s_full[2], p_ready[2][2], o_full[2], drained;
+    uint64_t q_full, kv_full[9], kv_empty[9], s_full[2], s_free[2], p_ready[2][2], o_done[2], drained;
     uint32_t tmem;
     int abort;
     int begin, len, unit0, units;  // the sequence and its first tile here; how many tiles
@@ -183,9 +190,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_addr(&ctl.s_full[t]), 1);
-            mbar_init(smem_addr(&ctl.p_ready[t][0]), 128);
-            mbar_init(smem_addr(&ctl.p_ready[t][1]), 128);
-            mbar_init(smem_addr(&ctl.o_full[t]), 1);
+            mbar_init(smem_addr(&ctl.p_ready[t][0]), 4);
+            mbar_init(smem_addr(&ctl.p_ready[t][1]), 4);
+            mbar_init(smem_addr(&ctl.s_free[t]), 4);
+            mbar_init(smem_addr(&ctl.o_done[t]), 1);
         }
         mbar_init(smem_addr(&ctl.drained), 1);
         ctl.abort = 0;
@@ -219,111 +227,97 @@ __global__ void __launch_bounds__(kThreads, 1)
     // warpgroups take 208, the issuing one keeps 80 (63488 in all).
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == kLoadWarp) {
-        if (lane == 0 && units > 0) {
-            const uint32_t qb = smem_addr(&ctl.q_full);
-            mbar_arrive_tx(qb, S::kTile * units);
-            for (int t = 0; t < units; ++t)
+        if (warp == kLoadWarp) {
+            if (units > 0 && elect_one()) {
+                const uint32_t qb = smem_addr(&ctl.q_full);
+                mbar_arrive_tx(qb, S::kTile * units);
+                for (int t = 0; t < units; ++t)
 #pragma unroll
-                for (int p = 0; p < DP / 64; ++p)
-                    tma_load_3d(q_smem + t * S::kTile + p * S::kPanel, &mq, qb, p * 64, head[t], begin + row0[t]);
-            int stage = 0, phase = 0, issued = 0;
-            for (int i = 0; i < 2 * most; ++i) {  // k and v of each block in turn
-                if (!mbar_wait(smem_addr(&ctl.kv_empty[stage]), phase ^ 1, abort)) break;
-                const uint32_t full = smem_addr(&ctl.kv_full[stage]);
-                mbar_arrive_tx(full, S::kTile);
+                    for (int p = 0; p < DP / 64; ++p)
+                        tma_load_3d(q_smem + t * S::kTile + p * S::kPanel, &mq, qb, p * 64, head[t], begin + row0[t]);
+                int stage = 0, phase = 0, issued = 0;
+                for (int i = 0; i < 2 * most; ++i) {  // k and v of each block in turn
+                    if (!mbar_wait(smem_addr(&ctl.kv_empty[stage]), phase ^ 1, abort)) break;
+                    const uint32_t full = smem_addr(&ctl.kv_full[stage]);
+                    mbar_arrive_tx(full, S::kTile);
 #pragma unroll
-                for (int p = 0; p < DP / 64; ++p)
-                    tma_load_3d(kv_smem + stage * S::kTile + p * S::kPanel, (i & 1) ? &mv : &mk, full, p * 64, kvh,
-                                begin + (i >> 1) * kN);
-                ++issued;
-                if (++stage == S::kStages) stage = 0, phase ^= 1;
-            }
-            if (*abort) {  // nothing may still be on its way when the CTA ends
-                int none = 0;
-                mbar_wait(qb, 0, &none);
-                for (int i = max(0, issued - S::kStages); i < issued; ++i)
-                    mbar_wait(smem_addr(&ctl.kv_full[i % S::kStages]), (i / S::kStages) & 1, &none);
-            }
-        }
-    } else if (warp == kMmaWarp) {
-        if (lane == 0 && units > 0) {
-            const uint32_t idesc_s = bf16_idesc(kM, kN, false) | (a.scale < 0.0f ? 1u << 13 : 0u);
-            constexpr uint32_t idesc_o = bf16_idesc(kM, DP, true);
-            int stage = 0, phase = 0;
-            bool ok = mbar_wait(smem_addr(&ctl.q_full), 0, abort);
-            auto next = [&] {
-                if (++stage == S::kStages) stage = 0, phase ^= 1;
-            };
-            auto scores = [&](int t, int st) {
-                const uint32_t q0 = q_smem + t * S::kTile, k0 = kv_smem + st * S::kTile;
-#pragma unroll
-                for (int x = 0; x < DP / 16; ++x) {
-                    const uint32_t off = (x / 4) * S::kPanel + (x % 4) * 32;
-                    mma_ss(tmem + t * 128, smem_desc(q0 + off, 16, 1024), smem_desc(k0 + off, 16, 1024), idesc_s,
-                           x > 0);
+                    for (int p = 0; p < DP / 64; ++p)
+                        tma_load_3d(kv_smem + stage * S::kTile + p * S::kPanel, (i & 1) ? &mv : &mk, full, p * 64, kvh,
+                                    begin + (i >> 1) * kN);
+                    ++issued;
+                    if (++stage == S::kStages) stage = 0, phase ^= 1;
                 }
-                mma_commit(smem_addr(&ctl.s_full[t]));
-            };
-            auto weigh = [&](int t, int st, int half, bool add) {
-                const uint32_t v0 = kv_smem + st * S::kTile;
-#pragma unroll
-                for (int y = 0; y < kN / 32; ++y) {
-                    const int x = half * (kN / 32) + y;
-                    mma_ts(tmem + 256 + t * 128, tmem + t * 128 + x * 8, smem_desc(v0 + x * 2048, S::kPanel, 1024),
-                           idesc_o, add || x > 0);
+                if (*abort) {  // nothing may still be on its way when the CTA ends
+                    int none = 0;
+                    mbar_wait(qb, 0, &none);
+                    for (int i = max(0, issued - S::kStages); i < issued; ++i)
+                        mbar_wait(smem_addr(&ctl.kv_full[i % S::kStages]), (i / S::kStages) & 1, &none);
                 }
-            };
-            ok = ok && mbar_wait(smem_addr(&ctl.kv_full[stage]), phase, abort);
-            if (ok) {
-                tc_fence_after();
-                if (blocks[0] > 0) scores(0, stage);
-                if (blocks[1] > 0) scores(1, stage);
-                mma_commit(smem_addr(&ctl.kv_empty[stage]));
             }
-            next();
-            for (int j = 0; ok && j < most; ++j) {
-                const int vs = stage, vp = phase;
-                next();
-                const int ks = stage, kp = phase;
-                const bool more = j + 1 < most;
-                if (more) next();
-                ok = mbar_wait(smem_addr(&ctl.kv_full[vs]), vp, abort);
-                bool have_k = false;
+        } else if (warp == kMmaWarp) {
+            if (units > 0 && elect_one()) {
+                const uint32_t idesc_s = bf16_idesc(kM, kN, false) | (a.scale < 0.0f ? 1u << 13 : 0u);
+                constexpr uint32_t idesc_o = bf16_idesc(kM, DP, true);
+                bool ok = mbar_wait(smem_addr(&ctl.q_full), 0, abort);
+                // load i (k of block i / 2, or v) lies in stage i % kStages
+                auto stage = [](int i) { return i % S::kStages; };
+                auto loaded = [&](int i) {
+                    return mbar_wait(smem_addr(&ctl.kv_full[stage(i)]), i / S::kStages & 1, abort);
+                };
+                auto release = [&](int i) { mma_commit(smem_addr(&ctl.kv_empty[stage(i)])); };
+                int last_t = -1, last_j = 0;  // the tile and block that S was last written for
+                auto scores = [&](int t, int j) {
+                    if (last_t >= 0) ok = ok && mbar_wait(smem_addr(&ctl.s_free[last_t]), last_j & 1, abort);
+                    if (!ok) return;
+                    last_t = t, last_j = j;
+                    tc_fence_after();
+                    const uint32_t q0 = q_smem + t * S::kTile, k0 = kv_smem + stage(2 * j) * S::kTile;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (!ok || j >= blocks[t]) continue;
-                    ok = mbar_wait(smem_addr(&ctl.p_ready[t][0]), j & 1, abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    weigh(t, vs, 0, j > 0);
-                    ok = mbar_wait(smem_addr(&ctl.p_ready[t][1]), j & 1, abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    weigh(t, vs, 1, j > 0);
-                    if (j + 1 == blocks[t]) mma_commit(smem_addr(&ctl.o_full[t]));
-                    if (t == 1 || j >= blocks[1]) mma_commit(smem_addr(&ctl.kv_empty[vs]));
-                    if (j + 1 < blocks[t]) {
-                        if (!have_k) ok = mbar_wait(smem_addr(&ctl.kv_full[ks]), kp, abort);
-                        if (!ok) break;
-                        have_k = true;
-                        tc_fence_after();
-                        scores(t, ks);
+                    for (int x = 0; x < DP / 16; ++x) {
+                        const uint32_t off = (x / 4) * S::kPanel + (x % 4) * 32;
+                        mma_ss(tmem, smem_desc(q0 + off, 16, 1024), smem_desc(k0 + off, 16, 1024), idesc_s, x > 0);
                     }
+                    mma_commit(smem_addr(&ctl.s_full[t]));
+                };
+                auto weigh = [&](int t, int j) {
+                    const uint32_t v0 = kv_smem + stage(2 * j + 1) * S::kTile;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        ok = ok && mbar_wait(smem_addr(&ctl.p_ready[t][half]), j & 1, abort);
+                        if (!ok) return;
+                        tc_fence_after();
+#pragma unroll
+                        for (int x = half * 4; x < half * 4 + 4; ++x)
+                            mma_ts(tmem + 256 + t * 128, tmem + 128 + t * 64 + x * 8,
+                                   smem_desc(v0 + x * 2048, S::kPanel, 1024), idesc_o, j > 0 || x > 0);
+                    }
+                    mma_commit(smem_addr(&ctl.o_done[t]));
+                };
+                ok = ok && loaded(0);
+                for (int t = 0; t < 2; ++t)
+                    if (ok && blocks[t] > 0) scores(t, 0);
+                if (ok) release(0);
+                for (int j = 0; ok && j < most; ++j) {
+                    if (j + 1 < most) ok = loaded(2 * j + 2);
+                    for (int t = 0; t < 2; ++t) {
+                        if (ok && j + 1 < blocks[t]) scores(t, j + 1);
+                        if (t == 0) ok = ok && loaded(2 * j + 1);
+                        if (t == 1 && ok && j + 1 < most) release(2 * j + 2);
+                        if (ok && j < blocks[t]) weigh(t, j);
+                    }
+                    if (ok) release(2 * j + 1);
                 }
-                if (ok && more) mma_commit(smem_addr(&ctl.kv_empty[ks]));
+                // every product is done before tensor memory is given back
+                mma_commit(smem_addr(&ctl.drained));
+                int none = 0;
+                mbar_wait(smem_addr(&ctl.drained), 0, &none);
             }
-            // every product is done before tensor memory is given back
-            mma_commit(smem_addr(&ctl.drained));
-            int none = 0;
-            mbar_wait(smem_addr(&ctl.drained), 0, &none);
         }
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = warp >> 2;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
-        const uint32_t ts = tmem + t * 128 + lanes, to = tmem + 256 + t * 128 + lanes;
+        const uint32_t ts = tmem + lanes, tp = tmem + 128 + t * 64 + lanes, to = tmem + 256 + t * 128 + lanes;
         const int n = blocks[t], row = row0[t] + (threadIdx.x & 127);
         const float c = fabsf(a.scale) * kLog2e;
         float m = -INFINITY, l = 0.0f;
@@ -335,7 +329,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t s[128];
 #pragma unroll
             for (int x = 0; x < 4; ++x) tmem_ld32(ts + x * 32, s + x * 32);
-            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) tmem_wait_ld32(s + x * 32);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&ctl.s_free[t]));
             if (j == n - 1) {  // the diagonal
                 const int seen = row - j * kN;
 #pragma unroll
@@ -374,6 +372,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             float add = weights(0, w);
             const float top = maximum();
             const bool grow = m == -INFINITY ? top > m : (top - m) * c > kGrowth;
+            if (j > 0) {  // the product with the last weights is done
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.o_done[t]), (j - 1) & 1, abort));
+                if (!ok) break;
+                tc_fence_after();
+            }
             if (__any_sync(0xFFFFFFFFu, grow)) {
                 const float m2 = grow ? top : m;
                 const float r = m == -INFINITY ? 0.0f : ex2((m - m2) * c);
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int x = 0; x < DP / 32; ++x) {
                     uint32_t o[32];
                     tmem_ld32(to + x * 32, o);
-                    tmem_wait_ld();
+                    tmem_wait_ld32(o);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
                     tmem_st32(to + x * 32, o);
@@ -391,18 +394,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 add = weights(0, w);
             }
             l += add;
-            tmem_st32(ts, w);
+            tmem_st32(tp, w);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(smem_addr(&ctl.p_ready[t][0]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[t][0]));
             l += weights(1, w);
-            tmem_st32(ts + 32, w);
+            tmem_st32(tp + 32, w);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(smem_addr(&ctl.p_ready[t][1]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[t][1]));
         }
         if (n > 0) {
-            ok = ok && mbar_wait(smem_addr(&ctl.o_full[t]), 0, abort);
+            ok = ok && mbar_wait(smem_addr(&ctl.o_done[t]), (n - 1) & 1, abort);
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
             const bool live = row < len;
@@ -415,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t o[32];
                 if (ok) {
                     tmem_ld32(to + x * 32, o);
-                    tmem_wait_ld();
+                    tmem_wait_ld32(o);
                 }
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
