@@ -60,7 +60,7 @@ struct Shape {
 };
 
 struct Control {
-    uint64_t q_full, kv_full[9], kv_empty[9], s_full[2], s_free[2], p_ready[2][2], o_done[2], drained;
+    uint64_t q_full, kv_full[9], kv_empty[9], s_full[2], s_free[2], p_ready[2], o_done[2], drained;
     uint32_t tmem;
     int abort;
     int begin, len, unit0, units;  // the sequence and its first tile here; how many tiles
@@ -190,8 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_addr(&ctl.s_full[t]), 1);
-            mbar_init(smem_addr(&ctl.p_ready[t][0]), 4);
-            mbar_init(smem_addr(&ctl.p_ready[t][1]), 4);
+            mbar_init(smem_addr(&ctl.p_ready[t]), 4);
             mbar_init(smem_addr(&ctl.s_free[t]), 4);
             mbar_init(smem_addr(&ctl.o_done[t]), 1);
         }
@@ -281,16 +280,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 auto weigh = [&](int t, int j) {
                     const uint32_t v0 = kv_smem + stage(2 * j + 1) * S::kTile;
+                    ok = ok && mbar_wait(smem_addr(&ctl.p_ready[t]), j & 1, abort);
+                    if (!ok) return;
+                    tc_fence_after();
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        ok = ok && mbar_wait(smem_addr(&ctl.p_ready[t][half]), j & 1, abort);
-                        if (!ok) return;
-                        tc_fence_after();
-#pragma unroll
-                        for (int x = half * 4; x < half * 4 + 4; ++x)
-                            mma_ts(tmem + 256 + t * 128, tmem + 128 + t * 64 + x * 8,
-                                   smem_desc(v0 + x * 2048, S::kPanel, 1024), idesc_o, j > 0 || x > 0);
-                    }
+                    for (int x = 0; x < kN / 16; ++x)
+                        mma_ts(tmem + 256 + t * 128, tmem + 128 + t * 64 + x * 8, smem_desc(v0 + x * 2048, S::kPanel, 1024),
+                               idesc_o, j > 0 || x > 0);
                     mma_commit(smem_addr(&ctl.o_done[t]));
                 };
                 ok = ok && loaded(0);
@@ -339,72 +335,60 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int x = 0; x < 128; ++x) s[x] = x <= seen ? s[x] : 0xFF800000u;
             }
-            auto maximum = [&] {
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int x = 0; x < 128; x += 8)
+            for (int x = 0; x < 128; x += 8)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[x + e]), __uint_as_float(s[x + 4 + e])));
-                return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            };
-            // half a row's weights, packed, and their sum
-            float2 sum[2];
-            auto weights = [&](int half, uint32_t (&w)[32]) {
-                const float shift = m == -INFINITY ? 0.0f : -m * c;
-                const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
-                sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    float2 x = fma2_rn(make_float2(__uint_as_float(s[64 * half + 2 * e]),
-                                                   __uint_as_float(s[64 * half + 2 * e + 1])), c2, shift2);
-                    x.x = ex2(x.x), x.y = ex2(x.y);
-                    sum[e & 1] = add2_rn(sum[e & 1], x);
-                    w[e] = f32x2_to_bf16x2_bits(x.x, x.y);
-                }
-                return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            };
-            // The first half is weighed with the maximum of the blocks before,
-            // while this block's is being found; only where that has grown too
-            // much are O and the sum rescaled and the half weighed again.
-            if (j == 0) m = maximum();
-            uint32_t w[32];
-            float add = weights(0, w);
-            const float top = maximum();
+                for (int e = 0; e < 4; ++e)
+                    mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[x + e]), __uint_as_float(s[x + 4 + e])));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             const bool grow = m == -INFINITY ? top > m : (top - m) * c > kGrowth;
-            if (j > 0) {  // the product with the last weights is done
+            auto last_done = [&] {  // the product with the last weights is done
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.o_done[t]), (j - 1) & 1, abort));
-                if (!ok) break;
                 tc_fence_after();
-            }
+            };
             if (__any_sync(0xFFFFFFFFu, grow)) {
                 const float m2 = grow ? top : m;
-                const float r = m == -INFINITY ? 0.0f : ex2((m - m2) * c);
-                m = m2;
-                l *= r;
+                if (j > 0) {
+                    last_done();
+                    if (!ok) break;
+                    const float r = m == -INFINITY ? 0.0f : ex2((m - m2) * c);
+                    l *= r;
 #pragma unroll
-                for (int x = 0; x < DP / 32; ++x) {
-                    uint32_t o[32];
-                    tmem_ld32(to + x * 32, o);
-                    tmem_wait_ld32(o);
+                    for (int x = 0; x < DP / 32; ++x) {
+                        uint32_t o[32];
+                        tmem_ld32(to + x * 32, o);
+                        tmem_wait_ld32(o);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
-                    tmem_st32(to + x * 32, o);
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
+                        tmem_st32(to + x * 32, o);
+                    }
                 }
-                add = weights(0, w);
+                m = m2;
             }
-            l += add;
+            const float shift = m == -INFINITY ? 0.0f : -m * c;
+            const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+            float2 sum[4] = {};
+            uint32_t w[64];
+#pragma unroll
+            for (int e = 0; e < 64; ++e) {
+                float2 x = fma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, shift2);
+                x.x = ex2(x.x), x.y = ex2(x.y);
+                sum[e & 3] = add2_rn(sum[e & 3], x);
+                w[e] = f32x2_to_bf16x2_bits(x.x, x.y);
+            }
+            const float2 add = add2_rn(add2_rn(sum[0], sum[1]), add2_rn(sum[2], sum[3]));
+            l += add.x + add.y;
+            if (j > 0) {
+                last_done();
+                if (!ok) break;
+            }
             tmem_st32(tp, w);
+            tmem_st32(tp + 32, w + 32);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[t][0]));
-            l += weights(1, w);
-            tmem_st32(tp + 32, w);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[t][1]));
+            if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[t]));
         }
         if (n > 0) {
             ok = ok && mbar_wait(smem_addr(&ctl.o_done[t]), (n - 1) & 1, abort);
