@@ -6,20 +6,23 @@
 //
 // A CTA works on two tiles of 128 query rows that share one kv head -- two
 // heads of its group at the same rows, or neighbouring row tiles -- and walks
-// the keys in blocks of 128 that a ring of shared-memory stages holds.  Three
-// warpgroups: one of softmax for each tile (a thread owns a row), and one of
-// which a warp issues the tensor copies and another the products.
+// the keys in blocks of 128 that a ring of shared-memory stages holds; then on
+// the next pair, its copies and first products already under way while the last
+// rows are written.  Three warpgroups: one of softmax for each tile (a thread
+// owns a row), and one of which a warp hands out the pairs, another issues the
+// tensor copies and two the products, each of a tile (one thread for both spent
+// more on its waits than the products took).
 //
 // Tensor memory (512 columns): one S for both tiles, O of each, and the
 // weights of each, rounded to bf16, which are the A operand of the second
 // product.  A block of 128 keys costs a tile 512 clocks of either product and
 // its warpgroup some 1400 clocks of softmax, so the products of a tile must not
-// wait for its softmax: they are issued in the order
+// wait for its softmax: they follow one another as
 //
 //   S0 = q0 k(j+1)^T, O0 += p0 v(j), S1 = q1 k(j+1)^T, O1 += p1 v(j)
 //
 // S is handed over as soon as a warpgroup has it in registers, and each
-// softmax then has 1500 clocks until its weights are asked for.  (With an S
+// softmax then has 1500 clocks until its weights are due.  (With an S
 // for each tile, overwritten by its weights, the next S had to wait for the
 // product with v, and a round of both tiles took 3300 clocks, not 2048.)
 //
@@ -41,7 +44,7 @@ namespace {
 
 constexpr int kM = 128, kN = 128;
 constexpr int kThreads = 384;  // three warpgroups: softmax of each tile, and the issuing warps
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kLoadWarp = 8, kItemWarp = 9, kMmaWarp = 10;  // products: a warp for each tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrowth = 8.0f;  // a maximum may lag this many powers of two
 
@@ -51,27 +54,39 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Pair `index` of the tiles that share a kv head, counted from the last
+// sequence's last pair (the ones with the most keys first): a sequence of r row
+// tiles has r * group tiles, tile u being head u % group of the group at rows
+// (u / group) * kM.
+struct Pair {
+    int begin, len, unit, units;  // units 0: no such pair
+};
+
+// What the scheduling warp hands out; units < 0: nothing more.
+struct Item {
+    Pair p;
+    int kvh;
+};
+constexpr int kItems = 4, kReaders = 11;  // items in hand; warps that read one: softmax, loads, products
+
+struct Control {
+    uint64_t q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], s_free[2], p_ready[2], o_done[2], o_free[2];
+    uint64_t drained[2];
+    uint64_t item_full[kItems], item_empty[kItems];
+    Item item[kItems];
+    uint32_t tmem;
+    int abort;
+};
+
 template <int DP>
 struct Shape {
     static constexpr int kPanel = 128 * 128;              // 128 rows of 64 bf16
     static constexpr int kTile = kPanel * (DP / 64);      // 128 rows of DP
-    static constexpr int kStages = DP == 128 ? 5 : 9;
-    static constexpr int kBytes = kTile * (2 + kStages) + 1024 + 512;
+    static constexpr int kStages = DP == 128 ? 4 : 8;
+    static constexpr int kOut = 8 * 32 * 128;             // 32 rows of 64 entries for each softmax warp
+    static constexpr int kBytes = kTile * (2 + kStages) + kOut + 1024 + (int)sizeof(Control);
 };
 
-struct Control {
-    uint64_t q_full, kv_full[9], kv_empty[9], s_full[2], s_free[2], p_ready[2], o_done[2], drained;
-    uint32_t tmem;
-    int abort;
-    int begin, len, unit0, units;  // the sequence and its first tile here; how many tiles
-};
-
-// Pair `index` of the tiles that share a kv head, counted from the last
-// sequence's last pair: a sequence of r row tiles has r * group tiles, tile u
-// being head u % group of the group at rows (u / group) * kM.
-struct Pair {
-    int begin, len, unit, units;  // units 0: no such pair
-};
 __device__ __forceinline__ Pair find_pair(const int32_t* starts, int n_seqs, int T, int group, uint32_t index) {
     const int lane = threadIdx.x & 31;
     uint32_t before = 0;
@@ -110,6 +125,8 @@ __device__ __forceinline__ Pair find_pair(const int32_t* starts, int n_seqs, int
 // a lane a key for the logits, a lane four entries for the output.
 __device__ __noinline__ void exact_row(const PromptArgs& a, int begin, int row, int head) {
     const int lane = threadIdx.x & 31, D = (int)a.D, kvh = head / (int)(a.Hq / a.Hkv);
+    const uint16_t* const k = static_cast<const uint16_t*>(a.k) + (int64_t)kvh * D;
+    const uint16_t* const v = static_cast<const uint16_t*>(a.v) + (int64_t)kvh * D;
     const float c = a.scale * kLog2e;
     float q[4], o[4] = {};
 #pragma unroll
@@ -124,9 +141,7 @@ __device__ __noinline__ void exact_row(const PromptArgs& a, int begin, int row, 
         float s = 0.0f;
         for (int d = 0; d < D; d += 4) {
             uint2 w = make_uint2(0, 0);
-            if (seen)
-                w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.k) + (begin + (int64_t)j) * a.k_stride +
-                                                    (int64_t)kvh * D + d);
+            if (seen) w = *reinterpret_cast<const uint2*>(k + (begin + (int64_t)j) * a.k_stride + d);
             s = fmaf(__shfl_sync(0xFFFFFFFFu, q[0], d >> 2), __uint_as_float(w.x << 16), s);
             s = fmaf(__shfl_sync(0xFFFFFFFFu, q[1], d >> 2), __uint_as_float(w.x & 0xFFFF0000u), s);
             s = fmaf(__shfl_sync(0xFFFFFFFFu, q[2], d >> 2), __uint_as_float(w.y << 16), s);
@@ -150,13 +165,11 @@ __device__ __noinline__ void exact_row(const PromptArgs& a, int begin, int row, 
         for (int t = 0; t < keys; ++t) {
             const float w = __shfl_sync(0xFFFFFFFFu, p, t);
             if (lane * 4 < D) {
-                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.v) +
-                                                                (begin + (int64_t)k0 + t) * a.v_stride + (int64_t)kvh * D +
-                                                                lane * 4);
-                o[0] = fmaf(w, __uint_as_float(v.x << 16), o[0]);
-                o[1] = fmaf(w, __uint_as_float(v.x & 0xFFFF0000u), o[1]);
-                o[2] = fmaf(w, __uint_as_float(v.y << 16), o[2]);
-                o[3] = fmaf(w, __uint_as_float(v.y & 0xFFFF0000u), o[3]);
+                const uint2 x = *reinterpret_cast<const uint2*>(v + (begin + (int64_t)k0 + t) * a.v_stride + lane * 4);
+                o[0] = fmaf(w, __uint_as_float(x.x << 16), o[0]);
+                o[1] = fmaf(w, __uint_as_float(x.x & 0xFFFF0000u), o[1]);
+                o[2] = fmaf(w, __uint_as_float(x.y << 16), o[2]);
+                o[3] = fmaf(w, __uint_as_float(x.y & 0xFFFF0000u), o[3]);
             }
         }
     }
@@ -167,34 +180,46 @@ __device__ __noinline__ void exact_row(const PromptArgs& a, int begin, int row, 
                                  m == -INFINITY ? 0.0f : o[e] / l);
 }
 
+// Work item `round` of this CTA: rounds go back and forth over the CTAs, so that
+// no CTA always gets the larger one.
+__device__ __forceinline__ uint32_t item_of(int round) {
+    return (uint32_t)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-              const __grid_constant__ CUtensorMap mv, PromptArgs a) {
+              const __grid_constant__ CUtensorMap mv, PromptArgs a, uint32_t n_items) {
     using S = Shape<DP>;
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
-    Control& ctl = *reinterpret_cast<Control*>(raw + (base - smem_addr(raw)) + S::kTile * (2 + S::kStages));
+    Control& ctl = *reinterpret_cast<Control*>(raw + (base - smem_addr(raw)) + S::kTile * (2 + S::kStages) + S::kOut);
     const uint32_t q_smem = base, kv_smem = base + 2 * S::kTile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = (int)(a.Hq / a.Hkv);
-    const int kvh = (int)(blockIdx.x % (unsigned)a.Hkv);
     volatile int* const abort = &ctl.abort;
 
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&ctl.tmem), 512);
     if (threadIdx.x == 0) {
         mbar_init(smem_addr(&ctl.q_full), 1);
+        mbar_init(smem_addr(&ctl.q_empty), 2);
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(smem_addr(&ctl.kv_full[i]), 1);
-            mbar_init(smem_addr(&ctl.kv_empty[i]), 1);
+            mbar_init(smem_addr(&ctl.kv_empty[i]), 2);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_addr(&ctl.s_full[t]), 1);
             mbar_init(smem_addr(&ctl.p_ready[t]), 4);
             mbar_init(smem_addr(&ctl.s_free[t]), 4);
             mbar_init(smem_addr(&ctl.o_done[t]), 1);
+            mbar_init(smem_addr(&ctl.o_free[t]), 4);
         }
-        mbar_init(smem_addr(&ctl.drained), 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(smem_addr(&ctl.item_full[i]), 1);
+            mbar_init(smem_addr(&ctl.item_empty[i]), kReaders);
+        }
+        mbar_init(smem_addr(&ctl.drained[0]), 1);
+        mbar_init(smem_addr(&ctl.drained[1]), 1);
         ctl.abort = 0;
         mbar_init_fence();
         tma_prefetch(&mq);
@@ -202,231 +227,348 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch(&mv);
     }
     pdl_begin();
-    if (warp == 0) {
-        const Pair p = find_pair(a.starts, (int)a.n_seqs, (int)a.T, group, blockIdx.x / (unsigned)a.Hkv);
-        if (lane == 0) ctl.begin = p.begin, ctl.len = p.len, ctl.unit0 = p.unit, ctl.units = p.units;
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
-    const int begin = ctl.begin, len = ctl.len, units = ctl.units;
-    // tile t: head and first row, and the blocks of keys up to its diagonal
-    int head[2], row0[2], blocks[2];
+
+    // Item i as its readers see it: tile t's head, first row and blocks of
+    // keys up to its diagonal.
+    struct Work {
+        int begin, len, kvh, units, most;
+        int head[2], row0[2], blocks[2];
+    };
+    auto as_work = [&](const Item& it) {
+        Work w;
+        w.begin = it.p.begin, w.len = it.p.len, w.kvh = it.kvh, w.units = it.p.units;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int u = ctl.unit0 + t;
-        head[t] = kvh * group + u % group;
-        row0[t] = u / group * kM;
-        blocks[t] = t < units ? u / group + 1 : 0;
-    }
-    const int most = max(blocks[0], blocks[1]);
+        for (int t = 0; t < 2; ++t) {
+            const int u = it.p.unit + t;
+            w.head[t] = it.kvh * group + u % group;
+            w.row0[t] = u / group * kM;
+            w.blocks[t] = t < w.units ? u / group + 1 : 0;
+        }
+        w.most = max(w.blocks[0], w.blocks[1]);
+        return w;
+    };
+    // false: a wait gave up
+    auto item_ready = [&](int i) { return mbar_wait(smem_addr(&ctl.item_full[i % kItems]), i / kItems & 1, abort); };
+    auto item_read = [&](int i) { mbar_arrive(smem_addr(&ctl.item_empty[i % kItems])); };
 
     // Registers: 384 threads were launched with 168 each (64512); the softmax
     // warpgroups take 208, the issuing one keeps 80 (63488 in all).
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        if (warp == kLoadWarp) {
-            if (units > 0 && elect_one()) {
-                const uint32_t qb = smem_addr(&ctl.q_full);
-                mbar_arrive_tx(qb, S::kTile * units);
-                for (int t = 0; t < units; ++t)
+        if (warp == kItemWarp) {
+            bool ok = true;
+            int i = 0;
+            for (int round = 0; ok; ++round) {
+                const uint32_t id = item_of(round);
+                const bool end = (uint64_t)round * gridDim.x >= n_items;
+                Item it = {{0, 0, 0, -1}, 0};
+                if (!end) {
+                    if (id >= n_items) continue;
+                    it.kvh = (int)(id % (uint32_t)a.Hkv);
+                    it.p = find_pair(a.starts, (int)a.n_seqs, (int)a.T, group, id / (uint32_t)a.Hkv);
+                    if (it.p.units == 0) continue;
+                }
+                ok = __all_sync(0xFFFFFFFFu,
+                                mbar_wait(smem_addr(&ctl.item_empty[i % kItems]), (i / kItems & 1) ^ 1, abort));
+                if (!ok) break;
+                if (lane == 0) {
+                    ctl.item[i % kItems] = it;
+                    mbar_arrive(smem_addr(&ctl.item_full[i % kItems]));
+                }
+                ++i;
+                if (end) break;
+            }
+        } else if (warp == kLoadWarp) {
+            if (elect_one()) {
+                int g = 0, items = 0;  // loads of the ring and items so far
+                bool ok = true;
+                for (int i = 0; ok; ++i) {
+                    if (!(ok = item_ready(i))) break;
+                    const Work w = as_work(ctl.item[i % kItems]);
+                    item_read(i);
+                    if (w.units < 0) break;
+                    for (int x = 0; ok && x < 2 * w.most; ++x) {  // k and v of each block in turn
+                        const int stage = g % S::kStages;
+                        ok = mbar_wait(smem_addr(&ctl.kv_empty[stage]), (g / S::kStages & 1) ^ 1, abort);
+                        if (!ok) break;
+                        const uint32_t full = smem_addr(&ctl.kv_full[stage]);
+                        mbar_arrive_tx(full, S::kTile);
 #pragma unroll
-                    for (int p = 0; p < DP / 64; ++p)
-                        tma_load_3d(q_smem + t * S::kTile + p * S::kPanel, &mq, qb, p * 64, head[t], begin + row0[t]);
-                int stage = 0, phase = 0, issued = 0;
-                for (int i = 0; i < 2 * most; ++i) {  // k and v of each block in turn
-                    if (!mbar_wait(smem_addr(&ctl.kv_empty[stage]), phase ^ 1, abort)) break;
-                    const uint32_t full = smem_addr(&ctl.kv_full[stage]);
-                    mbar_arrive_tx(full, S::kTile);
+                        for (int p = 0; p < DP / 64; ++p)
+                            tma_load_3d(kv_smem + stage * S::kTile + p * S::kPanel, (x & 1) ? &mv : &mk, full, p * 64,
+                                        w.kvh, w.begin + (x >> 1) * kN);
+                        ++g;
+                        if (x == 0) {  // q, once the last item's is done with
+                            ok = mbar_wait(smem_addr(&ctl.q_empty), (i & 1) ^ 1, abort);
+                            if (!ok) break;
+                            const uint32_t qb = smem_addr(&ctl.q_full);
+                            mbar_arrive_tx(qb, S::kTile * w.units);
+                            for (int t = 0; t < w.units; ++t)
 #pragma unroll
-                    for (int p = 0; p < DP / 64; ++p)
-                        tma_load_3d(kv_smem + stage * S::kTile + p * S::kPanel, (i & 1) ? &mv : &mk, full, p * 64, kvh,
-                                    begin + (i >> 1) * kN);
-                    ++issued;
-                    if (++stage == S::kStages) stage = 0, phase ^= 1;
+                                for (int p = 0; p < DP / 64; ++p)
+                                    tma_load_3d(q_smem + t * S::kTile + p * S::kPanel, &mq, qb, p * 64, w.head[t],
+                                                w.begin + w.row0[t]);
+                            ++items;
+                        }
+                    }
                 }
                 if (*abort) {  // nothing may still be on its way when the CTA ends
                     int none = 0;
-                    mbar_wait(qb, 0, &none);
-                    for (int i = max(0, issued - S::kStages); i < issued; ++i)
-                        mbar_wait(smem_addr(&ctl.kv_full[i % S::kStages]), (i / S::kStages) & 1, &none);
+                    if (items > 0) mbar_wait(smem_addr(&ctl.q_full), (items - 1) & 1, &none);
+                    for (int x = max(0, g - S::kStages); x < g; ++x)
+                        mbar_wait(smem_addr(&ctl.kv_full[x % S::kStages]), x / S::kStages & 1, &none);
                 }
             }
-        } else if (warp == kMmaWarp) {
-            if (units > 0 && elect_one()) {
-                const uint32_t idesc_s = bf16_idesc(kM, kN, false) | (a.scale < 0.0f ? 1u << 13 : 0u);
-                constexpr uint32_t idesc_o = bf16_idesc(kM, DP, true);
-                bool ok = mbar_wait(smem_addr(&ctl.q_full), 0, abort);
-                // load i (k of block i / 2, or v) lies in stage i % kStages
-                auto stage = [](int i) { return i % S::kStages; };
-                auto loaded = [&](int i) {
-                    return mbar_wait(smem_addr(&ctl.kv_full[stage(i)]), i / S::kStages & 1, abort);
+        } else if (elect_one()) {
+            const int t = warp - kMmaWarp;
+            const uint32_t idesc_s = bf16_idesc(kM, kN, false) | (a.scale < 0.0f ? 1u << 13 : 0u);
+            constexpr uint32_t idesc_o = bf16_idesc(kM, DP, true), hi = smem_desc_hi(1024);
+            const uint32_t q_lo = smem_desc_lo(q_smem + t * S::kTile, 16), k_lo = smem_desc_lo(kv_smem, 16);
+            const uint32_t v_lo = smem_desc_lo(kv_smem, S::kPanel);
+            const uint32_t o = tmem + 256 + t * 128, pw = tmem + 128 + t * 64;
+            bool ok = true;
+            int g = 0;              // the ring's loads before this item: k of block j is load g + 2 j
+            int done[2] = {0, 0};   // blocks of each tile before this item
+            int items = 0;          // items with a tile t
+            int last_t = -1;        // the tile that S was last written for in the item before
+            for (int i = 0; ok; ++i) {
+                if (!(ok = item_ready(i))) break;
+                const Work w = as_work(ctl.item[i % kItems]);
+                item_read(i);
+                if (w.units < 0) break;
+                const int mine = w.blocks[t], theirs = w.blocks[t ^ 1];
+                auto loaded = [&](int x) {
+                    ok = ok && mbar_wait(smem_addr(&ctl.kv_full[x % S::kStages]), x / S::kStages & 1, abort);
                 };
-                auto release = [&](int i) { mma_commit(smem_addr(&ctl.kv_empty[stage(i)])); };
-                int last_t = -1, last_j = 0;  // the tile and block that S was last written for
-                auto scores = [&](int t, int j) {
-                    if (last_t >= 0) ok = ok && mbar_wait(smem_addr(&ctl.s_free[last_t]), last_j & 1, abort);
+                // S is free once the block before in the order (0, j), (1, j), (0, j + 1), ... has been read
+                auto s_free = [&](int j) {
+                    int pt, pj;
+                    if (t == 1) {
+                        pt = j < theirs ? 0 : 1, pj = j < theirs ? j : j - 1;
+                    } else {
+                        pt = j - 1 < theirs ? 1 : 0, pj = j - 1;
+                    }
+                    if (pj < 0) pt = last_t;
+                    if (pt >= 0)
+                        ok = ok && mbar_wait(smem_addr(&ctl.s_free[pt]), (done[pt] + pj) & 1, abort);
+                };
+                auto scores = [&](int j) {
+                    loaded(g + 2 * j);
+                    s_free(j);
                     if (!ok) return;
-                    last_t = t, last_j = j;
                     tc_fence_after();
-                    const uint32_t q0 = q_smem + t * S::kTile, k0 = kv_smem + stage(2 * j) * S::kTile;
+                    const int stage = (g + 2 * j) % S::kStages;
+                    const uint32_t k0 = k_lo + stage * (S::kTile >> 4);
 #pragma unroll
                     for (int x = 0; x < DP / 16; ++x) {
-                        const uint32_t off = (x / 4) * S::kPanel + (x % 4) * 32;
-                        mma_ss(tmem, smem_desc(q0 + off, 16, 1024), smem_desc(k0 + off, 16, 1024), idesc_s, x > 0);
+                        const uint32_t off = ((x / 4) * S::kPanel + (x % 4) * 32) >> 4;
+                        mma_ss(tmem, q_lo + off, hi, k0 + off, hi, idesc_s, x > 0);
                     }
                     mma_commit(smem_addr(&ctl.s_full[t]));
+                    mma_commit(smem_addr(&ctl.kv_empty[stage]));
+                    if (j + 1 == mine) mma_commit(smem_addr(&ctl.q_empty));
                 };
-                auto weigh = [&](int t, int j) {
-                    const uint32_t v0 = kv_smem + stage(2 * j + 1) * S::kTile;
-                    ok = ok && mbar_wait(smem_addr(&ctl.p_ready[t]), j & 1, abort);
-                    if (!ok) return;
+                ok = mbar_wait(smem_addr(&ctl.q_full), i & 1, abort);
+                if (mine > 0)
+                    scores(0);
+                else
+                    mbar_arrive(smem_addr(&ctl.q_empty));
+                for (int j = 0; ok && j < mine; ++j) {
+                    if (j + 1 < mine) scores(j + 1);
+                    loaded(g + 2 * j + 1);
+                    ok = ok && mbar_wait(smem_addr(&ctl.p_ready[t]), (done[t] + j) & 1, abort);
+                    // O has been read for the last item
+                    if (j == 0 && items > 0)
+                        ok = ok && mbar_wait(smem_addr(&ctl.o_free[t]), (items - 1) & 1, abort);
+                    if (!ok) break;
                     tc_fence_after();
+                    const int stage = (g + 2 * j + 1) % S::kStages;
+                    const uint32_t v0 = v_lo + stage * (S::kTile >> 4);
 #pragma unroll
                     for (int x = 0; x < kN / 16; ++x)
-                        mma_ts(tmem + 256 + t * 128, tmem + 128 + t * 64 + x * 8, smem_desc(v0 + x * 2048, S::kPanel, 1024),
-                               idesc_o, j > 0 || x > 0);
+                        mma_ts(o, pw + x * 8, v0 + x * (2048 >> 4), hi, idesc_o, j > 0 || x > 0);
                     mma_commit(smem_addr(&ctl.o_done[t]));
-                };
-                ok = ok && loaded(0);
-                for (int t = 0; t < 2; ++t)
-                    if (ok && blocks[t] > 0) scores(t, 0);
-                if (ok) release(0);
-                for (int j = 0; ok && j < most; ++j) {
-                    if (j + 1 < most) ok = loaded(2 * j + 2);
-                    for (int t = 0; t < 2; ++t) {
-                        if (ok && j + 1 < blocks[t]) scores(t, j + 1);
-                        if (t == 0) ok = ok && loaded(2 * j + 1);
-                        if (t == 1 && ok && j + 1 < most) release(2 * j + 2);
-                        if (ok && j < blocks[t]) weigh(t, j);
-                    }
-                    if (ok) release(2 * j + 1);
+                    mma_commit(smem_addr(&ctl.kv_empty[stage]));
                 }
-                // every product is done before tensor memory is given back
-                mma_commit(smem_addr(&ctl.drained));
-                int none = 0;
-                mbar_wait(smem_addr(&ctl.drained), 0, &none);
+                // blocks that only the other tile works on
+                for (int x = 2 * mine; ok && x < 2 * w.most; ++x) {
+                    loaded(g + x);
+                    if (ok) mbar_arrive(smem_addr(&ctl.kv_empty[(g + x) % S::kStages]));
+                }
+                g += 2 * w.most;
+                done[0] += w.blocks[0], done[1] += w.blocks[1];
+                items += mine > 0;
+                last_t = w.blocks[1] > 0 ? 1 : 0;
             }
+            // every product is done before tensor memory is given back
+            mma_commit(smem_addr(&ctl.drained[t]));
+            int none = 0;
+            mbar_wait(smem_addr(&ctl.drained[t]), 0, &none);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = warp >> 2;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
         const uint32_t ts = tmem + lanes, tp = tmem + 128 + t * 64 + lanes, to = tmem + 256 + t * 128 + lanes;
-        const int n = blocks[t], row = row0[t] + (threadIdx.x & 127);
         const float c = fabsf(a.scale) * kLog2e;
-        float m = -INFINITY, l = 0.0f;
+        uint8_t* const stage = raw + (base - smem_addr(raw)) + S::kTile * (2 + S::kStages) + warp * (S::kOut / 8);
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.s_full[t]), j & 1, abort));
+        int done = 0;  // blocks of this tile before this item
+        for (int i = 0; ok; ++i) {
+            ok = __all_sync(0xFFFFFFFFu, item_ready(i));
             if (!ok) break;
-            tc_fence_after();
-            uint32_t s[128];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) tmem_ld32(ts + x * 32, s + x * 32);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) tmem_wait_ld32(s + x * 32);
-            tc_fence_before();
+            const Item it = ctl.item[i % kItems];
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&ctl.s_free[t]));
-            if (j == n - 1) {  // the diagonal
-                const int seen = row - j * kN;
-#pragma unroll
-                for (int x = 0; x < 128; ++x) s[x] = x <= seen ? s[x] : 0xFF800000u;
-            }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int x = 0; x < 128; x += 8)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[x + e]), __uint_as_float(s[x + 4 + e])));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const bool grow = m == -INFINITY ? top > m : (top - m) * c > kGrowth;
-            auto last_done = [&] {  // the product with the last weights is done
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.o_done[t]), (j - 1) & 1, abort));
+            if (lane == 0) item_read(i);
+            if (it.p.units < 0) break;
+            if (t >= it.p.units) continue;
+            const int u = it.p.unit + t, n = u / group + 1;
+            const int row = u / group * kM + (threadIdx.x & 127);
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < n; ++j) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.s_full[t]), (done + j) & 1, abort));
+                if (!ok) break;
                 tc_fence_after();
-            };
-            if (__any_sync(0xFFFFFFFFu, grow)) {
-                const float m2 = grow ? top : m;
+                uint32_t s[128];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) tmem_ld32(ts + x * 32, s + x * 32);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) tmem_wait_ld32(s + x * 32);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ctl.s_free[t]));
+                if (j == n - 1) {  // the diagonal
+                    const int seen = row - j * kN;
+#pragma unroll
+                    for (int x = 0; x < 128; ++x) s[x] = x <= seen ? s[x] : 0xFF800000u;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int x = 0; x < 128; x += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[x + e]), __uint_as_float(s[x + 4 + e])));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const bool grow = m == -INFINITY ? top > m : (top - m) * c > kGrowth;
+                auto last_done = [&] {  // the product with the last weights is done
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.o_done[t]), (done + j - 1) & 1, abort));
+                    tc_fence_after();
+                };
+                if (__any_sync(0xFFFFFFFFu, grow)) {
+                    const float m2 = grow ? top : m;
+                    if (j > 0) {
+                        last_done();
+                        if (!ok) break;
+                        const float r = m == -INFINITY ? 0.0f : ex2((m - m2) * c);
+                        l *= r;
+#pragma unroll
+                        for (int x = 0; x < DP / 32; ++x) {
+                            uint32_t o[32];
+                            tmem_ld32(to + x * 32, o);
+                            tmem_wait_ld32(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
+                            tmem_st32(to + x * 32, o);
+                        }
+                    }
+                    m = m2;
+                }
+                const float shift = m == -INFINITY ? 0.0f : -m * c;
+                const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+                float2 sum[4] = {};
+                uint32_t w[64];
+#pragma unroll
+                for (int e = 0; e < 64; ++e) {
+                    float2 x = fma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2,
+                                       shift2);
+                    x.x = ex2(x.x), x.y = ex2(x.y);
+                    sum[e & 3] = add2_rn(sum[e & 3], x);
+                    w[e] = f32x2_to_bf16x2_bits(x.x, x.y);
+                }
+                const float2 add = add2_rn(add2_rn(sum[0], sum[1]), add2_rn(sum[2], sum[3]));
+                l += add.x + add.y;
                 if (j > 0) {
                     last_done();
                     if (!ok) break;
-                    const float r = m == -INFINITY ? 0.0f : ex2((m - m2) * c);
-                    l *= r;
-#pragma unroll
-                    for (int x = 0; x < DP / 32; ++x) {
-                        uint32_t o[32];
-                        tmem_ld32(to + x * 32, o);
-                        tmem_wait_ld32(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
-                        tmem_st32(to + x * 32, o);
-                    }
                 }
-                m = m2;
+                tmem_st32(tp, w);
+                tmem_st32(tp + 32, w + 32);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[t]));
             }
-            const float shift = m == -INFINITY ? 0.0f : -m * c;
-            const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
-            float2 sum[4] = {};
-            uint32_t w[64];
-#pragma unroll
-            for (int e = 0; e < 64; ++e) {
-                float2 x = fma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, shift2);
-                x.x = ex2(x.x), x.y = ex2(x.y);
-                sum[e & 3] = add2_rn(sum[e & 3], x);
-                w[e] = f32x2_to_bf16x2_bits(x.x, x.y);
-            }
-            const float2 add = add2_rn(add2_rn(sum[0], sum[1]), add2_rn(sum[2], sum[3]));
-            l += add.x + add.y;
-            if (j > 0) {
-                last_done();
-                if (!ok) break;
-            }
-            tmem_st32(tp, w);
-            tmem_st32(tp + 32, w + 32);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[t]));
-        }
-        if (n > 0) {
-            ok = ok && mbar_wait(smem_addr(&ctl.o_done[t]), (n - 1) & 1, abort);
+            done += n;
+            ok = ok && mbar_wait(smem_addr(&ctl.o_done[t]), (done - 1) & 1, abort);
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
-            const bool live = row < len;
+            const int head = it.kvh * group + u % group;
+            const bool live = row < it.p.len;
             const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
-            uint16_t* const out = static_cast<uint16_t*>(a.out) + (begin + (int64_t)row) * a.out_stride +
-                                  (int64_t)head[t] * a.D;
-            uint32_t bad = 0;
+            const int row0 = u / group * kM + (warp & 3) * 32;
+            uint16_t* const out = static_cast<uint16_t*>(a.out) + (it.p.begin + (int64_t)row0) * a.out_stride +
+                                  (int64_t)head * a.D;
+            bool bad = false;
+            // 64 entries of the warp's rows at a time by way of shared memory, so
+            // that a store covers 128 bytes of each of four rows (a thread storing
+            // its own row took 5200 clocks a tile)
 #pragma unroll
-            for (int x = 0; x < DP / 32; ++x) {
-                uint32_t o[32];
+            for (int x = 0; x < DP / 64; ++x) {
+                uint32_t o[64] = {};
                 if (ok) {
-                    tmem_ld32(to + x * 32, o);
+                    tmem_ld32(to + x * 64, o);
+                    tmem_ld32(to + x * 64 + 32, o + 32);
                     tmem_wait_ld32(o);
+                    tmem_wait_ld32(o + 32);
+                    if (x == DP / 64 - 1) {  // the next item may have O
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&ctl.o_free[t]));
+                    }
                 }
+                __syncwarp();
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
+                for (int e = 0; e < 8; ++e) {
                     float f[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int y = 0; y < 8; ++y) {
                         // a wait that gave up leaves NaN
-                        f[i] = ok ? __uint_as_float(o[e + i]) * inv : __uint_as_float(0x7FC00000u);
-                        if (!(fabsf(f[i]) <= 3.402823466e38f)) bad = 1;
+                        f[y] = ok ? __uint_as_float(o[e * 8 + y]) * inv : __uint_as_float(0x7FC00000u);
+                        bad = bad || !(fabsf(f[y]) <= 3.402823466e38f);
                     }
-                    if (live && x * 32 + e < a.D)
-                        *reinterpret_cast<Vec16*>(out + x * 32 + e) = Store<kBF16>::pack(f);
+                    *reinterpret_cast<Vec16*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = Store<kBF16>::pack(f);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int r = e * 4 + (lane >> 3), piece = lane & 7, d = x * 64 + piece * 8;
+                    const Vec16 v = *reinterpret_cast<const Vec16*>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
+                    if (row0 + r < it.p.len && d < a.D) *reinterpret_cast<Vec16*>(out + r * a.out_stride + d) = v;
                 }
             }
             // rows that are not finite again, from their own keys alone
             uint32_t again = __ballot_sync(0xFFFFFFFFu, ok && live && bad);
             __syncwarp();
             while (again) {
-                const int i = __ffs((int)again) - 1;
+                const int r = __ffs((int)again) - 1;
                 again &= again - 1;
-                exact_row(a, begin, row0[t] + (warp & 3) * 32 + i, head[t]);
+                exact_row(a, it.p.begin, row0 + r, head);
             }
+        }
+        // a wait that gave up: NaN in every row of this CTA's tiles, done or not
+        for (int round = 0; !ok && (uint64_t)round * gridDim.x < n_items; ++round) {
+            const uint32_t id = item_of(round);
+            if (id >= n_items) continue;
+            const Pair p = find_pair(a.starts, (int)a.n_seqs, (int)a.T, group, id / (uint32_t)a.Hkv);
+            const int u = p.unit + t, row = u / group * kM + (threadIdx.x & 127);
+            if (t >= p.units || row >= p.len) continue;
+            uint16_t* const out = static_cast<uint16_t*>(a.out) + (p.begin + (int64_t)row) * a.out_stride +
+                                  ((int64_t)(id % (uint32_t)a.Hkv) * group + u % group) * a.D;
+            for (int d = 0; d < a.D; ++d) out[d] = 0x7FC0;
         }
     }
     tc_fence_before();
@@ -435,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tmem_free(tmem, 512);
 }
 
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeFn encode_fn() {
@@ -478,7 +620,9 @@ cudaError_t go(const PromptArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int64_t group = a.Hq / a.Hkv, seqs = a.n_seqs < a.T ? a.n_seqs : a.T;
     const int64_t pairs = ((a.T / kM + seqs) * group + (group & 1 ? seqs : 0)) / 2;
-    return launch(prompt_tc<DP>, dim3((unsigned)(pairs * a.Hkv)), dim3(kThreads), smem, st, mq, mk, mv, a);
+    const int64_t items = pairs * a.Hkv, sms = sm_count();
+    return launch(prompt_tc<DP>, dim3((unsigned)(items < sms ? items : sms)), dim3(kThreads), smem, st, mq, mk, mv, a,
+                  (uint32_t)items);
 }
 
 }  // namespace

@@ -33,7 +33,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Waits for the phase of this parity to complete; gives up after two seconds,
+// Waits for the phase of this parity to complete; gives up after ten seconds,
 // or when another thread of the CTA has (*abort), so that no wait is without
 // an end.  Returns whether the phase completed.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
@@ -45,7 +45,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
             if (*abort) return false;
             asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
             if (t0 == 0) t0 = t;
-            if (t - t0 > 2000000000ull) {
+            if (t - t0 > 10000000000ull) {
                 *abort = 1;
                 return false;
             }
@@ -123,29 +123,32 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
 
 // ---- products ------------------------------------------------------------------------
 
-// Descriptor of a shared-memory operand in the 128-byte swizzle: the start
-// address, the two strides (bytes), version 1.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading, uint32_t stride) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Descriptor of a shared-memory operand in the 128-byte swizzle, as its two
+// words: the start address and the leading stride (bytes) in the low one, the
+// other stride, version 1 and the swizzle in the high one.  A start `off` bytes
+// further on is the low word plus off / 16.
+__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t addr, uint32_t leading) {
+    return (addr & 0x3FFFFu) >> 4 | leading >> 4 << 16;
 }
+constexpr uint32_t smem_desc_hi(uint32_t stride) { return stride >> 4 | 1u << 14 | 2u << 29; }
 // Instruction descriptor of kind::f16 with bf16 operands and f32 sums; A and B
 // K-major unless b_mn; negate: A's sign flipped.
 constexpr uint32_t bf16_idesc(int M, int N, bool b_mn, bool negate = false) {
     return 1u << 4 | 1u << 7 | 1u << 10 | (negate ? 1u << 13 : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t)(N / 8) << 17 |
            (uint32_t)(M / 16) << 24;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-                 "r"((uint32_t)add)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+                 "setp.ne.u32 p, %6, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+                 "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
                  : "memory");
 }
 // A from tensor memory.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-                 "r"((uint32_t)add)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b_lo),
+                 "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
                  : "memory");
 }
 // The mbarrier is arrived at when every product issued so far by this thread is done.
