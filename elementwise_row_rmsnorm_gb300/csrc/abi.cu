@@ -812,7 +812,7 @@ int gbe_attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_st
     if (n_seqs < 0 || n_seqs > (1 << 24) || T < 0 || T > (1 << 28) || Hkv < 1 || Hq < Hkv || Hq > 65536 || Hq % Hkv)
         return GBE_ERR_SHAPE;
     if (D < 8 || D > 256 || D % 8) return GBE_ERR_SHAPE;
-    if (T / 64 + n_seqs > INT32_MAX / Hq) return GBE_ERR_SHAPE;
+    if (T / 32 + n_seqs > INT32_MAX / Hq) return GBE_ERR_SHAPE;
     if (rows_form(T, Hq, D, q_stride, es) || rows_form(T, Hkv, D, k_stride, es) ||
         rows_form(T, Hkv, D, v_stride, es) || rows_form(T, Hq, D, out_stride, es))
         return GBE_ERR_SHAPE;
@@ -837,6 +837,8 @@ int gbe_attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_st
         if ((st = chk.check(b)) != GBE_OK) return st;
     bool vec = true;
     for (const Rows& x : r) vec = vec && aligned16(x.p) && x.stride % 16 == 0;
+    // (with more than one row a stride is bounded by its buffer's extent, checked above)
+    if (T == 1) q_stride = out_stride = Hq * D, k_stride = v_stride = Hkv * D;
     const gbe::PromptArgs a = {q, k, v, out, q_stride, k_stride, v_stride, out_stride, starts, n_seqs, T, Hq, Hkv, D,
                                scale};
     return finish(gbe::launch_attn_prompt(a, dtype, vec, as_stream(stream)));

@@ -1,14 +1,19 @@
-// attn_prompt.cu -- causal attention over packed prompts with grouped heads,
-// on the CUDA cores: f32 storage, and any alignment.
+// attn_prompt.cu -- causal attention over packed prompts with grouped heads:
+// f32 storage, and what attn_prompt_tc.cu does not take.
 //
 //   out[i, h] = sum_j p_ij v_j,  p_i = softmax_j(scale * q[i, h] . k_j),
 //   j <= i within i's sequence, k and v of kv head h / (Hq / Hkv)
 //
-// One CTA takes 64 query rows of one head and walks the keys in tiles of 64
-// with the running maximum and sum of the softmax (base 2: scale * log2(e)
-// is folded into q).  Sixteen by sixteen threads: a thread holds a 4 x 4
-// piece of the logits and a 4 x D/16 piece of the output in registers; q, k,
-// v and the weights are staged in shared memory as f32.
+// On the CUDA cores, in f32 throughout.  (Three tf32 products in place of one,
+// on the tensor cores, came out 6 times as far from the definition as f32 sums
+// and were not kept.)  One CTA takes 32 query rows of one head and walks the
+// keys in tiles of 64 with the running maximum and sum of the softmax (base 2:
+// scale * log2(e) is folded into q).  Eight by sixteen threads: a thread holds a
+// 4 x 4 piece of the logits and a 4 x D/16 piece of the output in registers, two
+// multiply-adds an instruction; q, k, v and the weights lie in shared memory as
+// f32.  f32 rows on the 16-byte grid come by asynchronous copies, v while the
+// logits are formed and the next k while the output is.  Bound by the rate of
+// f32 multiply-adds (78 TFLOP/s) where there are tiles enough.
 #include <type_traits>
 
 #include "attn_tiles.cuh"
@@ -19,22 +24,14 @@
 namespace gbe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kM = 64, kN = 64;
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// 64 rows into shared memory as f32, times `scale`; zeros behind `rows` and D.
-template <int DT, int DP, bool VEC>
+constexpr int kThreads = 128;
+constexpr int kM = 32, kN = 64;
+// ROWS rows into shared memory as f32, times `scale`; zeros behind `rows` and D.
+template <int DT, int DP, bool VEC, int ROWS>
 __device__ __forceinline__ void stage(float* dst, const void* src, int64_t at, int64_t stride, int rows, int D,
                                       float scale) {
     constexpr int W = DP + 4;
-    for (int i = threadIdx.x; i < kN * (DP / 8); i += kThreads) {
+    for (int i = threadIdx.x; i < ROWS * (DP / 8); i += kThreads) {
         const int r = i / (DP / 8), d = (i - r * (DP / 8)) * 8;
         float f[8] = {};
         if (r < rows && d < D) {
@@ -44,9 +41,8 @@ __device__ __forceinline__ void stage(float* dst, const void* src, int64_t at, i
 #pragma unroll
                 for (int p = 0; p < 8 / V; ++p) {
                     float g[V];
-                    Store<DT>::unpack(
-                        ld_reuse(static_cast<const char*>(src) + (x + p * V) * (int64_t)sizeof(typename Store<DT>::T)),
-                        g);
+                    const char* const from = static_cast<const char*>(src);
+                    Store<DT>::unpack(ld_reuse(from + (x + p * V) * (int64_t)sizeof(typename Store<DT>::T)), g);
 #pragma unroll
                     for (int e = 0; e < V; ++e) f[p * V + e] = g[e];
                 }
@@ -61,48 +57,87 @@ __device__ __forceinline__ void stage(float* dst, const void* src, int64_t at, i
     }
 }
 
+// kN rows of f32 on their way into shared memory; zeros behind `rows` and D.
+template <int DP>
+__device__ __forceinline__ void stage_async(float* dst, const float* src, int64_t at, int64_t stride, int rows,
+                                            int D) {
+    constexpr int W = DP + 4;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < kN * (DP / 4); i += kThreads) {
+        const int r = i / (DP / 4), d = (i - r * (DP / 4)) * 4;
+        const bool there = r < rows && d < D;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(dst + r * W + d)),
+                     "l"(src + (there ? at + r * stride + d : 0)), "r"(there ? 16 : 0)
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
 template <int DT, int DP, bool VEC>
-__global__ void __launch_bounds__(kThreads) prompt_rows(PromptArgs a) {
+__global__ void __launch_bounds__(kThreads, DP == 64 ? 4 : 2) prompt_rows(PromptArgs a) {
     constexpr int W = DP + 4, WP = kN + 4, Q4 = DP / 64;
+    constexpr bool ASYNC = DT == kF32 && VEC;
     extern __shared__ float sm[];
     float* qs = sm;
-    float* ks = qs + kM * W;
+    float* ps = qs + kM * W;
+    float* ks = ps + kM * WP;
     float* vs = ks + kN * W;
-    float* ps = vs + kN * W;
-    __shared__ SeqTile where;
+    __shared__ SeqPiece where;
     pdl_begin();
     const int head = (int)(blockIdx.x % (unsigned)a.Hq);
     const unsigned index = blockIdx.x / (unsigned)a.Hq;
     if (threadIdx.x < 32) {
-        const SeqTile t = find_tile(a.starts, (int)a.n_seqs, (int)a.T, kM, index);
+        const SeqPiece t = find_piece(a.starts, (int)a.n_seqs, (int)a.T, index,
+                                      [](int n) { return (uint32_t)((n + kM - 1) / kM); });
         if (threadIdx.x == 0) where = t;
     }
     __syncthreads();
-    const SeqTile w = where;
-    if (w.row < 0) return;
+    if (where.index < 0) return;
+    const struct {
+        int begin, len, row;
+    } w = {where.begin, where.len, where.index * kM};
     const int kvh = head / (int)(a.Hq / a.Hkv), D = (int)a.D;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int rows = min(kM, w.len - w.row);
-    stage<DT, DP, VEC>(qs, a.q, (int64_t)(w.begin + w.row) * a.q_stride + (int64_t)head * D, a.q_stride, rows, D,
+    stage<DT, DP, VEC, kM>(qs, a.q, (int64_t)(w.begin + w.row) * a.q_stride + (int64_t)head * D, a.q_stride, rows, D,
                        a.scale * kLog2e);
-    float o[4][4 * Q4], m[4], l[4];
+    float2 o[4][2 * Q4];
+    float m[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4 * Q4; ++e) o[i][e] = 0.0f;
+        for (int e = 0; e < 2 * Q4; ++e) o[i][e] = make_float2(0.0f, 0.0f);
     }
-    for (int k0 = 0; k0 < w.row + rows; k0 += kN) {
-        const int keys = min(kN, w.len - k0);
+    const int64_t k_at = (int64_t)w.begin * a.k_stride + (int64_t)kvh * D;
+    const int64_t v_at = (int64_t)w.begin * a.v_stride + (int64_t)kvh * D;
+    auto fetch_k = [&](int k0) {
+        if constexpr (ASYNC)
+            stage_async<DP>(ks, static_cast<const float*>(a.k), k_at + (int64_t)k0 * a.k_stride, a.k_stride,
+                            min(kN, w.len - k0), D);
+        else
+            stage<DT, DP, VEC, kN>(ks, a.k, k_at + (int64_t)k0 * a.k_stride, a.k_stride, min(kN, w.len - k0), D,
+                                   1.0f);
+    };
+    auto fetch_v = [&](int k0) {
+        if constexpr (ASYNC)
+            stage_async<DP>(vs, static_cast<const float*>(a.v), v_at + (int64_t)k0 * a.v_stride, a.v_stride,
+                            min(kN, w.len - k0), D);
+        else
+            stage<DT, DP, VEC, kN>(vs, a.v, v_at + (int64_t)k0 * a.v_stride, a.v_stride, min(kN, w.len - k0), D,
+                                   1.0f);
+    };
+    const int end = w.row + rows;
+    fetch_k(0);
+    for (int k0 = 0; k0 < end; k0 += kN) {
         const bool last = k0 + kN > w.row;  // the tile that holds the diagonal
-        __syncthreads();
-        stage<DT, DP, VEC>(ks, a.k, (int64_t)(w.begin + k0) * a.k_stride + (int64_t)kvh * D, a.k_stride, keys, D,
-                           1.0f);
-        stage<DT, DP, VEC>(vs, a.v, (int64_t)(w.begin + k0) * a.v_stride + (int64_t)kvh * D, a.v_stride, keys, D,
-                           1.0f);
-        __syncthreads();
-        float s[4][4] = {};
+        __syncthreads();  // v of the tile before is done with
+        fetch_v(k0);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();  // k is there
+        float2 s2[4][4] = {};  // sums over even and odd entries: two multiply-adds an instruction
 #pragma unroll 4
         for (int d = 0; d < DP; d += 4) {
             float4 x[4], y[4];
@@ -114,12 +149,18 @@ __global__ void __launch_bounds__(kThreads) prompt_rows(PromptArgs a) {
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
-                    s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
-                    s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
-                    s[i][j] = fmaf(x[i].w, y[j].w, s[i][j]);
+                    s2[i][j] = fma2_rn(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), s2[i][j]);
+                    s2[i][j] = fma2_rn(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w), s2[i][j]);
                 }
         }
+        float s[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // k is done with, and v is there
+        if (k0 + kN < end) fetch_k(k0 + kN);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = w.row + ty * 4 + i;
@@ -144,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) prompt_rows(PromptArgs a) {
             for (int x = 8; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
             l[i] = fmaf(l[i], r, sum);
 #pragma unroll
-            for (int e = 0; e < 4 * Q4; ++e) o[i][e] *= r;
+            for (int e = 0; e < 2 * Q4; ++e) o[i][e] = mul2_rn(o[i][e], make_float2(r, r));
         }
         __syncwarp();  // a row's weights come from its own half warp
         auto weigh = [&](auto masked) {
@@ -162,10 +203,9 @@ __global__ void __launch_bounds__(kThreads) prompt_rows(PromptArgs a) {
                         for (int i = 0; i < 4; ++i) {
                             const float w1 = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
                             if (decltype(masked)::value && w1 < 0.0f) continue;
-                            o[i][4 * c + 0] = fmaf(w1, v.x, o[i][4 * c + 0]);
-                            o[i][4 * c + 1] = fmaf(w1, v.y, o[i][4 * c + 1]);
-                            o[i][4 * c + 2] = fmaf(w1, v.z, o[i][4 * c + 2]);
-                            o[i][4 * c + 3] = fmaf(w1, v.w, o[i][4 * c + 3]);
+                            const float2 w2 = make_float2(w1, w1);
+                            o[i][2 * c] = fma2_rn(w2, make_float2(v.x, v.y), o[i][2 * c]);
+                            o[i][2 * c + 1] = fma2_rn(w2, make_float2(v.z, v.w), o[i][2 * c + 1]);
                         }
                     }
             }
@@ -185,7 +225,8 @@ __global__ void __launch_bounds__(kThreads) prompt_rows(PromptArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int d = tx * 4 + 64 * c + e;
-                if (d < D) Store<DT>::store1(a.out, at + d, m[i] == -INFINITY ? 0.0f : o[i][4 * c + e] * inv);
+                const float y = e & 1 ? o[i][2 * c + e / 2].y : o[i][2 * c + e / 2].x;
+                if (d < D) Store<DT>::store1(a.out, at + d, m[i] == -INFINITY ? 0.0f : y * inv);
             }
     }
 }
@@ -202,17 +243,17 @@ cudaError_t go(const PromptArgs& a, cudaStream_t st) {
 
 template <int DT, bool VEC>
 cudaError_t pick(const PromptArgs& a, cudaStream_t st) {
-    if (a.D <= 64) return go<DT, 64, VEC>(a, st);
-    if (a.D <= 128) return go<DT, 128, VEC>(a, st);
+    if constexpr (DT == kF32 || !VEC) {  // (bf16 on the grid up to D = 128 has a kernel of its own)
+        if (a.D <= 64) return go<DT, 64, VEC>(a, st);
+        if (a.D <= 128) return go<DT, 128, VEC>(a, st);
+    }
     return go<DT, 256, VEC>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_prompt(const PromptArgs& a, int dtype, bool vec, cudaStream_t st) {
-    constexpr int64_t kFar = 1LL << 38;  // strides that a tensor copy can describe
-    if (dtype == GBE_BF16 && vec && a.D <= 128 && a.q_stride < kFar && a.k_stride < kFar && a.v_stride < kFar)
-        return launch_attn_prompt_tc(a, st);
+    if (dtype == GBE_BF16 && vec && a.D <= 128) return launch_attn_prompt_tc(a, st);
     if (dtype == GBE_F32) return vec ? pick<kF32, true>(a, st) : pick<kF32, false>(a, st);
     return vec ? pick<kBF16, true>(a, st) : pick<kBF16, false>(a, st);
 }

@@ -45,19 +45,11 @@ namespace {
 constexpr int kM = 128, kN = 128;
 constexpr int kThreads = 384;  // three warpgroups: softmax of each tile, and the issuing warps
 constexpr int kLoadWarp = 8, kItemWarp = 9, kMmaWarp = 10;  // products: a warp for each tile
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrowth = 8.0f;  // a maximum may lag this many powers of two
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Pair `index` of the tiles that share a kv head, counted from the last
-// sequence's last pair (the ones with the most keys first): a sequence of r row
-// tiles has r * group tiles, tile u being head u % group of the group at rows
-// (u / group) * kM.
+// Pair `index` of the tiles that share a kv head, the ones with the most keys
+// first: a sequence of r row tiles has r * group tiles, tile u being head
+// u % group of the group at rows (u / group) * kM.
 struct Pair {
     int begin, len, unit, units;  // units 0: no such pair
 };
@@ -88,96 +80,10 @@ struct Shape {
 };
 
 __device__ __forceinline__ Pair find_pair(const int32_t* starts, int n_seqs, int T, int group, uint32_t index) {
-    const int lane = threadIdx.x & 31;
-    uint32_t before = 0;
-    for (int top = n_seqs; top > 0; top -= 32) {
-        const int b = top - 1 - lane;
-        int s = 0, n = 0;
-        if (b >= 0) {
-            s = min(max(starts[b], 0), T);
-            n = max(min(max(starts[b + 1], 0), T) - s, 0);
-        }
-        const uint32_t units = (uint32_t)((n + kM - 1) / kM) * (uint32_t)group;
-        uint32_t sum = (units + 1) / 2;
-#pragma unroll
-        for (int x = 1; x < 32; x <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, sum, x);
-            if (lane >= x) sum += y;
-        }
-        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, index < before + sum);
-        if (hit) {
-            const int who = __ffs((int)hit) - 1;
-            const uint32_t upto = __shfl_sync(0xFFFFFFFFu, before + sum, who);
-            const uint32_t own = __shfl_sync(0xFFFFFFFFu, units, who);
-            Pair p;
-            p.begin = __shfl_sync(0xFFFFFFFFu, s, who);
-            p.len = __shfl_sync(0xFFFFFFFFu, n, who);
-            p.unit = (int)(upto - 1 - index) * 2;
-            p.units = min(2, (int)own - p.unit);
-            return p;
-        }
-        before += __shfl_sync(0xFFFFFFFFu, sum, 31);
-    }
-    return {0, 0, 0, 0};
-}
-
-// One row in f32 from its own keys alone, by a whole warp: 32 keys at a time,
-// a lane a key for the logits, a lane four entries for the output.
-__device__ __noinline__ void exact_row(const PromptArgs& a, int begin, int row, int head) {
-    const int lane = threadIdx.x & 31, D = (int)a.D, kvh = head / (int)(a.Hq / a.Hkv);
-    const uint16_t* const k = static_cast<const uint16_t*>(a.k) + (int64_t)kvh * D;
-    const uint16_t* const v = static_cast<const uint16_t*>(a.v) + (int64_t)kvh * D;
-    const float c = a.scale * kLog2e;
-    float q[4], o[4] = {};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        q[e] = lane * 4 + e < D
-                   ? Store<kBF16>::load1(a.q, (begin + (int64_t)row) * a.q_stride + (int64_t)head * D + lane * 4 + e)
-                   : 0.0f;
-    float m = -INFINITY, l = 0.0f;
-    for (int k0 = 0; k0 <= row; k0 += 32) {
-        const int j = k0 + lane;
-        const bool seen = j <= row;
-        float s = 0.0f;
-        for (int d = 0; d < D; d += 4) {
-            uint2 w = make_uint2(0, 0);
-            if (seen) w = *reinterpret_cast<const uint2*>(k + (begin + (int64_t)j) * a.k_stride + d);
-            s = fmaf(__shfl_sync(0xFFFFFFFFu, q[0], d >> 2), __uint_as_float(w.x << 16), s);
-            s = fmaf(__shfl_sync(0xFFFFFFFFu, q[1], d >> 2), __uint_as_float(w.x & 0xFFFF0000u), s);
-            s = fmaf(__shfl_sync(0xFFFFFFFFu, q[2], d >> 2), __uint_as_float(w.y << 16), s);
-            s = fmaf(__shfl_sync(0xFFFFFFFFu, q[3], d >> 2), __uint_as_float(w.y & 0xFFFF0000u), s);
-        }
-        s *= c;
-        // a NaN logit leaves a finite maximum, so that its NaN weight reaches the result
-        float mx = seen ? fmaxf(m, s == s ? s : -3.0e38f) : m;
-#pragma unroll
-        for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
-        const float r = m == -INFINITY ? 0.0f : ex2(m - mx);
-        const float p = !seen || s == -INFINITY ? 0.0f : ex2(s - mx);
-        m = mx;
-        float sum = p;
-#pragma unroll
-        for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
-        l = fmaf(l, r, sum);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] *= r;
-        const int keys = min(32, row + 1 - k0);
-        for (int t = 0; t < keys; ++t) {
-            const float w = __shfl_sync(0xFFFFFFFFu, p, t);
-            if (lane * 4 < D) {
-                const uint2 x = *reinterpret_cast<const uint2*>(v + (begin + (int64_t)k0 + t) * a.v_stride + lane * 4);
-                o[0] = fmaf(w, __uint_as_float(x.x << 16), o[0]);
-                o[1] = fmaf(w, __uint_as_float(x.x & 0xFFFF0000u), o[1]);
-                o[2] = fmaf(w, __uint_as_float(x.y << 16), o[2]);
-                o[3] = fmaf(w, __uint_as_float(x.y & 0xFFFF0000u), o[3]);
-            }
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (lane * 4 + e < D)
-            Store<kBF16>::store1(a.out, (begin + (int64_t)row) * a.out_stride + (int64_t)head * D + lane * 4 + e,
-                                 m == -INFINITY ? 0.0f : o[e] / l);
+    auto tiles = [&](int n) { return (uint32_t)((n + kM - 1) / kM) * (uint32_t)group; };
+    const SeqPiece p = find_piece(starts, n_seqs, T, index, [&](int n) { return (tiles(n) + 1) / 2; });
+    if (p.index < 0) return {0, 0, 0, 0};
+    return {p.begin, p.len, 2 * p.index, min(2, (int)tiles(p.len) - 2 * p.index)};
 }
 
 // Work item `round` of this CTA: rounds go back and forth over the CTAs, so that
@@ -556,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (again) {
                 const int r = __ffs((int)again) - 1;
                 again &= again - 1;
-                exact_row(a, it.p.begin, row0 + r, head);
+                exact_row<kBF16>(a, it.p.begin, row0 + r, head);
             }
         }
         // a wait that gave up: NaN in every row of this CTA's tiles, done or not
