@@ -24,14 +24,14 @@
 namespace gbe {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;  // of a group
 constexpr int kM = 32, kN = 64;
 // ROWS rows into shared memory as f32, times `scale`; zeros behind `rows` and D.
 template <int DT, int DP, bool VEC, int ROWS>
 __device__ __forceinline__ void stage(float* dst, const void* src, int64_t at, int64_t stride, int rows, int D,
                                       float scale) {
     constexpr int W = DP + 4;
-    for (int i = threadIdx.x; i < ROWS * (DP / 8); i += kThreads) {
+    for (int i = threadIdx.x & (kThreads - 1); i < ROWS * (DP / 8); i += kThreads) {
         const int r = i / (DP / 8), d = (i - r * (DP / 8)) * 8;
         float f[8] = {};
         if (r < rows && d < D) {
@@ -63,7 +63,7 @@ __device__ __forceinline__ void stage_async(float* dst, const float* src, int64_
                                             int D) {
     constexpr int W = DP + 4;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < kN * (DP / 4); i += kThreads) {
+    for (int i = threadIdx.x & (kThreads - 1); i < kN * (DP / 4); i += kThreads) {
         const int r = i / (DP / 4), d = (i - r * (DP / 4)) * 4;
         const bool there = r < rows && d < D;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
@@ -74,15 +74,24 @@ __device__ __forceinline__ void stage_async(float* dst, const float* src, int64_
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
+// Up to D = 128 two groups of threads take every other tile of keys each and
+// join their sums at the end, which halves the walk of the longest rows.
+template <int DP>
+constexpr int kGroups = DP <= 128 ? 2 : 1;
+template <int DP>
+constexpr int kGroupFloats = 2 * kN * (DP + 4) + kM * (kN + 4);  // k, v and weights
+
 template <int DT, int DP, bool VEC>
-__global__ void __launch_bounds__(kThreads, DP == 64 ? 4 : 2) prompt_rows(PromptArgs a) {
+__global__ void __launch_bounds__(kThreads* kGroups<DP>, DP == 64 ? 2 : 1) prompt_rows(PromptArgs a) {
     constexpr int W = DP + 4, WP = kN + 4, Q4 = DP / 64;
     constexpr bool ASYNC = DT == kF32 && VEC;
     extern __shared__ float sm[];
     float* qs = sm;
-    float* ps = qs + kM * W;
-    float* ks = ps + kM * WP;
-    float* vs = ks + kN * W;
+    const int group = threadIdx.x / kThreads;
+    float* const ps = qs + kM * W + group * kGroupFloats<DP>;
+    float* const ks = ps + kM * WP;
+    float* const vs = ks + kN * W;
+    auto sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kThreads) : "memory"); };
     __shared__ SeqPiece where;
     pdl_begin();
     const int head = (int)(blockIdx.x % (unsigned)a.Hq);
@@ -98,10 +107,11 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 4 : 2) prompt_rows(Prompt
         int begin, len, row;
     } w = {where.begin, where.len, where.index * kM};
     const int kvh = head / (int)(a.Hq / a.Hkv), D = (int)a.D;
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int ty = threadIdx.x % kThreads >> 4, tx = threadIdx.x & 15;
     const int rows = min(kM, w.len - w.row);
-    stage<DT, DP, VEC, kM>(qs, a.q, (int64_t)(w.begin + w.row) * a.q_stride + (int64_t)head * D, a.q_stride, rows, D,
-                       a.scale * kLog2e);
+    if (group == 0)
+        stage<DT, DP, VEC, kM>(qs, a.q, (int64_t)(w.begin + w.row) * a.q_stride + (int64_t)head * D, a.q_stride, rows,
+                               D, a.scale * kLog2e);
     float2 o[4][2 * Q4];
     float m[4], l[4];
 #pragma unroll
@@ -130,13 +140,15 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 4 : 2) prompt_rows(Prompt
                                    1.0f);
     };
     const int end = w.row + rows;
-    fetch_k(0);
-    for (int k0 = 0; k0 < end; k0 += kN) {
+    constexpr int kHop = kGroups<DP> * kN;
+    if (group * kN < end) fetch_k(group * kN);
+    __syncthreads();  // q is there
+    for (int k0 = group * kN; k0 < end; k0 += kHop) {
         const bool last = k0 + kN > w.row;  // the tile that holds the diagonal
-        __syncthreads();  // v of the tile before is done with
+        sync();  // v of the tile before is done with
         fetch_v(k0);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncthreads();  // k is there
+        sync();  // k is there
         float2 s2[4][4] = {};  // sums over even and odd entries: two multiply-adds an instruction
 #pragma unroll 4
         for (int d = 0; d < DP; d += 4) {
@@ -159,8 +171,8 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 4 : 2) prompt_rows(Prompt
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();  // k is done with, and v is there
-        if (k0 + kN < end) fetch_k(k0 + kN);
+        sync();  // k is done with, and v is there
+        if (k0 + kHop < end) fetch_k(k0 + kHop);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = w.row + ty * 4 + i;
@@ -215,6 +227,40 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 4 : 2) prompt_rows(Prompt
         else
             weigh(std::false_type{});
     }
+    if constexpr (kGroups<DP> == 2) {
+        // the second group's sums by way of its own k
+        float* const other = qs + kM * W + kGroupFloats<DP> + kM * WP;
+        if (group == 1) {
+            sync();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float* const to = other + (ty * 4 + i) * W;
+#pragma unroll
+                for (int c = 0; c < Q4; ++c)
+                    *reinterpret_cast<float4*>(to + tx * 4 + 64 * c) =
+                        make_float4(o[i][2 * c].x, o[i][2 * c].y, o[i][2 * c + 1].x, o[i][2 * c + 1].y);
+                if (tx == 0) to[DP] = m[i], to[DP + 1] = l[i];
+            }
+        }
+        __syncthreads();
+        if (group == 1) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float* const from = other + (ty * 4 + i) * W;
+            const float m1 = from[DP], m2 = fmaxf(m[i], m1);
+            const float r0 = m[i] == -INFINITY ? 0.0f : ex2(m[i] - m2), r1 = m1 == -INFINITY ? 0.0f : ex2(m1 - m2);
+            m[i] = m2;
+            l[i] = l[i] * r0 + from[DP + 1] * r1;
+#pragma unroll
+            for (int c = 0; c < Q4; ++c) {
+                const float4 v = *reinterpret_cast<const float4*>(from + tx * 4 + 64 * c);
+                o[i][2 * c].x = o[i][2 * c].x * r0 + v.x * r1;
+                o[i][2 * c].y = o[i][2 * c].y * r0 + v.y * r1;
+                o[i][2 * c + 1].x = o[i][2 * c + 1].x * r0 + v.z * r1;
+                o[i][2 * c + 1].y = o[i][2 * c + 1].y * r0 + v.w * r1;
+            }
+        }
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (ty * 4 + i >= rows) continue;
@@ -233,12 +279,13 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 4 : 2) prompt_rows(Prompt
 
 template <int DT, int DP, bool VEC>
 cudaError_t go(const PromptArgs& a, cudaStream_t st) {
-    constexpr int smem = ((kM + 2 * kN) * (DP + 4) + kM * (kN + 4)) * 4;
+    constexpr int smem = (kM * (DP + 4) + kGroups<DP> * kGroupFloats<DP>) * 4;
     static FunctionLimit limit;
     const cudaError_t e = limit.raise(reinterpret_cast<const void*>(prompt_rows<DT, DP, VEC>), smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = a.T / kM + (a.n_seqs < a.T ? a.n_seqs : a.T);
-    return launch(prompt_rows<DT, DP, VEC>, dim3((unsigned)(tiles * a.Hq)), dim3(kThreads), smem, st, a);
+    const dim3 grid((unsigned)(tiles * a.Hq)), threads(kThreads * kGroups<DP>);
+    return launch(prompt_rows<DT, DP, VEC>, grid, threads, smem, st, a);
 }
 
 template <int DT, bool VEC>
