@@ -99,6 +99,7 @@ class Checker {
             cudaGetLastError();
             return GBE_ERR_POINTER;
         }
+        if (a.type != cudaMemoryTypeDevice) off_device_ = true;
         CUdeviceptr base = 0;
         size_t size = 0;
         bool ranged = false;
@@ -128,6 +129,9 @@ class Checker {
         return GBE_OK;
     }
 
+    // whether a buffer checked so far is managed or host memory
+    bool off_device() const { return off_device_; }
+
   private:
     static bool host_range(uintptr_t p, CUdeviceptr* base, size_t* size) {
         PointerAttributeFn fn = pointer_attribute_fn();
@@ -147,6 +151,7 @@ class Checker {
         uintptr_t lo, hi;
     };
     int dev_ = 0;
+    bool off_device_ = false;
     Span seen_[kSeen];
     int n_ = 0;
 };
@@ -841,6 +846,8 @@ int gbe_attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_st
     if (T == 1) q_stride = out_stride = Hq * D, k_stride = v_stride = Hkv * D;
     const gbe::PromptArgs a = {q, k, v, out, q_stride, k_stride, v_stride, out_stride, starts, n_seqs, T, Hq, Hkv, D,
                                scale};
+    // the tensor copies of the bf16 kernel are for device memory; elsewhere rows are read one by one
+    if (chk.off_device() && dtype == GBE_BF16) vec = vec && D > 128;
     return finish(gbe::launch_attn_prompt(a, dtype, vec, as_stream(stream)));
 }
 

@@ -36,14 +36,6 @@ struct Piece<GBE_KV_F32> {
     }
 };
 template <>
-struct Piece<GBE_KV_BF16> {
-    Vec16 a;
-    __device__ __forceinline__ void load(const void* base, int64_t i) {
-        a = ld_stream(static_cast<const uint16_t*>(base) + i);
-    }
-    __device__ __forceinline__ void widen(float (&f)[8]) const { Store<kBF16>::unpack(a, f); }
-};
-template <>
 struct Piece<GBE_KV_E4M3> {
     uint2 a;
     __device__ __forceinline__ void load(const void* base, int64_t i) {
@@ -61,7 +53,7 @@ struct Piece<GBE_KV_E4M3> {
 // output's in registers.  A stream takes four tokens at a time: their loads are
 // on their way together (64 KB for a CTA's f32 rows, enough to cover HBM's
 // latency from one CTA an SM), and the running maximum moves once for the four.
-template <int DT, int KV, int H>
+template <int KV, int H>
 __global__ void __launch_bounds__(kThreads, 1) decode_rows(Args a, int lanes_log2) {
     constexpr int U = 4;
     extern __shared__ float sm[];  // [kWarps][H][D + 2]
@@ -88,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_rows(Args a, int lanes_log
             acc[h][e] = 0.0f;
             q[h][e] = 0.0f;
             if (mine && h < heads)
-                q[h][e] = Store<DT>::load1(a.q, b * a.q_stride + (int64_t)(h0 + h) * D + d0 + e) * a.scale;
+                q[h][e] = Store<kF32>::load1(a.q, b * a.q_stride + (int64_t)(h0 + h) * D + d0 + e) * a.scale;
         }
     }
     const int32_t* pages = a.table + (int64_t)b * a.max_pages;
@@ -206,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_rows(Args a, int lanes_log
             sum = fmaf(x[D + 1], r, sum), o = fmaf(x[d], r, o);
         }
         if (whole) {
-            Store<DT>::store1(a.out, b * a.out_stride + (int64_t)(h0 + h) * D + d,
+            Store<kF32>::store1(a.out, b * a.out_stride + (int64_t)(h0 + h) * D + d,
                               mx == -INFINITY ? 0.0f : o / sum);
         } else {
             const int64_t row = ((int64_t)b * a.Hq + h0 + h) * a.split + p.chunk;
@@ -284,25 +276,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join(Args a) {
     }
 }
 
-template <int DT, int KV, int H>
+template <int KV, int H>
 cudaError_t go(Args a, int64_t B, cudaStream_t st) {
     int lg = 0;
     while ((8 << lg) < a.c.D) ++lg;
     a.parts = (a.group + H - 1) / H;
     const size_t smem = (size_t)kWarps * H * (a.c.D + 2) * 4;
     static FunctionLimit limit;
-    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(decode_rows<DT, KV, H>), kWarps * H * 258 * 4);
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(decode_rows<KV, H>), kWarps * H * 258 * 4);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(B * a.split * a.c.Hkv * a.parts));
-    return launch(decode_rows<DT, KV, H>, grid, dim3(kThreads), smem, st, a, lg);
+    return launch(decode_rows<KV, H>, grid, dim3(kThreads), smem, st, a, lg);
 }
 
-template <int DT, int KV>
+template <int KV>
 cudaError_t pick(const Args& a, int64_t B, cudaStream_t st) {
-    if (a.group == 1) return go<DT, KV, 1>(a, B, st);
-    if (a.group == 2) return go<DT, KV, 2>(a, B, st);
-    if (a.group <= 4) return go<DT, KV, 4>(a, B, st);
-    return go<DT, KV, 8>(a, B, st);
+    if (a.group == 1) return go<KV, 1>(a, B, st);
+    if (a.group == 2) return go<KV, 2>(a, B, st);
+    if (a.group <= 4) return go<KV, 4>(a, B, st);
+    return go<KV, 8>(a, B, st);
 }
 
 }  // namespace
@@ -333,7 +325,7 @@ cudaError_t launch_attn_decode(const DecodeArgs& d, int dtype, cudaStream_t st) 
     if (dtype == GBE_BF16)
         e = decode::launch_mma(a, d.B, st);
     else
-        e = d.c.dtype == GBE_KV_E4M3 ? pick<kF32, GBE_KV_E4M3>(a, d.B, st) : pick<kF32, GBE_KV_F32>(a, d.B, st);
+        e = d.c.dtype == GBE_KV_E4M3 ? pick<GBE_KV_E4M3>(a, d.B, st) : pick<GBE_KV_F32>(a, d.B, st);
     if (e != cudaSuccess || s.split == 1) return e;
     const dim3 rows((unsigned)(d.B * d.Hq)), threads(kJoinWarps * 32);
     return dtype == GBE_F32 ? launch(attn_join<kF32>, rows, threads, 0, st, a)

@@ -3,19 +3,11 @@
 
 #include <stdint.h>
 
-#include "common.cuh"
+#include "attn_common.cuh"
 #include "launch.h"
 
 namespace gbe {
 namespace decode {
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // A partial softmax's weight when its maximum m moves to m2: 0 while nothing
 // has been seen (m = -inf).

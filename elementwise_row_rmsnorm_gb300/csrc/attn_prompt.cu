@@ -17,7 +17,6 @@
 #include <type_traits>
 
 #include "attn_tiles.cuh"
-#include "common.cuh"
 #include "gbe_elementwise.h"
 #include "launch.h"
 

@@ -34,7 +34,6 @@
 // later row of v would reach the sum; a row that ends up not finite is
 // therefore computed again by exact_row, which looks at its own keys alone.
 #include "attn_tiles.cuh"
-#include "common.cuh"
 #include "gbe_elementwise.h"
 #include "launch.h"
 #include "tensor_core.cuh"

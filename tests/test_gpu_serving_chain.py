@@ -77,3 +77,31 @@ def test_prompt_then_decode(dtype, kind):
         out = gbe.attn_decode(q, cache, table.cuda(), _i32(n))
         want, tol = attn_ref.decode(q, cache, table.cuda(), n, scale, dtype == BF)
         attn_ref.assert_within(out, want, tol, f"step {step}")
+
+
+@pytest.mark.parametrize("dtype,kind", [(F32, F32), (F32, F8), (BF, BF), (BF, F8)])
+def test_pinned_host_tensors(dtype, kind):
+    """The four entry points on pinned host memory, read and written in place: the cache's bits are those of device
+    tensors, the attention is within the definition's bounds."""
+    n, scale = 150, 0.1
+    g = torch.Generator(device="cuda").manual_seed(6)
+    q, k, v = (torch.randn(n, h, D, generator=g, device="cuda").to(dtype) for h in (Hq, H, H))
+    hq, hk, hv = (x.cpu().pin_memory() for x in (q, k, v))
+    slots = _i32(list(range(16, 16 + n)))
+    cache = gbe.kv_cache(11, H, P, D, kind)
+    host = gbe.KvCache(*(None if t is None else torch.zeros(t.shape, dtype=t.dtype).pin_memory()
+                         for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)))
+    gbe.gbe_kv_write(k, v, slots, cache)
+    gbe.gbe_kv_write(hk, hv, slots.cpu().pin_memory(), host)
+    rk, rv = torch.empty_like(hk).pin_memory(), torch.empty_like(hv).pin_memory()
+    gbe.gbe_kv_read(rk, rv, slots.cpu().pin_memory(), host)
+    dk, dv = gbe.kv_read(cache, slots, dtype)
+    out, dec = torch.empty_like(hq).pin_memory(), torch.empty_like(hq[:1]).pin_memory()
+    gbe.gbe_attn_prompt(hq, hk, hv, out, _i32([0, 60, n]).cpu().pin_memory(), scale)
+    table = torch.arange(1, 11, dtype=torch.int32)[None]
+    gbe.gbe_attn_decode(hq[:1], dec, host, table.pin_memory(), torch.tensor([n], dtype=torch.int32).pin_memory(), scale)
+    torch.cuda.synchronize()
+    assert torch.equal(rk.cuda(), dk) and torch.equal(rv.cuda(), dv)
+    want, tol, _ = attn_ref.prompt(q, k, v, [0, 60, n], scale, dtype == BF)
+    attn_ref.assert_within(out.cuda(), want, tol, "prompt")
+    assert torch.equal(dec.cuda(), gbe.attn_decode(q[:1], cache, table.cuda(), _i32([n]), scale))
