@@ -247,3 +247,76 @@ def test_stream_argument():
     torch.cuda.synchronize()
     for g in got:
         assert torch.equal(g, want)
+
+
+@pytest.mark.parametrize("kind", [BF, F8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_large_batch_has_the_bits_of_its_rows_alone(kind, D):
+    """Batches in which a CTA takes several chunks one after another; lengths of every residue."""
+    B, Hq, H, P = 60, 16, 8, 64
+    g = torch.Generator().manual_seed(5)
+    lens = [8192, 0, 1, 511, 512, 513, 8191, 4097] + torch.randint(0, 8193, (B - 8,), generator=g).tolist()
+    need = [-(-n // P) for n in lens]
+    pages = sum(need) + 1
+    cache = gbe.kv_cache(pages, H, P, D, kind)
+    for t, seed in ((cache.k, 1), (cache.v, 2)):
+        if kind == F8:  # codes of magnitude up to 30, no NaN
+            t.view(torch.uint8).copy_(torch.randint(0, 96, t.shape, dtype=torch.uint8, device="cuda")
+                                      | torch.randint(0, 2, t.shape, dtype=torch.uint8, device="cuda") << 7)
+        else:
+            t.copy_(_rand(t.shape, BF, seed))
+    if kind == F8:
+        for t in (cache.k_scale, cache.v_scale):
+            t.copy_(torch.randint(121, 126, t.shape, dtype=torch.uint8, device="cuda"))
+    table = torch.zeros(B, max(need), dtype=torch.int32)
+    order = torch.randperm(pages, generator=g).tolist()
+    for b, m in enumerate(need):
+        for i in range(m):
+            table[b, i] = order.pop()
+    table = table.cuda()
+    q = _rand((B, Hq, D), BF, 3)
+    lens_t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    whole = gbe.attn_decode(q, cache, table, lens_t)
+    for b in range(B):
+        one = gbe.attn_decode(q[b:b + 1], cache, table[b:b + 1], lens_t[b:b + 1])
+        assert torch.equal(one[0], whole[b]), (b, lens[b])
+    for b in (0, 3, 7, 20):
+        want, tol = attn_ref.decode(q[b:b + 1], cache, table[b:b + 1], lens[b:b + 1], 1.0 / math.sqrt(D), True)
+        attn_ref.assert_within(whole[b:b + 1], want, tol, f"row {b}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("D", [64, 72, 128])
+def test_e4m3_scales_far_apart(dtype, D):
+    """Rows of v from 1e-9 to 1e9 in one sequence, the large ones with small weights, and rows of zeros; k likewise."""
+    P, H, Hq, n = 16, 2, 8, 600
+    cache = gbe.kv_cache(40, H, P, D, F8)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    size = torch.rand(n, H, 1, generator=g, device="cuda") * 18.0 - 9.0
+    size[::7] = -9.0
+    size[5] = 9.0
+    k, v = _rand((n, H, D), dtype, 1), (_rand((n, H, D), F32, 2) * 10.0 ** size).to(dtype)
+    v[::50] = 0.0
+    # a common direction that the tokens with large values are turned away from
+    away = _rand((1, H, D), F32, 4)
+    k = (k.float() - away * (size + 9.0) * 0.6).to(dtype)
+    k[3] *= 1e-6
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    gbe.gbe_kv_write(k, v, slots, cache)
+    table = torch.arange(38, dtype=torch.int32, device="cuda")[None]
+    q = (_rand((1, Hq, D), F32, 3) * 0.3 + away.repeat_interleave(Hq // H, 1)).to(dtype)
+    for m in (n, 16, 100):
+        _check(q, cache, table, [m], 1.0 / math.sqrt(D), f"{m} tokens")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("power", [-100, -60, 60, 100])
+def test_e4m3_magnitudes_that_make_up_for_one_another(dtype, power):
+    """q of 2^power and k of 2^-power, and the other way round: the logits are ordinary."""
+    P, H, Hq, D, n = 16, 1, 4, 64, 200
+    cache = gbe.kv_cache(13, H, P, D, F8)
+    k, v = _rand((n, H, D), F32, 11), _rand((n, H, D), dtype, 12)
+    gbe.gbe_kv_write((k * 2.0 ** -power).to(dtype), v, torch.arange(n, dtype=torch.int32, device="cuda"), cache)
+    table = torch.arange(13, dtype=torch.int32, device="cuda")[None]
+    q = (_rand((1, Hq, D), F32, 13) * 2.0 ** power).to(dtype)
+    _check(q, cache, table, [n], 0.125, f"2^{power}")
