@@ -31,8 +31,8 @@
 // f32 (both floats) and keeps sums far from overflow.
 //
 // Masked weights are exact zeros, but zero times an infinity or a NaN in a
-// later row of v would reach the sum; a row that ends up not finite is
-// therefore computed again by exact_row, which looks at its own keys alone.
+// later row of v would reach the sum: rows that come out not finite are looked
+// at once more (repair_row).
 #include "attn_tiles.cuh"
 #include "gbe_elementwise.h"
 #include "launch.h"
@@ -83,6 +83,103 @@ __device__ __forceinline__ Pair find_pair(const int32_t* starts, int n_seqs, int
     const SeqPiece p = find_piece(starts, n_seqs, T, index, [&](int n) { return (tiles(n) + 1) / 2; });
     if (p.index < 0) return {0, 0, 0, 0};
     return {p.begin, p.len, 2 * p.index, min(2, (int)tiles(p.len) - 2 * p.index)};
+}
+
+// Four consecutive values, widened.
+__device__ __forceinline__ float4 load4(const void* base, int64_t i) {
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xFFFF0000u));
+}
+
+// One row in f32 from its own keys alone, by a whole warp: 32 keys at a time, a
+// lane a key for the logits, a lane four entries for the output.
+__device__ __noinline__ void exact_row(const PromptArgs& a, int begin, int row, int head) {
+    const int lane = threadIdx.x & 31, D = (int)a.D, kvh = head / (int)(a.Hq / a.Hkv);
+    const float c = a.scale * kLog2e;
+    float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f), o = q;
+    if (lane * 4 < D) q = load4(a.q, (begin + (int64_t)row) * a.q_stride + (int64_t)head * D + lane * 4);
+    float m = -INFINITY, l = 0.0f;
+    for (int k0 = 0; k0 <= row; k0 += 32) {
+        const int j = k0 + lane;
+        const bool seen = j <= row;
+        const int64_t k_at = (begin + (int64_t)(seen ? j : row)) * a.k_stride + (int64_t)kvh * D;
+        float s = 0.0f;
+        for (int d = 0; d < D; d += 4) {
+            const float4 k = load4(a.k, k_at + d);
+            s = fmaf(__shfl_sync(0xFFFFFFFFu, q.x, d >> 2), k.x, s);
+            s = fmaf(__shfl_sync(0xFFFFFFFFu, q.y, d >> 2), k.y, s);
+            s = fmaf(__shfl_sync(0xFFFFFFFFu, q.z, d >> 2), k.z, s);
+            s = fmaf(__shfl_sync(0xFFFFFFFFu, q.w, d >> 2), k.w, s);
+        }
+        s *= c;
+        // a NaN logit leaves a finite maximum, so that its NaN weight reaches the result
+        float mx = seen ? fmaxf(m, s == s ? s : -3.0e38f) : m;
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+        const float r = m == -INFINITY ? 0.0f : ex2(m - mx);
+        const float p = !seen || s == -INFINITY ? 0.0f : ex2(s - mx);
+        m = mx;
+        float sum = p;
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+        l = fmaf(l, r, sum);
+        o.x *= r, o.y *= r, o.z *= r, o.w *= r;
+        const int keys = min(32, row + 1 - k0);
+        for (int t = 0; t < keys; ++t) {
+            const float w = __shfl_sync(0xFFFFFFFFu, p, t);
+            if (lane * 4 < D) {
+                const float4 v =
+                    load4(a.v, (begin + (int64_t)k0 + t) * a.v_stride + (int64_t)kvh * D + lane * 4);
+                o.x = fmaf(w, v.x, o.x);
+                o.y = fmaf(w, v.y, o.y);
+                o.z = fmaf(w, v.z, o.z);
+                o.w = fmaf(w, v.w, o.w);
+            }
+        }
+    }
+    if (lane * 4 < D) {
+        const float y[4] = {o.x, o.y, o.z, o.w};
+        const int64_t at = (begin + (int64_t)row) * a.out_stride + (int64_t)head * D + lane * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) Store<kBF16>::store1(a.out, at + e, m == -INFINITY ? 0.0f : y[e] / l);
+    }
+}
+
+// Which of four consecutive values are infinite or NaN, a bit each.
+__device__ __forceinline__ uint32_t not_finite4(const void* base, int64_t i) {
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
+    return ((w.x & 0x7F80u) == 0x7F80u ? 1u : 0u) | ((w.x >> 16 & 0x7F80u) == 0x7F80u ? 2u : 0u) |
+           ((w.y & 0x7F80u) == 0x7F80u ? 4u : 0u) | ((w.y >> 16 & 0x7F80u) == 0x7F80u ? 8u : 0u);
+}
+
+// A row that came out not finite: right as it is where the keys that it attends
+// to made it so, but a weight of zero may also have met an infinity or a NaN of
+// v behind the mask, in rows row + 1 .. tile_end - 1 of the tile.  Computed
+// again only if an entry is not finite, has such a value behind the mask, and
+// has none before it.  By a whole warp; the row has been written.
+__device__ __noinline__ void repair_row(const PromptArgs& a, int begin, int row, int tile_end, int head) {
+    const int lane = threadIdx.x & 31, D = (int)a.D, kvh = head / (int)(a.Hq / a.Hkv);
+    const bool mine = lane * 4 < D;
+    const int64_t v0 = (int64_t)begin * a.v_stride + (int64_t)kvh * D + lane * 4;
+    const int64_t out0 = (begin + (int64_t)row) * a.out_stride + (int64_t)head * D + lane * 4;
+    uint32_t open = mine ? not_finite4(a.out, out0) : 0u;  // entries that may have to be computed again
+    const int end = (int)min((int64_t)tile_end, a.T - begin);
+    uint32_t behind = 0;
+    for (int j = row + 1; j < end && __any_sync(0xFFFFFFFFu, open & ~behind); j += 8)
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            if (mine && j + x < end) behind |= not_finite4(a.v, v0 + (int64_t)(j + x) * a.v_stride);
+    open &= behind;
+    for (int j = row; j >= 0; j -= 8) {
+        if (!__any_sync(0xFFFFFFFFu, open)) return;
+        uint32_t before = 0;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            if (mine && j - x >= 0) before |= not_finite4(a.v, v0 + (int64_t)(j - x) * a.v_stride);
+        open &= ~before;
+    }
+    if (__any_sync(0xFFFFFFFFu, open)) exact_row(a, begin, row, head);
 }
 
 // Work item `round` of this CTA: rounds go back and forth over the CTAs, so that
@@ -319,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = warp >> 2;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
         const uint32_t ts = tmem + lanes, tp = tmem + 128 + t * 64 + lanes, to = tmem + 256 + t * 128 + lanes;
-        const float c = fabsf(a.scale) * kLog2e;
+        // (never 0, so that c times the -inf of a masked place stays -inf)
+        const float c = fmaxf(fabsf(a.scale) * kLog2e, __uint_as_float(1u));
         uint8_t* const stage = raw + (base - smem_addr(raw)) + S::kTile * (2 + S::kStages) + warp * (S::kOut / 8);
         bool ok = true;
         int done = 0;  // blocks of this tile before this item
@@ -455,13 +553,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (row0 + r < it.p.len && d < a.D) *reinterpret_cast<Vec16*>(out + r * a.out_stride + d) = v;
                 }
             }
-            // rows that are not finite again, from their own keys alone
             uint32_t again = __ballot_sync(0xFFFFFFFFu, ok && live && bad);
             __syncwarp();
             while (again) {
                 const int r = __ffs((int)again) - 1;
                 again &= again - 1;
-                exact_row<kBF16>(a, it.p.begin, row0 + r, head);
+                repair_row(a, it.p.begin, row0 + r, u / group * kM + kM, head);
             }
         }
         // a wait that gave up: NaN in every row of this CTA's tiles, done or not

@@ -463,7 +463,9 @@ int gbe_kv_read(void *k, int64_t k_stride, void *v, int64_t v_stride, const int3
  *         aligned, of any content, used until the call's work on `stream` is
  *         done: calls in flight on other streams need their own.  May be NULL
  *         when 0 bytes are needed.
- * Sums, maxima and the softmax are f32; results are rounded once at the end.
+ * Sums, maxima and the softmax are f32; for bf16 queries the products go
+ * through the tensor cores, with weights of 8 bits or more; results are
+ * rounded once at the end.
  * What lies in the cache behind a sequence's last token is not looked at
  * (infinities and NaN there stay there).  A NaN in an attended place gives
  * NaN; a row with nothing to attend to is zeros.
@@ -499,6 +501,11 @@ int64_t gbe_attn_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
  * Sums, maxima and the softmax are f32; results are rounded once at the end.
  * Alias : out overlaps nothing; q, k and v may interleave in one buffer.
  * A row's bits depend on its sequence alone, not on its place in the packing.
+ * bf16 with D up to 128 and every row on the 16-byte grid, in device memory,
+ * goes through the tensor cores, the weights rounded to bf16 for the second
+ * product; other bf16 calls do not, and differ from it within that rounding.
+ * An infinity or a NaN in an attended place makes the entries that it reaches
+ * not finite.
  * Hq is a multiple of Hkv, at most 65536; T at most 2^28, n_seqs at most 2^24.
  */
 int gbe_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
