@@ -471,7 +471,8 @@ class KvCache:
                     raise ValueError("KvCache: a float8_e4m3fn cache has uint8 scales [n_pages, Hkv, page_size]")
         elif k_scale is not None or v_scale is not None:
             raise ValueError("KvCache: only a float8_e4m3fn cache has scales")
-        _where(k, v, k_scale, v_scale)
+        if not (k.is_cuda and v.is_cuda and k_scale is None):
+            _where(k, v, k_scale, v_scale)
         self.k, self.v, self.k_scale, self.v_scale, self.shape = k, v, k_scale, v_scale, shape
         # the bytes of a gbe_kv_cache, which the library reads during the call
         self.desc = _pack_cache(k.data_ptr(), v.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
@@ -487,14 +488,15 @@ def _where(*ts):
 
 def _kv_sides(what, k, v, cache, slots, bad):
     T, H, sk = _rows_view(k, cache.shape[3])
-    Tv, Hv, sv = _rows_view(v, cache.shape[3])
-    if Tv != T or H != cache.shape[1] or Hv != H:
+    if v.shape != k.shape or H != cache.shape[1]:
         raise ValueError(f"{what}: k and v are [T, Hkv, D] with the cache's Hkv and D")
+    sv = sk if v.stride() == k.stride() else _rows_view(v, cache.shape[3])[2]
     if slots.dtype != torch.int32 or slots.numel() != T or not slots.is_contiguous():
         raise ValueError(f"{what}: slots is int32[T]")
     if bad is not None and (bad.dtype != torch.int32 or bad.numel() != 1):
         raise ValueError(f"{what}: bad_slot_count is one int32")
-    _where(k, v, slots, bad)
+    if not (k.is_cuda and v.is_cuda and slots.is_cuda and bad is None):
+        _where(k, v, slots, bad)
     return (k.data_ptr(), sk, v.data_ptr(), sv, slots.data_ptr(), T, cache.desc, None if bad is None else bad.data_ptr(),
             _dt(k, v))
 
@@ -524,21 +526,20 @@ def attn_decode_workspace(B: int, Hq: int, cache: KvCache, max_pages: int) -> in
 def gbe_attn_decode(q, out, cache: KvCache, table, lens, scale: float, workspace=None, stream=None) -> None:
     """q, out: [B, Hq, D]; table: int32[B, max_pages]; lens: int32[B], the new token included; workspace: any tensor
     of attn_decode_workspace bytes (None when that is 0)."""
-    D = cache.shape[3]
-    B, Hq, sq = _rows_view(q, D)
-    Bo, Ho, so = _rows_view(out, D)
-    if Bo != B or Ho != Hq:
+    B, Hq, sq = _rows_view(q, cache.shape[3])
+    if out.shape != q.shape:
         raise ValueError("attn_decode: out has q's shape")
+    so = sq if out.stride() == q.stride() else _rows_view(out, cache.shape[3])[2]
     rows = table.shape
     if table.dtype != torch.int32 or len(rows) != 2 or rows[0] != B or not table.is_contiguous():
         raise ValueError("attn_decode: table is int32[B, max_pages]")
     if lens.dtype != torch.int32 or lens.numel() != B or not lens.is_contiguous():
         raise ValueError("attn_decode: lens is int32[B]")
-    _where(q, out, table, lens, workspace)
+    if not (q.is_cuda and out.is_cuda and table.is_cuda and lens.is_cuda):
+        _where(q, out, table, lens)
     room = 0
     if workspace is not None:
-        if not workspace.is_contiguous():
-            raise ValueError("tensors must be contiguous")
+        _dev(workspace)
         room = workspace.numel() * workspace.element_size()
     _check("gbe_attn_decode", lib().gbe_attn_decode(
         q.data_ptr(), sq, out.data_ptr(), so, B, Hq, cache.desc, table.data_ptr(), rows[1], lens.data_ptr(), scale,

@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row0 = u / group * kM + (warp & 3) * 32;
             uint16_t* const out = static_cast<uint16_t*>(a.out) + (it.p.begin + (int64_t)row0) * a.out_stride +
                                   (int64_t)head * a.D;
-            bool bad = false;
+            float2 bad = make_float2(0.0f, 0.0f);
             // 64 entries of the warp's rows at a time by way of shared memory, so
             // that a store covers 128 bytes of each of four rows (a thread storing
             // its own row took 5200 clocks a tile)
@@ -534,16 +534,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 __syncwarp();
+                // a wait that gave up leaves NaN
+                const float by = ok ? inv : __uint_as_float(0x7FC00000u);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    float f[8];
+                    Vec16 v;
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        // a wait that gave up leaves NaN
-                        f[y] = ok ? __uint_as_float(o[e * 8 + y]) * inv : __uint_as_float(0x7FC00000u);
-                        bad = bad || !(fabsf(f[y]) <= 3.402823466e38f);
+                    for (int y = 0; y < 4; ++y) {
+                        const float2 f = mul2_rn(make_float2(__uint_as_float(o[e * 8 + 2 * y]),
+                                                             __uint_as_float(o[e * 8 + 2 * y + 1])),
+                                                 make_float2(by, by));
+                        bad = fma2_rn(f, make_float2(0.0f, 0.0f), bad);  // 0, or NaN
+                        v.w[y] = f32x2_to_bf16x2_bits(f.x, f.y);
                     }
-                    *reinterpret_cast<Vec16*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = Store<kBF16>::pack(f);
+                    *reinterpret_cast<Vec16*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = v;
                 }
                 __syncwarp();
 #pragma unroll
@@ -553,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (row0 + r < it.p.len && d < a.D) *reinterpret_cast<Vec16*>(out + r * a.out_stride + d) = v;
                 }
             }
-            uint32_t again = __ballot_sync(0xFFFFFFFFu, ok && live && bad);
+            uint32_t again = __ballot_sync(0xFFFFFFFFu, ok && live && bad.x + bad.y != 0.0f);
             __syncwarp();
             while (again) {
                 const int r = __ffs((int)again) - 1;
