@@ -17,170 +17,217 @@
 namespace gbe {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr float kGrowth = 8.0f;  // powers of two that the maximum in use may lag
 using namespace decode;
 
-// One 8-value piece of a cached row, widened to f32.
-template <int KV>
-struct Piece;
-template <>
-struct Piece<GBE_KV_F32> {
-    Vec16 a, b;
-    __device__ __forceinline__ void load(const void* base, int64_t i) {
-        const float* p = static_cast<const float*>(base) + i;
-        a = ld_stream(p), b = ld_stream(p + 4);
-    }
-    __device__ __forceinline__ void widen(float (&f)[8]) const {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(a.w[e]), f[4 + e] = __uint_as_float(b.w[e]);
-    }
-};
-template <>
-struct Piece<GBE_KV_E4M3> {
-    uint2 a;
-    __device__ __forceinline__ void load(const void* base, int64_t i) {
-        a = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + i);
-    }
-    __device__ __forceinline__ void widen(float (&f)[8]) const {
-        e4m3x4_to_f32(a.x, f);
-        e4m3x4_to_f32(a.y, f + 4);
-    }
-};
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* p, bool there) {
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(there ? 16 : 0)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(p), "r"(there ? 8 : 0)
+                     : "memory");
+}
 
-// The CUDA-core form, for f32 queries: G lanes (the power of two at or above
-// D / 8) hold one token's row, eight values each, so a warp walks 32 / G
-// streams of tokens and each lane keeps the query heads' pieces and the
-// output's in registers.  A stream takes four tokens at a time: their loads are
-// on their way together (64 KB for a CTA's f32 rows, enough to cover HBM's
-// latency from one CTA an SM), and the running maximum moves once for the four.
-template <int KV, int H>
-__global__ void __launch_bounds__(kThreads, 1) decode_rows(Args a, int lanes_log2) {
-    constexpr int U = 4;
-    extern __shared__ float sm[];  // [kWarps][H][D + 2]
+// The f32 form, on the CUDA cores: G lanes hold one token's row, eight values
+// each, so a warp walks 32 / G streams of tokens, and a lane keeps the query
+// heads' pieces and the output's in registers.  A lane's pieces of k and v come
+// by asynchronous copies into a ring that is the lane's alone, kDepth tokens
+// ahead, so that no wait but its own stands between a copy and its use; 16-byte
+// pieces of the 32 lanes lie side by side.  Logits are summed over the G lanes
+// by halves -- a lane passes on half of its heads at every step, and ends up
+// with one -- so H heads take log2(H) + log2(G) - 1 + (H / 2 - 1) shuffles in
+// place of H log2(G), and one exponential; the weights are passed back.
+template <int KV, int H, int LG>
+__global__ void __launch_bounds__(kThreads, H == 8 ? 3 : 4) decode_rows(Args a) {
+    constexpr bool E4 = KV == GBE_KV_E4M3;
+    constexpr int G = 1 << LG, LH = H == 1 ? 0 : H == 2 ? 1 : H == 4 ? 2 : 3;
+    constexpr int kPieces = E4 ? 1 : 2, kBytes = E4 ? 8 : 16;         // of k, and as many of v, for a lane and token
+    constexpr int kDepth = E4 ? 8 : 4, kSlot = 2 * kPieces * kBytes * 32;  // of a warp
+    constexpr int streams = kThreads / G;
+    extern __shared__ __align__(128) uint8_t raw[];  // the rings; then [kWarps][heads][D + 2]
     pdl_begin();
     const KvCacheArgs& c = a.c;
-    const int G = 1 << lanes_log2, D = c.D;
+    const int D = c.D;
     const Part p = find_part(a, blockIdx.x);
     if (p.t0 >= p.t1 && p.chunk > 0) return;
-    const int b = p.b, kvh = p.kvh, t0 = p.t0, t1 = p.t1;
-    const int h0 = kvh * a.group + p.part * H;            // first query head
+    const int h0 = p.kvh * a.group + p.part * H;  // first query head
     const int heads = min(H, a.group - p.part * H);
-
-    const int sub = threadIdx.x & (G - 1), d0 = sub * 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & (G - 1), d0 = sub * 8;
     const bool mine = d0 < D;
-    const int stream = threadIdx.x >> lanes_log2, streams = kThreads >> lanes_log2;
 
-    float q[H][8], acc[H][8], m[H], l[H];
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-        m[h] = -INFINITY;
-        l[h] = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            acc[h][e] = 0.0f;
-            q[h][e] = 0.0f;
-            if (mine && h < heads)
-                q[h][e] = Store<kF32>::load1(a.q, b * a.q_stride + (int64_t)(h0 + h) * D + d0 + e) * a.scale;
-        }
-    }
-    const int32_t* pages = a.table + (int64_t)b * a.max_pages;
-    // all streams of a warp take the same number of steps, so that its
-    // shuffles meet
-    for (int base = t0; base < t1; base += U * streams) {
-        Piece<KV> kp[U], vp[U];
-        float ks[U], vs[U];
-        bool good[U];
-        int64_t at[U], si[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = base + u * streams + stream;
-            const bool live = t < t1;
-            const int page_i = live ? t / c.page_size : 0;
-            const int32_t page = live ? pages[page_i] : -1;
-            const int row = t - page_i * c.page_size;
-            good[u] = page >= 0 && page < c.n_pages;
-            at[u] = page * c.page_stride + ((int64_t)kvh * c.page_size + row) * D + d0;
-            si[u] = ((int64_t)page * c.Hkv + kvh) * c.page_size + row;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            kp[u] = {}, vp[u] = {};
-            ks[u] = vs[u] = 1.0f;
-            if (good[u] && mine) kp[u].load(c.k, at[u]), vp[u].load(c.v, at[u]);
-            if (KV == GBE_KV_E4M3 && good[u]) {
-                ks[u] = __uint_as_float((uint32_t)c.k_scale[si[u]] << 23);
-                vs[u] = __uint_as_float((uint32_t)c.v_scale[si[u]] << 23);
+    // the stream's token that is fetched next, and its page
+    int tok = p.t0 + threadIdx.x / G, page_i = tok / c.page_size, row = tok - page_i * c.page_size;
+    const int hop_pages = streams / c.page_size, hop_rows = streams - hop_pages * c.page_size;
+    const int32_t* pages = a.table + (int64_t)p.b * a.max_pages;
+    auto page_of = [&] { return tok < p.t1 ? pages[page_i] : -1; };
+    int32_t page = page_of();
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(raw) + warp * kDepth * kSlot + lane * kBytes;
+    uint32_t live = 0;  // bit i: the stream's token i steps ahead is there
+    float scales[kDepth][2];
+    auto fetch = [&](int slot, float (&sc)[2]) {
+        const bool good = page >= 0 && page < c.n_pages;
+        int64_t at = 0;
+        if (good) {
+            at = page * c.page_stride + ((int64_t)p.kvh * c.page_size + row) * D + d0;
+            if constexpr (E4) {
+                const int64_t si = ((int64_t)page * c.Hkv + p.kvh) * c.page_size + row;
+                sc[0] = __uint_as_float((uint32_t)c.k_scale[si] << 23);
+                sc[1] = __uint_as_float((uint32_t)c.v_scale[si] << 23);
             }
         }
-        float s[U][H];
+        if (!mine) at = 0;
+        if (good) {  // (lanes past D fill their places with zeros)
+            const uint32_t to = ring + slot * kSlot;
+            const uint8_t* k = static_cast<const uint8_t*>(c.k) + at * (E4 ? 1 : 4);
+            const uint8_t* v = static_cast<const uint8_t*>(c.v) + at * (E4 ? 1 : 4);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float k[8];
-            kp[u].widen(k);
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                float x = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x = fmaf(q[h][e], k[e], x);
-                for (int y = G >> 1; y >= 1; y >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, y);
-                s[u][h] = good[u] ? (KV == GBE_KV_E4M3 ? x * ks[u] : x) : -INFINITY;
+            for (int x = 0; x < kPieces; ++x) {
+                copy_async<kBytes>(to + x * kBytes * 32, k + x * kBytes, mine);
+                copy_async<kBytes>(to + (kPieces + x) * kBytes * 32, v + x * kBytes, mine);
             }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        tok += streams;
+        page_i += hop_pages;
+        row += hop_rows;
+        if (row >= c.page_size) row -= c.page_size, ++page_i;
+        page = page_of();
+        return good;
+    };
+#pragma unroll
+    for (int x = 0; x < kDepth - 1; ++x) live |= (uint32_t)fetch(x, scales[x]) << x;
+
+    float2 q[H][4], acc[H][4];
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            acc[h][e] = q[h][e] = make_float2(0.0f, 0.0f);
+            if (mine && h < heads) {
+                const int64_t at = p.b * a.q_stride + (int64_t)(h0 + h) * D + d0 + 2 * e;
+                const float* from = static_cast<const float*>(a.q) + at;
+                q[h][e] = make_float2(from[0] * a.scale, from[1] * a.scale);
+            }
+        }
+    float m = -INFINITY, l = 0.0f;  // of the lane's own head, number sub >> (LG - LH)
+    auto to_all = [&](float own, int h) {
+        return __shfl_sync(0xFFFFFFFFu, own, (lane & ~(G - 1)) | (h << (LG - LH)));
+    };
+    // all streams of a CTA take the same number of steps, so that its shuffles meet
+    const int steps = (p.t1 - p.t0 + streams - 1) / streams;
+    int slot = 0;
+    for (int step = 0; step < steps; ++step) {
+        live |= (uint32_t)fetch(slot == 0 ? kDepth - 1 : slot - 1, scales[kDepth - 1]) << (kDepth - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+        const uint8_t* const from = raw + warp * kDepth * kSlot + slot * kSlot + lane * kBytes;
+        const bool good = live & 1u;
+        auto piece = [&](int first, float2 (&f)[4]) {
+            float y[8];
+            if constexpr (E4) {
+                const uint2 w = *reinterpret_cast<const uint2*>(from + first * kBytes * 32);
+                e4m3x4_to_f32(w.x, y);
+                e4m3x4_to_f32(w.y, y + 4);
+            } else {
+                const uint8_t* const at = from + first * kBytes * 32;
+                *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(at);
+                *reinterpret_cast<float4*>(y + 4) = *reinterpret_cast<const float4*>(at + kBytes * 32);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = make_float2(y[2 * e], y[2 * e + 1]);
+        };
+        float2 k[4];
+        piece(0, k);
+        float s[H];
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-            float m2 = m[h];
-            // a NaN logit leaves a finite maximum, so that its NaN weight reaches the result
+            float2 x = mul2_rn(q[h][0], k[0]);
 #pragma unroll
-            for (int u = 0; u < U; ++u) m2 = fmaxf(m2, s[u][h] == s[u][h] ? s[u][h] : -3.0e38f);
-            const float r = rescale(m[h], m2);
-            m[h] = m2;
-            l[h] *= r;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[h][e] *= r;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                s[u][h] = s[u][h] == -INFINITY ? 0.0f : ex2(s[u][h] - m2);
-                l[h] += s[u][h];
-            }
+            for (int e = 1; e < 4; ++e) x = fma2_rn(q[h][e], k[e], x);
+            s[h] = x.x + x.y;
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float v[8];
-            vp[u].widen(v);
+        for (int b = 0; b < LH; ++b) {
+            const int mask = G >> (b + 1), n = H >> (b + 1);
+            const bool up = lane & mask;
+#pragma unroll
+            for (int x = 0; x < n; ++x) {
+                const float send = up ? s[x] : s[x + n];
+                s[x] = (up ? s[x + n] : s[x]) + __shfl_xor_sync(0xFFFFFFFFu, send, mask);
+            }
+        }
+        float t = s[0];
+#pragma unroll
+        for (int mask = G >> (LH + 1); mask >= 1; mask >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, mask);
+        if (E4) t *= scales[0][0];
+        t = good ? t : -INFINITY;
+        if (__any_sync(0xFFFFFFFFu, t > m + kGrowth || (t != t && m == -INFINITY))) {
+            // (a NaN logit leaves a finite maximum, so that its NaN weight reaches the result)
+            const float top = t == t ? t : -3.0e38f;
+            const float m2 = top > m + kGrowth ? top : m, r = rescale(m, m2);
+            m = m2;
+            l *= r;
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                const float w = KV == GBE_KV_E4M3 ? s[u][h] * vs[u] : s[u][h];
+                const float rh = to_all(r, h);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[h][e] = fmaf(w, v[e], acc[h][e]);
+                for (int e = 0; e < 4; ++e) acc[h][e] = mul2_rn(acc[h][e], make_float2(rh, rh));
             }
         }
+        const float w = ex2(t - (m == -INFINITY ? 0.0f : m));
+        l += w;
+        if (good) {
+            float2 v[4];
+            piece(kPieces, v);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                // (the streams of a warp may differ in `good`: a shuffle within one stream's lanes)
+                float wh = __shfl_sync(G == 32 ? 0xFFFFFFFFu : ((1u << G) - 1u) << (lane & ~(G - 1)), w,
+                                       (lane & ~(G - 1)) | (h << (LG - LH)));
+                if (E4) wh *= scales[0][1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[h][e] = fma2_rn(make_float2(wh, wh), v[e], acc[h][e]);
+            }
+        }
+        live >>= 1;
+#pragma unroll
+        for (int x = 0; x + 1 < kDepth; ++x) scales[x][0] = scales[x + 1][0], scales[x][1] = scales[x + 1][1];
+        if (++slot == kDepth) slot = 0;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     // the warp's streams joined, pair by pair: both sides compute the same sums
+#pragma unroll
     for (int x = G; x < 32; x <<= 1) {
+        const float mo = __shfl_xor_sync(0xFFFFFFFFu, m, x), lo = __shfl_xor_sync(0xFFFFFFFFu, l, x);
+        const float m2 = fmaxf(m, mo), r = rescale(m, m2), ro = rescale(mo, m2);
+        l = __fadd_rn(__fmul_rn(l, r), __fmul_rn(lo, ro));
+        m = m2;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-            const float mo = __shfl_xor_sync(0xFFFFFFFFu, m[h], x), lo = __shfl_xor_sync(0xFFFFFFFFu, l[h], x);
-            const float m2 = fmaxf(m[h], mo), r = rescale(m[h], m2), ro = rescale(mo, m2);
-            l[h] = l[h] * r + lo * ro;
-            m[h] = m2;
+            const float rh = to_all(r, h), roh = to_all(ro, h);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float o = __shfl_xor_sync(0xFFFFFFFFu, acc[h][e], x);
-                acc[h][e] = __fadd_rn(__fmul_rn(acc[h][e], r), __fmul_rn(o, ro));
+            for (int e = 0; e < 4; ++e) {
+                const float ox = __shfl_xor_sync(0xFFFFFFFFu, acc[h][e].x, x);
+                const float oy = __shfl_xor_sync(0xFFFFFFFFu, acc[h][e].y, x);
+                acc[h][e].x = __fadd_rn(__fmul_rn(acc[h][e].x, rh), __fmul_rn(ox, roh));
+                acc[h][e].y = __fadd_rn(__fmul_rn(acc[h][e].y, rh), __fmul_rn(oy, roh));
             }
         }
     }
     // and the warps in order, in shared memory
-    const int W = D + 2, warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) < G) {
+    float* const sm = reinterpret_cast<float*>(raw + kWarps * kDepth * kSlot);
+    const int W = D + 2;
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-            float* o = sm + (warp * H + h) * W;
-            if (mine)
+    for (int h = 0; h < H; ++h) {
+        const float mh = to_all(m, h), lh = to_all(l, h);
+        if (lane >= G || h >= heads) continue;
+        float* o = sm + (warp * heads + h) * W;
+        if (mine)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[d0 + e] = acc[h][e];
-            if (sub == 0) o[D] = m[h], o[D + 1] = l[h];
-        }
+            for (int e = 0; e < 4; ++e) *reinterpret_cast<float2*>(o + d0 + 2 * e) = acc[h][e];
+        if (sub == 0) o[D] = mh, o[D + 1] = lh;
     }
     __syncthreads();
     const bool whole = p.C >= p.n;
@@ -188,22 +235,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode_rows(Args a, int lanes_log
         const int h = i / D, d = i - h * D;
         float mx = -INFINITY;
 #pragma unroll
-        for (int s = 0; s < kWarps; ++s) mx = fmaxf(mx, sm[(s * H + h) * W + D]);
+        for (int x = 0; x < kWarps; ++x) mx = fmaxf(mx, sm[(x * heads + h) * W + D]);
         float sum = 0.0f, o = 0.0f;
 #pragma unroll
-        for (int s = 0; s < kWarps; ++s) {
-            const float* x = sm + (s * H + h) * W;
-            if (x[D] == -INFINITY) continue;  // nothing seen; a weight of 0 still carries NaN on
-            const float r = ex2(x[D] - mx);
-            sum = fmaf(x[D + 1], r, sum), o = fmaf(x[d], r, o);
+        for (int x = 0; x < kWarps; ++x) {
+            const float* y = sm + (x * heads + h) * W;
+            if (y[D] == -INFINITY) continue;  // nothing seen; a weight of 0 still carries NaN on
+            const float r = ex2(y[D] - mx);
+            sum = fmaf(y[D + 1], r, sum), o = fmaf(y[d], r, o);
         }
         if (whole) {
-            Store<kF32>::store1(a.out, b * a.out_stride + (int64_t)(h0 + h) * D + d,
-                              mx == -INFINITY ? 0.0f : o / sum);
+            Store<kF32>::store1(a.out, p.b * a.out_stride + (int64_t)(h0 + h) * D + d,
+                                mx == -INFINITY ? 0.0f : o / sum);
         } else {
-            const int64_t row = ((int64_t)b * a.Hq + h0 + h) * a.split + p.chunk;
-            a.part_o[row * D + d] = o;
-            if (d == 0) a.part_ml[row] = make_float2(mx, sum);
+            const int64_t at = ((int64_t)p.b * a.Hq + h0 + h) * a.split + p.chunk;
+            a.part_o[at * D + d] = o;
+            if (d == 0) a.part_ml[at] = make_float2(mx, sum);
         }
     }
 }
@@ -276,17 +323,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join(Args a) {
     }
 }
 
-template <int KV, int H>
-cudaError_t go(Args a, int64_t B, cudaStream_t st) {
-    int lg = 0;
-    while ((8 << lg) < a.c.D) ++lg;
-    a.parts = (a.group + H - 1) / H;
-    const size_t smem = (size_t)kWarps * H * (a.c.D + 2) * 4;
+template <int KV, int H, int LG>
+cudaError_t run(Args a, int64_t B, cudaStream_t st) {
+    constexpr int rings = kWarps * (KV == GBE_KV_E4M3 ? 8 * 512 : 4 * 2048);
     static FunctionLimit limit;
-    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(decode_rows<KV, H>), kWarps * H * 258 * 4);
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(decode_rows<KV, H, LG>),
+                                      rings + kWarps * H * ((8 << LG) + 2) * 4);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(B * a.split * a.c.Hkv * a.parts));
-    return launch(decode_rows<KV, H>, grid, dim3(kThreads), smem, st, a, lg);
+    a.parts = (a.group + H - 1) / H;
+    const int smem = rings + kWarps * (a.group < H ? a.group : H) * (a.c.D + 2) * 4;
+    return launch(decode_rows<KV, H, LG>, dim3((unsigned)(B * a.split * a.c.Hkv * a.parts)), dim3(kThreads), smem, st,
+                  a);
+}
+
+template <int KV, int H>
+cudaError_t go(const Args& a, int64_t B, cudaStream_t st) {
+    if (a.c.D <= 64) return run<KV, H, 3>(a, B, st);
+    if (a.c.D <= 128) return run<KV, H, 4>(a, B, st);
+    return run<KV, H, 5>(a, B, st);
 }
 
 template <int KV>
