@@ -17,7 +17,15 @@
 namespace gbe {
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
+// Threads of a CTA: with four warps a chunk of f32 rows takes long enough to show
+// in small batches (17 sequences of up to 2000 tokens, 7 heads a kv head: 32 us,
+// 29 us with six, 22 us with eight; 64 x 4096, 8 heads a kv head: 606, 619 and
+// 702 us), with eight a chunk of 8-bit rows spends more on its ends (64 x 4096, 4
+// heads a kv head: 374 us, 322 us with four).
+template <int KV>
+constexpr int kThreadsOf = KV == GBE_KV_E4M3 ? 128 : 256;
+template <int KV, int H>
+constexpr int kResident = KV == GBE_KV_E4M3 ? (H == 8 ? 3 : 4) : H == 8 ? 1 : 2;  // CTAs an SM
 constexpr float kGrowth = 8.0f;  // powers of two that the maximum in use may lag
 using namespace decode;
 
@@ -41,8 +49,9 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void* p, bool ther
 // with one -- so H heads take log2(H) + log2(G) - 1 + (H / 2 - 1) shuffles in
 // place of H log2(G), and one exponential; the weights are passed back.
 template <int KV, int H, int LG>
-__global__ void __launch_bounds__(kThreads, H == 8 ? 3 : 4) decode_rows(Args a) {
+__global__ void __launch_bounds__(kThreadsOf<KV>, kResident<KV, H>) decode_rows(Args a) {
     constexpr bool E4 = KV == GBE_KV_E4M3;
+    constexpr int kThreads = kThreadsOf<KV>, kWarps = kThreads / 32;
     constexpr int G = 1 << LG, LH = H == 1 ? 0 : H == 2 ? 1 : H == 4 ? 2 : 3;
     constexpr int kPieces = E4 ? 1 : 2, kBytes = E4 ? 8 : 16;         // of k, and as many of v, for a lane and token
     constexpr int kDepth = E4 ? 8 : 4, kSlot = 2 * kPieces * kBytes * 32;  // of a warp
@@ -325,6 +334,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join(Args a) {
 
 template <int KV, int H, int LG>
 cudaError_t run(Args a, int64_t B, cudaStream_t st) {
+    constexpr int kThreads = kThreadsOf<KV>, kWarps = kThreads / 32;
     constexpr int rings = kWarps * (KV == GBE_KV_E4M3 ? 8 * 512 : 4 * 2048);
     static FunctionLimit limit;
     const cudaError_t e = limit.raise(reinterpret_cast<const void*>(decode_rows<KV, H, LG>),
