@@ -23,6 +23,10 @@
 // chunk meanwhile, and a CTA takes several chunks one after another where there
 // are enough of them.
 //
+// A bf16 cache takes weights as two bf16 each, 16 bits in all: the second product
+// with v costs nothing that HBM would not have taken anyway, and the result is
+// as good as its one rounding.
+//
 // e4m3: codes widen to f16 exactly (one conversion for two), so the products
 // are f16; a product may number its inner index and its rows as it likes, so
 // the order in which codes come out of ldmatrix is taken as it is.  q is
@@ -434,6 +438,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) decode_mma(Args a
                     uint32_t b0, b1;
                     if constexpr (decltype(half)::value) {
                         b0 = transpose8(f16x2(s[u][0], s[u][1])), b1 = transpose8(f16x2(s[u][2], s[u][3]));
+                    } else if constexpr (!E4) {  // cut off, not rounded
+                        b0 = transpose8(__byte_perm(__float_as_uint(s[u][0]), __float_as_uint(s[u][1]), 0x7632));
+                        b1 = transpose8(__byte_perm(__float_as_uint(s[u][2]), __float_as_uint(s[u][3]), 0x7632));
                     } else {
                         b0 = transpose8(f32x2_to_bf16x2_bits(s[u][0], s[u][1]));
                         b1 = transpose8(f32x2_to_bf16x2_bits(s[u][2], s[u][3]));
@@ -461,11 +468,21 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) decode_mma(Args a
                             }
                         }
                     } else {
+                        // the rest of each weight, cut off above, as a second bf16; never zero beside a weight that
+                        // is not, so that an infinity of v is not met by a zero
+                        float rest[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            rest[i] = fmaxf(s[u][i] - __uint_as_float(__float_as_uint(s[u][i]) & 0xFFFF0000u),
+                                            s[u][i] * 0x1p-30f);
+                        const uint32_t r0 = transpose8(f32x2_to_bf16x2_bits(rest[0], rest[1]));
+                        const uint32_t r1 = transpose8(f32x2_to_bf16x2_bits(rest[2], rest[3]));
                         const int r = 16 * u + (lane & 7) + (lane >> 4) * 8, c0 = lane >> 3 & 1;
 #pragma unroll
                         for (int x = 0; x < kTiles; ++x) {
                             uint32_t f[4];
                             ldmatrix4_trans(f, vb + S::at(r, 2 * x + c0));
+                            mma_bf16(o[x], f, r0, r1);
                             mma_bf16(o[x], f, b0, b1);
                         }
                     }

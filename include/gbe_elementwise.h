@@ -464,8 +464,9 @@ int gbe_kv_read(void *k, int64_t k_stride, void *v, int64_t v_stride, const int3
  *         done: calls in flight on other streams need their own.  May be NULL
  *         when 0 bytes are needed.
  * Sums, maxima and the softmax are f32; for bf16 queries the products go
- * through the tensor cores, with weights of 8 bits or more; results are
- * rounded once at the end.
+ * through the tensor cores, with weights of 16 bits over a bf16 cache and of
+ * 11 over an e4m3 one (8 where scales nearby differ by more than 2^8);
+ * results are rounded once at the end.
  * What lies in the cache behind a sequence's last token is not looked at
  * (infinities and NaN there stay there).  A NaN in an attended place gives
  * NaN; a row with nothing to attend to is zeros.
