@@ -48,6 +48,9 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void* p, bool ther
 // by halves -- a lane passes on half of its heads at every step, and ends up
 // with one -- so H heads take log2(H) + log2(G) - 1 + (H / 2 - 1) shuffles in
 // place of H log2(G), and one exponential; the weights are passed back.
+// Measured on a GB300: 64 x 4096 tokens, 32 heads of 128 over 8 kv heads, 523 us
+// (4.1 TB/s, bound by instructions, shuffles foremost; over e4m3 322 us); 17 x
+// up to 2000 tokens, 7 heads a kv head, 19 us (latency of a chunk and the join).
 template <int KV, int H, int LG>
 __global__ void __launch_bounds__(kThreadsOf<KV>, kResident<KV, H>) decode_rows(Args a) {
     constexpr bool E4 = KV == GBE_KV_E4M3;

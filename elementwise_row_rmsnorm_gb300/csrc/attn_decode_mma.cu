@@ -27,6 +27,11 @@
 // with v costs nothing that HBM would not have taken anyway, and the result is
 // as good as its one rounding.
 //
+// Measured on a GB300, 32 heads of 128 over 8 kv heads: 64 sequences of up to
+// 8192 tokens in bf16 165 us (6.5 TB/s, 0.97 of a plain copy's rate), 2 of 131072
+// 164 us; 64 of 8192 in e4m3 191 us (5.7 TB/s, 0.84), bound by the instructions
+// that widen codes and place pieces.
+//
 // e4m3: codes widen to f16 exactly (one conversion for two), so the products
 // are f16; a product may number its inner index and its rows as it likes, so
 // the order in which codes come out of ldmatrix is taken as it is.  q is

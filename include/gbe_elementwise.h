@@ -425,6 +425,9 @@ typedef struct gbe_kv_cache {
  *         zeroes) is given, counted.  The other slots must differ from one
  *         another: a slot that occurs twice holds bytes of either row.
  * Rows of the cache that no slot names are left as they were.
+ * Errors: GBE_ERR_DTYPE when the cache holds another type than dtype or e4m3,
+ * GBE_ERR_SHAPE for sizes and strides out of range, GBE_ERR_ALIGN, GBE_ERR_NULL,
+ * GBE_ERR_ALIAS and GBE_ERR_POINTER as everywhere.
  * T * Hkv is at most 2^30.  Alias: none (k and v may interleave in one buffer).
  */
 int gbe_kv_write(const void *k, int64_t k_stride, const void *v, int64_t v_stride, const int32_t *slots, int64_t T,
@@ -472,6 +475,8 @@ int gbe_kv_read(void *k, int64_t k_stride, void *v, int64_t v_stride, const int3
  * NaN; a row with nothing to attend to is zeros.
  * A row's bits depend on its own q, cache rows and length, and on Hq, Hkv, D,
  * page_size, max_pages: the same in a batch of any size.
+ * Errors: as for gbe_kv_write, GBE_ERR_SCALE, and GBE_ERR_WORKSPACE when
+ * workspace_bytes is too small.
  * Hq is a multiple of Hkv, at most 65536; max_pages * page_size at most 2^30;
  * B at most 2^20.
  */
@@ -501,6 +506,7 @@ int64_t gbe_attn_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
  * scale  : finite, usually 1 / sqrt(D).  D : a multiple of 8, 8 to 256.
  * Sums, maxima and the softmax are f32; results are rounded once at the end.
  * Alias : out overlaps nothing; q, k and v may interleave in one buffer.
+ * Errors : as for gbe_attn_decode.
  * A row's bits depend on its sequence alone, not on its place in the packing.
  * bf16 with D up to 128 and every row on the 16-byte grid, in device memory,
  * goes through the tensor cores, the weights rounded to bf16 for the second
