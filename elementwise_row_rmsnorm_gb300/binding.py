@@ -450,8 +450,14 @@ class KvCache:
     contiguous and share a stride (the halves k = kv[:, 0], v = kv[:, 1] of one
     [n_pages, 2, Hkv, page_size, D] tensor will do); a float8_e4m3fn cache also
     has k_scale and v_scale, uint8 [n_pages, Hkv, page_size].  Holds the
-    tensors and their description; no state of its own."""
-    __slots__ = ("k", "v", "k_scale", "v_scale", "shape", "desc")
+    tensors and the description of them that the library reads; the tensors
+    cannot be exchanged (make another KvCache, it holds no state of its own)."""
+    __slots__ = ("_tensors", "shape", "desc")
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
                  v_scale: torch.Tensor | None = None):
@@ -473,7 +479,7 @@ class KvCache:
             raise ValueError("KvCache: only a float8_e4m3fn cache has scales")
         if not (k.is_cuda and v.is_cuda and k_scale is None):
             _where(k, v, k_scale, v_scale)
-        self.k, self.v, self.k_scale, self.v_scale, self.shape = k, v, k_scale, v_scale, shape
+        self._tensors, self.shape = (k, v, k_scale, v_scale), shape
         # the bytes of a gbe_kv_cache, which the library reads during the call
         self.desc = _pack_cache(k.data_ptr(), v.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
                                 0 if v_scale is None else v_scale.data_ptr(), N, H, P, D, stride, kind)
@@ -591,11 +597,12 @@ def attn_decode(q, cache: KvCache, table, lens, scale: float | None = None, work
     out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if workspace is None:
         n = attn_decode_workspace(q.shape[0], q.shape[1], cache, table.shape[1])
-        if n:
+        if n and stream is None:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-            if stream is not None and workspace.is_cuda:  # it is released on return, while `stream` may still use it
-                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                        else torch.cuda.ExternalStream(_stream(stream)))
+        elif n:  # of the stream that uses it: what held the memory before, and what will after, is in order with it
+            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                                   else torch.cuda.ExternalStream(_stream(stream))):
+                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     gbe_attn_decode(q, out, cache, table, lens, 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale, workspace,
                     stream)
     return out

@@ -472,7 +472,10 @@ int gbe_kv_read(void *k, int64_t k_stride, void *v, int64_t v_stride, const int3
  * results are rounded once at the end.
  * What lies in the cache behind a sequence's last token is not looked at
  * (infinities and NaN there stay there).  A NaN in an attended place gives
- * NaN; a row with nothing to attend to is zeros.
+ * NaN; a logit of -infinity weighs nothing; a row with nothing to attend to, or
+ * with such logits alone, is zeros.
+ * Sums run in f32 before they are divided: scale * q, logits, and 2^8 times the
+ * number of tokens times the largest of v must stay within its range.
  * A row's bits depend on its own q, cache rows and length, and on Hq, Hkv, D,
  * page_size, max_pages: the same in a batch of any size.
  * Errors: as for gbe_kv_write, GBE_ERR_SCALE, and GBE_ERR_WORKSPACE when
@@ -512,7 +515,8 @@ int64_t gbe_attn_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
  * goes through the tensor cores, the weights rounded to bf16 for the second
  * product; other bf16 calls do not, and differ from it within that rounding.
  * An infinity or a NaN in an attended place makes the entries that it reaches
- * not finite.
+ * not finite, but for a logit of -infinity, which weighs nothing; the range of
+ * f32 bounds sums as in gbe_attn_decode.
  * Hq is a multiple of Hkv, at most 65536; T at most 2^28, n_seqs at most 2^24.
  */
 int gbe_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,

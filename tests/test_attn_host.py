@@ -157,3 +157,10 @@ def test_binding_checks():
         gbe.gbe_attn_prompt(q, q[:, :2], q[:, :2], q, torch.zeros(2), 1.0)
     with pytest.raises(ValueError):
         gbe.gbe_attn_prompt(q, q[:, :2], q[:, :2], q, torch.zeros(2, dtype=torch.int32), 1.0)  # not on a GPU
+
+
+def test_a_caches_tensors_cannot_be_exchanged():
+    """The description that the library reads was made of the tensors given."""
+    for name in ("k", "v", "k_scale", "v_scale"):
+        with pytest.raises(AttributeError):
+            setattr(gbe.KvCache.__new__(gbe.KvCache), name, torch.zeros(1))

@@ -320,3 +320,26 @@ def test_e4m3_magnitudes_that_make_up_for_one_another(dtype, power):
     table = torch.arange(13, dtype=torch.int32, device="cuda")[None]
     q = (_rand((1, Hq, D), F32, 13) * 2.0 ** power).to(dtype)
     _check(q, cache, table, [n], 0.125, f"2^{power}")
+
+
+def test_a_workspace_allocated_for_another_stream_is_that_streams():
+    """The memory is not one that work still queued on the current stream writes to."""
+    lens, Hq, H, D, P = [6000, 3000], 8, 2, 128, 64
+    cache, table = _filled(lens, P, H, D, BF, BF, 111)
+    q = _rand((2, Hq, D), BF, 113)
+    lens_t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want = gbe.attn_decode(q, cache, table, lens_t, 0.1)
+    n = gbe.attn_decode_workspace(2, Hq, cache, table.shape[1])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    big = torch.zeros(1 << 28, device="cuda")
+    for _ in range(3):
+        for _ in range(20):
+            big.add_(1.0)  # keeps the current stream busy
+        scratch = torch.empty(n, dtype=torch.uint8, device="cuda")
+        for _ in range(50):
+            scratch.fill_(0xFF)
+        del scratch  # its memory is free for the next allocation on the current stream
+        got = gbe.attn_decode(q, cache, table, lens_t, 0.1, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
