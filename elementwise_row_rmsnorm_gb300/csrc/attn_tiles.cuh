@@ -65,8 +65,9 @@ __device__ __forceinline__ SeqPiece find_piece(const int32_t* starts, int n_seqs
             const uint32_t has = __ballot_sync(0xFFFFFFFFu, c[x] > lo);
             const uint32_t k = __popc(has);
             if (r.index < 0) {
-                if (skip < k) {
-                    const int who = __fns(has, 0, (int)skip + 1);
+                if (skip < k) {  // the lane that has one and `skip` such lanes before it
+                    const bool it = c[x] > lo && __popc(has & ((1u << lane) - 1u)) == (int)skip;
+                    const int who = __ffs((int)__ballot_sync(0xFFFFFFFFu, it)) - 1;
                     r.begin = __shfl_sync(0xFFFFFFFFu, s[x], who);
                     r.len = __shfl_sync(0xFFFFFFFFu, n[x], who);
                     r.index = (int)lo;
