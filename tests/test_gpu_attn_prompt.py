@@ -192,3 +192,21 @@ def test_two_streams_at_once():
     for j in range(2):
         for o in outs[j]:
             assert torch.equal(o, want[j])
+
+
+@pytest.mark.parametrize("dtype,pad", [(F32, 0), (F32, 1), (BF, 1)])
+@pytest.mark.parametrize("D", [64, 96, 128])
+def test_a_sequence_has_the_same_bits_in_a_large_call(dtype, pad, D):
+    """Large calls may cut the rows otherwise than small ones (rows off the 16-byte grid: bf16 without tensor cores)."""
+    n, Hq, H, before, T = 333, 8, 2, 4000, 5200
+    q, k, v = _qkv(n, Hq, H, D, dtype, 31, pad=pad)
+    alone = gbe.attn_prompt(q, k, v, _i32([0, n]))
+    pq, pk, pv = _qkv(T, Hq, H, D, dtype, 32, pad=pad)
+    for dst, src in ((pq, q), (pk, k), (pv, v)):
+        dst[before:before + n] = src
+    starts = [0, 150, before, before + n, T]
+    out = gbe.attn_prompt(pq, pk, pv, _i32(starts))
+    assert torch.equal(out[before:before + n], alone)
+    part = slice(before + n, T)
+    want, tol, _ = attn_ref.prompt(pq[part], pk[part], pv[part], [0, T - before - n], 1.0 / math.sqrt(D), False)
+    attn_ref.assert_within(out[part], want, tol)
