@@ -3,6 +3,10 @@ projection's buffer, store k and v, attend over the prompt, then one token at
 a time over the cache -- each against the definition on what the cache holds,
 and the two attentions against each other."""
 import math
+import os
+import subprocess
+import sys
+import threading
 
 import numpy as np
 import pytest
@@ -105,3 +109,75 @@ def test_pinned_host_tensors(dtype, kind):
     want, tol, _ = attn_ref.prompt(q, k, v, [0, 60, n], scale, dtype == BF)
     attn_ref.assert_within(out.cuda(), want, tol, "prompt")
     assert torch.equal(dec.cuda(), gbe.attn_decode(q[:1], cache, table.cuda(), _i32([n]), scale))
+
+
+def test_the_first_calls_may_be_captured():
+    """A process whose first calls of every operator are made while a graph is captured."""
+    code = """
+import torch
+import elementwise_row_rmsnorm_gb300 as gbe
+for dtype in (torch.bfloat16, torch.float32):
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(200, 12, 64, generator=g, device="cuda").to(dtype)
+    q, k, v = x[:, :8], x[:, 8:10], x[:, 10:]
+    cache = gbe.kv_cache(20, 2, 64, 64, dtype)
+    slots = torch.arange(200, dtype=torch.int32, device="cuda")
+    table = torch.arange(20, dtype=torch.int32, device="cuda")[None]
+    starts, lens = (torch.tensor(t, dtype=torch.int32, device="cuda") for t in ([0, 200], [200]))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        a = gbe.attn_prompt(q, k, v, starts)
+        gbe.gbe_kv_write(k, v, slots, cache)
+        b = gbe.attn_decode(q[-1:], cache, table, lens)
+        kk, vv = gbe.kv_read(cache, slots)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(kk, k) and torch.equal(vv, v)
+    assert torch.equal(a, gbe.attn_prompt(q, k, v, starts))
+    assert torch.equal(b, gbe.attn_decode(q[-1:], cache, table, lens))
+    # the weights rounded to bf16 in one of them, and both results rounded
+    assert float((a[-1].float() - b[0].float()).abs().max()) <= 3 * 2.0 ** -8 * float(v.float().abs().max())
+print("done")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "done" in run.stdout, run.stderr[-2000:]
+
+
+def test_threads_call_at_once():
+    """Four host threads, each with a stream, a cache and a workspace of its own."""
+    P, H, Hq, D = 64, 2, 8, 128
+    want, got, sets = {}, {}, []
+    for i in range(4):
+        dtype = (torch.bfloat16, torch.float32)[i % 2]
+        g = torch.Generator(device="cuda").manual_seed(50 + i)
+        n = 1500 + 100 * i
+        x = torch.randn(n, Hq + 2 * H, D, generator=g, device="cuda").to(dtype)
+        sets.append((x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:], gbe.kv_cache(40, H, P, D, dtype),
+                     torch.randperm(40 * P, generator=g, device="cuda")[:n].to(torch.int32),
+                     torch.arange(40, dtype=torch.int32, device="cuda")[None],
+                     *(torch.tensor(t, dtype=torch.int32, device="cuda") for t in ([0, n], [40 * P]))))
+
+    def work(i, out):
+        q, k, v, cache, slots, table, starts, lens = sets[i]
+        gbe.gbe_kv_write(k, v, slots, cache)
+        out[i] = (gbe.attn_prompt(q, k, v, starts), gbe.attn_decode(q[-1:], cache, table, lens), *gbe.kv_read(cache, slots))
+
+    def many(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                work(i, got)
+            torch.cuda.current_stream().synchronize()
+
+    for i in range(4):
+        work(i, want)
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=many, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(4):
+        assert len(got[i]) == 4 and all(torch.equal(x, y) for x, y in zip(got[i], want[i])), i
