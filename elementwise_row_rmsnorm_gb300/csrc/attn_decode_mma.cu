@@ -29,7 +29,7 @@
 //
 // Measured on a GB300, 32 heads of 128 over 8 kv heads: 64 sequences of up to
 // 8192 tokens in bf16 165 us (6.5 TB/s, 0.97 of a plain copy's rate), 2 of 131072
-// 164 us; 64 of 8192 in e4m3 191 us (5.7 TB/s, 0.84), bound by the instructions
+// 164 us; 64 of 8192 in e4m3 190 us (5.7 TB/s, 0.85), bound by the instructions
 // that widen codes and place pieces.
 //
 // e4m3: codes widen to f16 exactly (one conversion for two), so the products
