@@ -572,6 +572,34 @@ def gbe_attn_prompt(q, k, v, out, starts, scale: float, stream=None) -> None:
 
 # ---- conveniences that allocate the outputs -------------------------------------------
 
+def _scratch(stream, shape, dtype, device):
+    """Uninitialised memory that work on `stream` (None: the current one) writes first.  It comes from that stream's own
+    pool, so that what held the memory before and what will after are in order with the call."""
+    if stream is None or torch.device(device).type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)  # (an ExternalStream of 0 would be a new stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty(stream, shape, dtype, device):
+    """Such memory for an output: the stream that is current may use it too, once it waits for `stream`, and it is handed
+    out again only when both are done with it."""
+    t = _scratch(stream, shape, dtype, device)
+    if stream is not None and t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _like(x: torch.Tensor, stream):
+    """A contiguous output of x's shape, type and device."""
+    if stream is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    return _empty(stream, x.shape, x.dtype, x.device)
+
+
 def kv_cache(n_pages: int, Hkv: int, page_size: int, D: int, dtype=torch.bfloat16, device="cuda") -> KvCache:
     """A zeroed cache; dtype torch.float8_e4m3fn for the 8-bit one."""
     k, v = (torch.zeros((n_pages, Hkv, page_size, D), dtype=dtype, device=device) for _ in range(2))
@@ -586,23 +614,18 @@ def kv_read(cache: KvCache, slots, dtype=None, stream=None):
     if dtype is None:
         dtype = torch.bfloat16 if cache.k.dtype == torch.float8_e4m3fn else cache.k.dtype
     shape = (slots.numel(), cache.shape[1], cache.shape[3])
-    k = torch.empty(shape, dtype=dtype, device=slots.device)
-    v = torch.empty_like(k)
+    k, v = (_empty(stream, shape, dtype, slots.device) for _ in range(2))
     gbe_kv_read(k, v, slots, cache, None, stream)
     return k, v
 
 
 def attn_decode(q, cache: KvCache, table, lens, scale: float | None = None, workspace=None, stream=None):
     """[B, Hq, D]; allocates the workspace unless one is given."""
-    out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    out = _like(q, stream)
     if workspace is None:
         n = attn_decode_workspace(q.shape[0], q.shape[1], cache, table.shape[1])
-        if n and stream is None:
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-        elif n:  # of the stream that uses it: what held the memory before, and what will after, is in order with it
-            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                                   else torch.cuda.ExternalStream(_stream(stream))):
-                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        if n:
+            workspace = _scratch(stream, n, torch.uint8, q.device)
     gbe_attn_decode(q, out, cache, table, lens, 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale, workspace,
                     stream)
     return out
@@ -610,79 +633,79 @@ def attn_decode(q, cache: KvCache, table, lens, scale: float | None = None, work
 
 def attn_prompt(q, k, v, starts, scale: float | None = None, stream=None):
     """[T, Hq, D]; rows outside [starts[0], starts[-1]) are not written."""
-    out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    out = _like(q, stream)
     gbe_attn_prompt(q, k, v, out, starts, 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale, stream)
     return out
 
 
 def rmsnorm(x, w, eps: float = 1e-5, out=None, stream=None):
-    y = torch.empty_like(x) if out is None else out
+    y = _like(x, stream) if out is None else out
     gbe_rmsnorm(x, w, y, eps, stream)
     return y
 
 
 def layernorm(x, g, b=None, eps: float = 1e-5, stream=None):
-    y = torch.empty_like(x)
+    y = _like(x, stream)
     gbe_layernorm(x, g, b, y, eps, stream)
     return y
 
 
 def add_rmsnorm(x, residual, w, eps: float = 1e-5, stream=None):
-    y, h = torch.empty_like(x), torch.empty_like(x)
+    y, h = _like(x, stream), _like(x, stream)
     gbe_add_rmsnorm(x, residual, w, y, h, eps, stream)
     return y, h
 
 
 def rope(x, pos, inv_freq, r: int, mu: float = 1.0, layout: int = 0, in_place: bool = False, stream=None):
-    y = x if in_place else torch.empty_like(x)
+    y = x if in_place else _like(x, stream)
     gbe_rope(x, y, pos, inv_freq, r, mu, layout, stream)
     return y
 
 
 def rope_cos_sin(inv_freq, r: int, cache_len: int, stream=None):
-    t = torch.empty((cache_len, r // 2, 2), dtype=torch.float32, device=inv_freq.device)
+    t = _empty(stream, (cache_len, r // 2, 2), torch.float32, inv_freq.device)
     gbe_rope_cos_sin(t, inv_freq, r, stream)
     return t
 
 
 def silu_mul(gate, up, stream=None):
-    y = torch.empty_like(gate)
+    y = _like(gate, stream)
     gbe_silu_mul(gate, up, y, stream)
     return y
 
 
 def add(a, b, stream=None):
-    y = torch.empty_like(a)
+    y = _like(a, stream)
     gbe_add(a, b, y, stream)
     return y
 
 
 def embedding(table, ids, bad_id_count=None, stream=None):
-    out = torch.empty((ids.numel(), table.shape[1]), dtype=table.dtype, device=table.device)
+    out = _empty(stream, (ids.numel(), table.shape[1]), table.dtype, table.device)
     gbe_embedding(table, ids, out, bad_id_count, stream)
     return out
 
 
 def argmax(x, stream=None):
-    out = torch.empty(x.shape[:-1], dtype=torch.int32, device=x.device)
+    out = _empty(stream, x.shape[:-1], torch.int32, x.device)
     gbe_argmax(x, out, stream)
     return out
 
 
 def sample_seeded(x, method: str, seed: int, offset: int = 0, temperature: float = 1.0, top_k: int = 1,
                   p: float = 1.0, stream=None):
-    out = torch.empty(x.shape[:-1], dtype=torch.int32, device=x.device)
+    out = _empty(stream, x.shape[:-1], torch.int32, x.device)
     gbe_sample_seeded(x, out, method, seed, offset, temperature, top_k, p, stream)
     return out
 
 
 def pcg64_uniforms(n: int, seed: int, offset: int = 0, device="cuda", stream=None):
-    u = torch.empty(n, dtype=torch.float32, device=device)
+    u = _empty(stream, n, torch.float32, device)
     gbe_pcg64_uniforms(u, seed, offset, stream)
     return u
 
 
 def sample(x, u, method: str, temperature: float = 1.0, top_k: int = 1, p: float = 1.0, stream=None):
-    out = torch.empty(x.shape[:-1], dtype=torch.int32, device=x.device)
+    out = _empty(stream, x.shape[:-1], torch.int32, x.device)
     gbe_sample(x, u, out, method, temperature, top_k, p, stream)
     return out
