@@ -36,8 +36,15 @@
 // of up to 500 tokens 27 us, bound by the latency of one to four blocks a tile.
 //
 // Masked weights are exact zeros, but zero times an infinity or a NaN in a
-// later row of v would reach the sum: rows that come out not finite are looked
-// at once more (repair_row).
+// later row of v would reach the sum.  Rows of v behind the sequence's end are
+// left out: of the block that crosses it, copies of 32, 8 and 1 rows bring those
+// before the end, and zeros (from behind the tensor's end) in place of the others.
+// That costs 0 to 3 % of a call of short prompts (100 of up to 50 tokens 45.9 ->
+// 47.1 us, 12 of up to 500 27.0 -> 27.4 us); the rows written over with zeros by
+// the softmax warps 3 to 9 %, by the issuing thread 1 to 5 %, copies of 8 and 1
+// rows 1 to 7 %, of every power of two 1 to 11 %.  Within the sequence, rows that
+// come out not finite are looked at once more (repair_row).  So a row's bits
+// depend on its own sequence alone.
 #include "attn_tiles.cuh"
 #include "gbe_elementwise.h"
 #include "launch.h"
@@ -160,16 +167,15 @@ __device__ __forceinline__ uint32_t not_finite4(const void* base, int64_t i) {
 
 // A row that came out not finite: right as it is where the keys that it attends
 // to made it so, but a weight of zero may also have met an infinity or a NaN of
-// v behind the mask, in rows row + 1 .. tile_end - 1 of the tile.  Computed
-// again only if an entry is not finite, has such a value behind the mask, and
-// has none before it.  By a whole warp; the row has been written.
-__device__ __noinline__ void repair_row(const PromptArgs& a, int begin, int row, int tile_end, int head) {
+// v behind the mask, in rows row + 1 .. end - 1, the sequence's in the tile.
+// Computed again only if an entry is not finite, has such a value behind the
+// mask, and has none before it.  By a whole warp; the row has been written.
+__device__ __noinline__ void repair_row(const PromptArgs& a, int begin, int row, int end, int head) {
     const int lane = threadIdx.x & 31, D = (int)a.D, kvh = head / (int)(a.Hq / a.Hkv);
     const bool mine = lane * 4 < D;
     const int64_t v0 = (int64_t)begin * a.v_stride + (int64_t)kvh * D + lane * 4;
     const int64_t out0 = (begin + (int64_t)row) * a.out_stride + (int64_t)head * D + lane * 4;
     uint32_t open = mine ? not_finite4(a.out, out0) : 0u;  // entries that may have to be computed again
-    const int end = (int)min((int64_t)tile_end, a.T - begin);
     uint32_t behind = 0;
     for (int j = row + 1; j < end && __any_sync(0xFFFFFFFFu, open & ~behind); j += 8)
 #pragma unroll
@@ -196,7 +202,9 @@ __device__ __forceinline__ uint32_t item_of(int round) {
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-              const __grid_constant__ CUtensorMap mv, PromptArgs a, uint32_t n_items) {
+              const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mv32,
+              const __grid_constant__ CUtensorMap mv8, const __grid_constant__ CUtensorMap mv1, PromptArgs a,
+              uint32_t n_items) {
     using S = Shape<DP>;
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
@@ -233,6 +241,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch(&mq);
         tma_prefetch(&mk);
         tma_prefetch(&mv);
+        tma_prefetch(&mv32);
+        tma_prefetch(&mv8);
+        tma_prefetch(&mv1);
     }
     pdl_begin();
     tc_fence_before();
@@ -305,10 +316,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         const uint32_t full = smem_addr(&ctl.kv_full[stage]);
                         mbar_arrive_tx(full, S::kTile);
+                        const uint32_t to = kv_smem + stage * S::kTile;
+                        const int row = w.begin + (x >> 1) * kN, have = w.len - (x >> 1) * kN;
+                        if (!(x & 1) || have >= kN) {
 #pragma unroll
-                        for (int p = 0; p < DP / 64; ++p)
-                            tma_load_3d(kv_smem + stage * S::kTile + p * S::kPanel, (x & 1) ? &mv : &mk, full, p * 64,
-                                        w.kvh, w.begin + (x >> 1) * kN);
+                            for (int p = 0; p < DP / 64; ++p)
+                                tma_load_3d(to + p * S::kPanel, (x & 1) ? &mv : &mk, full, p * 64, w.kvh, row);
+                        } else {  // v where the sequence ends within the block; from row T on there are zeros
+                            auto part = [&](const CUtensorMap* m, int r) {
+#pragma unroll
+                                for (int p = 0; p < DP / 64; ++p)
+                                    tma_load_3d(to + p * S::kPanel + r * 128, m, full, p * 64, w.kvh,
+                                                r < have ? row + r : (int)a.T);
+                            };
+#pragma unroll 1
+                            for (int r = 0; r < kN;) {
+                                const int left = have - r;
+                                if (r % 32 == 0 && (left >= 32 || left <= 0))
+                                    part(&mv32, r), r += 32;
+                                else if (r % 8 == 0 && (left >= 8 || left <= 0))
+                                    part(&mv8, r), r += 8;
+                                else
+                                    part(&mv1, r), ++r;
+                            }
+                        }
                         ++g;
                         if (x == 0) {  // q, once the last item's is done with
                             ok = mbar_wait(smem_addr(&ctl.q_empty), (i & 1) ^ 1, abort);
@@ -572,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (again) {
                 const int r = __ffs((int)again) - 1;
                 again &= again - 1;
-                repair_row(a, it.p.begin, row0 + r, u / group * kM + kM, head);
+                repair_row(a, it.p.begin, row0 + r, min(u / group * kM + kM, it.p.len), head);
             }
         }
         // a wait that gave up: NaN in every row of this CTA's tiles, done or not
@@ -611,14 +642,15 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-// [T, H, D] bf16 with a token stride, copied in boxes of 128 tokens of one
-// head and 64 entries (128 bytes, swizzled); zeros outside.
-bool encode(CUtensorMap* m, const void* p, int64_t T, int64_t H, int64_t D, int64_t stride) {
+// [T, H, D] bf16 with a token stride, copied in boxes of `rows` tokens of one
+// head and 64 entries (128 bytes, swizzled by the place in shared memory, so
+// that a box may begin at any row of a tile); zeros outside.
+bool encode(CUtensorMap* m, const void* p, int64_t T, int64_t H, int64_t D, int64_t stride, cuuint32_t rows) {
     const EncodeFn fn = encode_fn();
     if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {64, 1, 128}, step[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, 1, rows}, step[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, step,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -626,9 +658,10 @@ bool encode(CUtensorMap* m, const void* p, int64_t T, int64_t H, int64_t D, int6
 
 template <int DP>
 cudaError_t go(const PromptArgs& a, cudaStream_t st) {
-    CUtensorMap mq, mk, mv;
-    if (!encode(&mq, a.q, a.T, a.Hq, a.D, a.q_stride) || !encode(&mk, a.k, a.T, a.Hkv, a.D, a.k_stride) ||
-        !encode(&mv, a.v, a.T, a.Hkv, a.D, a.v_stride))
+    CUtensorMap mq, mk, mv, mv32, mv8, mv1;
+    if (!encode(&mq, a.q, a.T, a.Hq, a.D, a.q_stride, kM) || !encode(&mk, a.k, a.T, a.Hkv, a.D, a.k_stride, kN) ||
+        !encode(&mv, a.v, a.T, a.Hkv, a.D, a.v_stride, kN) || !encode(&mv32, a.v, a.T, a.Hkv, a.D, a.v_stride, 32) ||
+        !encode(&mv8, a.v, a.T, a.Hkv, a.D, a.v_stride, 8) || !encode(&mv1, a.v, a.T, a.Hkv, a.D, a.v_stride, 1))
         return cudaErrorNotSupported;
     constexpr int smem = Shape<DP>::kBytes;
     static FunctionLimit limit;
@@ -637,8 +670,8 @@ cudaError_t go(const PromptArgs& a, cudaStream_t st) {
     const int64_t group = a.Hq / a.Hkv, seqs = a.n_seqs < a.T ? a.n_seqs : a.T;
     const int64_t pairs = ((a.T / kM + seqs) * group + (group & 1 ? seqs : 0)) / 2;
     const int64_t items = pairs * a.Hkv, sms = sm_count();
-    return launch(prompt_tc<DP>, dim3((unsigned)(items < sms ? items : sms)), dim3(kThreads), smem, st, mq, mk, mv, a,
-                  (uint32_t)items);
+    return launch(prompt_tc<DP>, dim3((unsigned)(items < sms ? items : sms)), dim3(kThreads), smem, st, mq, mk, mv, mv32,
+                  mv8, mv1, a, (uint32_t)items);
 }
 
 }  // namespace
