@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, kResident<KV, H>) decode_rows(
         auto piece = [&](int first, float2 (&f)[4]) {
             float y[8];
             if constexpr (E4) {
-                const uint2 w = *reinterpret_cast<const uint2*>(from + first * kBytes * 32);
+                uint2 w = *reinterpret_cast<const uint2*>(from + first * kBytes * 32);
+                if (scales[0][first] == 0.0f) w = make_uint2(0u, 0u);  // zeros, whatever the codes
                 e4m3x4_to_f32(w.x, y);
                 e4m3x4_to_f32(w.y, y + 4);
             } else {

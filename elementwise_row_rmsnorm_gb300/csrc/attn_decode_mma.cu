@@ -345,6 +345,22 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) decode_mma(Args a
         __syncwarp();
         if (live[0] != 0) {
             const uint32_t kb = ring + stage * S::kStage, vb = kb + S::kHalf;
+            if constexpr (E4) {
+                // a row whose scale byte is 0 stands for zeros, whatever its codes
+                const uint32_t byte0 = (scales[0] & 0xFFu ? 0u : 1u) | (scales[0] >> 8 ? 0u : 2u);
+                const bool here = lane < S::kStep && (live[0] >> lane & 1u);
+                if (__any_sync(0xFFFFFFFFu, here && byte0)) {
+                    if (here) {
+                        uint8_t* const at = raw + (warp * NST + stage) * S::kStage;
+                        for (int c0 = 0; c0 < kPieces; ++c0) {
+                            uint4* const k = reinterpret_cast<uint4*>(at + S::at(lane, c0));
+                            if (byte0 & 1u) *k = make_uint4(0u, 0u, 0u, 0u);
+                            if (byte0 & 2u) *(k + S::kHalf / 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
 
             float s[SUB][4];  // tokens g (heads 2 t, 2 t + 1) and g + 8 of each group
 #pragma unroll
