@@ -394,6 +394,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pt = j - 1 < theirs ? 1 : 0, pj = j - 1;
                     }
                     if (pj < 0) pt = last_t;
+                    // A wait by parity holds only where the phase before has completed.  The second tile's thread has
+                    // passed over the first one's blocks of an item before that has no second tile: S of this item's
+                    // first block, once it is there, says that those have been read.
+                    if (t == 1 && j == 0 && last_t == 0)
+                        ok = ok && mbar_wait(smem_addr(&ctl.s_full[0]), done[0] & 1, abort);
                     if (pt >= 0)
                         ok = ok && mbar_wait(smem_addr(&ctl.s_free[pt]), (done[pt] + pj) & 1, abort);
                 };
