@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(kThreads* kGroups<DP>, DP == 64 ? 2 : 1) promp
     const unsigned index = blockIdx.x / (unsigned)a.Hq;
     if (threadIdx.x < 32) {
         const SeqPiece t = find_piece(a.starts, (int)a.n_seqs, (int)a.T, index,
-                                      [](int n) { return (uint32_t)((n + 8 * R - 1) / (8 * R)); });
+                                      [](int n) { return (uint32_t)((n + M - 1) / M); },
+                                      [](uint32_t rows, uint32_t seqs) { return rows / M + seqs; });
         if (threadIdx.x == 0) where = t;
     }
     __syncthreads();

@@ -92,7 +92,11 @@ struct Shape {
 
 __device__ __forceinline__ Pair find_pair(const int32_t* starts, int n_seqs, int T, int group, uint32_t index) {
     auto tiles = [&](int n) { return (uint32_t)((n + kM - 1) / kM) * (uint32_t)group; };
-    const SeqPiece p = find_piece(starts, n_seqs, T, index, [&](int n) { return (tiles(n) + 1) / 2; });
+    const SeqPiece p = find_piece(
+        starts, n_seqs, T, index, [&](int n) { return (tiles(n) + 1) / 2; },
+        [&](uint32_t rows, uint32_t seqs) {  // a sequence of an odd number of tiles leaves half a pair
+            return ((rows / kM + seqs) * (uint32_t)group + (group & 1 ? seqs : 0u)) / 2;
+        });
     if (p.index < 0) return {0, 0, 0, 0};
     return {p.begin, p.len, 2 * p.index, min(2, (int)tiles(p.len) - 2 * p.index)};
 }
