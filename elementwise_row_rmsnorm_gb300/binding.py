@@ -192,12 +192,13 @@ def gbe_rope(x, y, pos, inv_freq, r: int, mu: float = 1.0, layout: int = 0, stre
                                       _dt(x, y), _stream(stream)))
 
 
-def _rows_view(t: torch.Tensor, D: int):
+def _rows_view(t: torch.Tensor, D: int, what: str):
     """(T, H, token stride) of a [T, H, D] view whose heads and entries are
-    contiguous but whose tokens may be strided (a slice of a QKV buffer)."""
+    contiguous but whose tokens may be strided (a slice of a QKV buffer);
+    `what` is the call that a refusal names."""
     shape, st = t.shape, t.stride()  # one query each (the per-call host cost matters at decode sizes)
     if len(shape) != 3 or shape[2] != D or st[2] != 1 or (shape[1] > 1 and st[1] != D):
-        raise ValueError("rope_qk: operands are [T, H, D] views with contiguous heads")
+        raise ValueError(f"{what}: operands are [T, H, D] views with contiguous heads")
     return shape[0], shape[1], st[0] if shape[0] > 1 else shape[1] * D
 
 
@@ -216,8 +217,8 @@ def gbe_rope_qk(q, q_out, k, k_out, pos, inv_freq, r: int, mu: float = 1.0, layo
         if x is None:
             sides.append((None, None, 0, 0))
             continue
-        Tx, H, sx = _rows_view(x, D)
-        _, _, sy = _rows_view(y, D)
+        Tx, H, sx = _rows_view(x, D, "rope_qk")
+        _, _, sy = _rows_view(y, D, "rope_qk")
         if Tx != T or y.shape != x.shape or sx != sy:
             raise ValueError("rope_qk: an output has its input's shape and token stride")
         sides.append((x.data_ptr(), y.data_ptr(), sx, H))
@@ -258,8 +259,8 @@ def gbe_rope_pair(a, b, pos, stream=None) -> None:
             if not _on_device(t):
                 raise ValueError("tensors must be on the CUDA device or in pinned host memory")
         D = x.shape[2] if D is None else D
-        Tx, H, sx = _rows_view(x, D)
-        _, _, sy = _rows_view(y, D)
+        Tx, H, sx = _rows_view(x, D, "rope_pair")
+        _, _, sy = _rows_view(y, D, "rope_pair")
         T = Tx if T is None else T
         if Tx != T or y.shape != x.shape or sx != sy:
             raise ValueError("rope_pair: the operands share T and D; an output has its input's shape and stride")
@@ -292,8 +293,8 @@ def gbe_qk_norm_rope(q, q_out, gq, k, k_out, gk, eps: float, pos, inv_freq, r: i
         if x is None:
             sides.append((None, None, None, 0, 0))
             continue
-        Tx, H, sx = _rows_view(x, D)
-        _, _, sy = _rows_view(y, D)
+        Tx, H, sx = _rows_view(x, D, "qk_norm_rope")
+        _, _, sy = _rows_view(y, D, "qk_norm_rope")
         if Tx != T or y.shape != x.shape or sx != sy:
             raise ValueError("qk_norm_rope: an output has its input's shape and token stride")
         if g is None or g.numel() != D or not g.is_contiguous() or g.dtype != x.dtype:
@@ -493,10 +494,10 @@ def _where(*ts):
 
 
 def _kv_sides(what, k, v, cache, slots, bad):
-    T, H, sk = _rows_view(k, cache.shape[3])
+    T, H, sk = _rows_view(k, cache.shape[3], what)
     if v.shape != k.shape or H != cache.shape[1]:
         raise ValueError(f"{what}: k and v are [T, Hkv, D] with the cache's Hkv and D")
-    sv = sk if v.stride() == k.stride() else _rows_view(v, cache.shape[3])[2]
+    sv = sk if v.stride() == k.stride() else _rows_view(v, cache.shape[3], what)[2]
     if slots.dtype != torch.int32 or slots.numel() != T or not slots.is_contiguous():
         raise ValueError(f"{what}: slots is int32[T]")
     if bad is not None and (bad.dtype != torch.int32 or bad.numel() != 1):
@@ -532,10 +533,10 @@ def attn_decode_workspace(B: int, Hq: int, cache: KvCache, max_pages: int) -> in
 def gbe_attn_decode(q, out, cache: KvCache, table, lens, scale: float, workspace=None, stream=None) -> None:
     """q, out: [B, Hq, D]; table: int32[B, max_pages]; lens: int32[B], the new token included; workspace: any tensor
     of attn_decode_workspace bytes (None when that is 0)."""
-    B, Hq, sq = _rows_view(q, cache.shape[3])
+    B, Hq, sq = _rows_view(q, cache.shape[3], "attn_decode")
     if out.shape != q.shape:
         raise ValueError("attn_decode: out has q's shape")
-    so = sq if out.stride() == q.stride() else _rows_view(out, cache.shape[3])[2]
+    so = sq if out.stride() == q.stride() else _rows_view(out, cache.shape[3], "attn_decode")[2]
     rows = table.shape
     if table.dtype != torch.int32 or len(rows) != 2 or rows[0] != B or not table.is_contiguous():
         raise ValueError("attn_decode: table is int32[B, max_pages]")
@@ -556,10 +557,10 @@ def gbe_attn_prompt(q, k, v, out, starts, scale: float, stream=None) -> None:
     """q, out: [T, Hq, D], k, v: [T, Hkv, D] views with contiguous heads; starts: int32[n_seqs + 1]; rows outside
     [starts[0], starts[-1]) of out are left as they were."""
     D = q.shape[-1]
-    T, Hq, sq = _rows_view(q, D)
-    Tk, Hkv, sk = _rows_view(k, D)
-    Tv, Hv, sv = _rows_view(v, D)
-    _, _, so = _rows_view(out, D)
+    T, Hq, sq = _rows_view(q, D, "attn_prompt")
+    Tk, Hkv, sk = _rows_view(k, D, "attn_prompt")
+    Tv, Hv, sv = _rows_view(v, D, "attn_prompt")
+    _, _, so = _rows_view(out, D, "attn_prompt")
     if Tk != T or Tv != T or Hv != Hkv or out.shape != q.shape:
         raise ValueError("attn_prompt: q and out are [T, Hq, D], k and v [T, Hkv, D]")
     if starts.dtype != torch.int32 or starts.numel() < 1 or not starts.is_contiguous():
