@@ -218,7 +218,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = (int)(a.Hq / a.Hkv);
     volatile int* const abort = &ctl.abort;
 
-    if (warp == kMmaWarp) tmem_alloc(smem_addr(&ctl.tmem), 512);
     if (threadIdx.x == 0) {
         mbar_init(smem_addr(&ctl.q_full[0]), 1);
         mbar_init(smem_addr(&ctl.q_full[1]), 1);
@@ -250,6 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch(&mv1);
     }
     pdl_begin();
+    // (not ahead of it: a kernel before this one may have yet to take its share)
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(&ctl.tmem), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
