@@ -74,3 +74,26 @@ def test_a_million_sequences(dtype, n_seqs, T):
     b.synchronize()
     assert torch.equal(out, v.repeat_interleave(Hq // H, 1))
     assert a.elapsed_time(b) < 500.0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_offsets_past_32_bits(dtype):
+    """More than 2^31 entries of q and out, and as many bytes again behind column slices of one buffer."""
+    Hq, H, D, n, seqs = 16, 1, 128, 400, 2700
+    T = n * seqs
+    wide = torch.empty((T, Hq + 2 * H, D), dtype=dtype, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(7)
+    for a in range(0, T, n * 100):  # (no temporaries of the whole)
+        wide[a:a + n * 100] = torch.randn(wide[a:a + n * 100].shape, generator=g, device="cuda").to(dtype)
+    q, k, v = wide[:, :Hq], wide[:, Hq:Hq + H], wide[:, Hq + H:]
+    assert q.stride(0) * T > 2 ** 31
+    starts = torch.arange(0, T + 1, n, dtype=torch.int32, device="cuda")
+    out = torch.full((T, Hq, D), 9.0, dtype=dtype, device="cuda")
+    gbe.gbe_attn_prompt(q, k, v, out, starts, 0.1)
+    one = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    for b in (0, 1, seqs // 2, seqs - 800, seqs - 2, seqs - 1):
+        s = slice(b * n, (b + 1) * n)
+        assert torch.equal(out[s], gbe.attn_prompt(q[s], k[s], v[s], one, 0.1)), b
+    s = slice(T - n, T)
+    want, tol, _ = attn_ref.prompt(q[s], k[s], v[s], [0, n], 0.1, dtype == BF)
+    attn_ref.assert_within(out[s], want, tol)

@@ -131,3 +131,33 @@ def test_the_default_streams_handle():
         got = call(0)
         torch.cuda.synchronize()
         assert got.data_ptr() != mine and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("name", ["attn_decode", "kv_read", "attn_prompt", "rmsnorm"])
+@pytest.mark.parametrize("forked", [True, False])
+def test_calls_with_a_stream_may_be_captured(name, forked):
+    """On a stream forked from the capturing one, and on that one itself; replayed beside other work."""
+    call = _make(name)
+    want = [x.clone() for x in _outputs(call(None))]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        s = side if forked else here
+        if forked:
+            side.wait_stream(here)
+        dropped = call(s)
+        del dropped
+        got = _outputs(call(s))
+        if forked:
+            here.wait_stream(side)
+        sums = [x.float().sum() for x in got]
+    for _ in range(3):
+        graph.replay()
+        other = call(side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(torch.equal(a, b) for a, b in zip(_outputs(other), want))
+        assert all(torch.equal(a, b.float().sum()) for a, b in zip(sums, want))
+    del got, sums, graph
+    torch.cuda.synchronize()
