@@ -17,15 +17,16 @@
 namespace gbe {
 namespace {
 
-// Threads of a CTA: with four warps a chunk of f32 rows takes long enough to show
-// in small batches (17 sequences of up to 2000 tokens, 7 heads a kv head: 32 us,
-// 29 us with six, 22 us with eight; 64 x 4096, 8 heads a kv head: 606, 619 and
-// 702 us), with eight a chunk of 8-bit rows spends more on its ends (64 x 4096, 4
-// heads a kv head: 374 us, 322 us with four).
+// Threads of a CTA.  f32 rows: eight warps, for the small batches, where a chunk
+// walked by four takes long enough to show (17 sequences of up to 2000 tokens, 7
+// heads a kv head: 32 us with four, 29 with six, 22 with eight); a large batch
+// with 8 heads a kv head pays for it, an SM holding one CTA of eight warps (64 x
+// 4096: 606, 619 and 702 us).  8-bit rows: four, for with eight a chunk spends
+// more on its ends (64 x 4096, 4 heads a kv head: 374 us, 320 us with four).
 template <int KV>
 constexpr int kThreadsOf = KV == GBE_KV_E4M3 ? 128 : 256;
 template <int KV, int H>
-constexpr int kResident = KV == GBE_KV_E4M3 ? (H == 8 ? 3 : 4) : H == 8 ? 1 : 2;  // CTAs an SM
+constexpr int kResident = KV == GBE_KV_E4M3 ? (H == 8 ? 3 : 4) : H == 8 ? 1 : 2;  // CTAs an SM; of three 12 words spill
 constexpr float kGrowth = 8.0f;  // powers of two that the maximum in use may lag
 using namespace decode;
 
@@ -49,7 +50,7 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void* p, bool ther
 // with one -- so H heads take log2(H) + log2(G) - 1 + (H / 2 - 1) shuffles in
 // place of H log2(G), and one exponential; the weights are passed back.
 // Measured on a GB300: 64 x 4096 tokens, 32 heads of 128 over 8 kv heads, 523 us
-// (4.1 TB/s, bound by instructions, shuffles foremost; over e4m3 322 us); 17 x
+// (4.1 TB/s, bound by instructions, shuffles foremost; over e4m3 320 us); 17 x
 // up to 2000 tokens, 7 heads a kv head, 19 us (latency of a chunk and the join).
 template <int KV, int H, int LG>
 __global__ void __launch_bounds__(kThreadsOf<KV>, kResident<KV, H>) decode_rows(Args a) {

@@ -26,14 +26,21 @@
 // for each tile, overwritten by its weights, the next S had to wait for the
 // product with v, and a round of both tiles took 3300 clocks, not 2048.)
 //
+// Weights of one bf16, 8 bits, are what the second product takes beside a v of
+// bf16; the results are 1.2 to 1.3 times as far from the definition as their own
+// rounding leaves them (0.0019 and 0.0021 of their norm, 0.0016).  A second bf16
+// a weight, as decode keeps, would want 128 more columns than the 512 there are,
+// and 3072 clocks a round in place of 2048.
+//
 // O is rescaled only when a row's maximum has grown by more than 2^8 over the
 // one in use; until then weights go up to 2^8, which costs nothing in bf16 or
 // f32 (both floats) and keeps sums far from overflow.
 //
 // Measured on a GB300: one sequence of 8192 tokens, 32 heads of 128 over 8 kv
-// heads, 356 us (1.55 PFLOP/s, 0.79 of cuBLAS's bf16 rate), bound by the shared
+// heads, 355 us (1.55 PFLOP/s, 0.79 of cuBLAS's bf16 rate), bound by the shared
 // memory that the first product reads and by the softmax between; 12 sequences
 // of up to 500 tokens 27 us, bound by the latency of one to four blocks a tile.
+// (Of the softmax's 208 registers a thread five words spill.)
 //
 // Masked weights are exact zeros, but zero times an infinity or a NaN in a
 // later row of v would reach the sum.  Rows of v behind the sequence's end are
