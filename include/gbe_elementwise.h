@@ -404,7 +404,7 @@ typedef struct gbe_kv_cache {
  *
  * GBE_KV_E4M3: value = code * 2^(byte - 127), the code an e4m3 number (4
  * exponent and 3 mantissa bits, no infinities, largest 448), the byte one of
- * 1 .. 254; a row whose byte is 0 stands for zeros.
+ * 1 .. 254; a row whose byte is 0 stands for zeros, whatever its codes.
  */
 
 /*
