@@ -30,7 +30,7 @@
 // bf16; the results are 1.2 to 1.3 times as far from the definition as their own
 // rounding leaves them (0.0019 and 0.0021 of their norm, 0.0016).  A second bf16
 // a weight, as decode keeps, would want 128 more columns than the 512 there are,
-// and 3072 clocks a round in place of 2048.
+// and half as many clocks a round again.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 over the
 // one in use; until then weights go up to 2^8, which costs nothing in bf16 or
