@@ -97,3 +97,19 @@ def test_offsets_past_32_bits(dtype):
     s = slice(T - n, T)
     want, tol, _ = attn_ref.prompt(q[s], k[s], v[s], [0, n], 0.1, dtype == BF)
     attn_ref.assert_within(out[s], want, tol)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_starts_of_any_kind_reach_no_other_memory(dtype):
+    """Hundreds of entries outside [0, T], going back and forth: nothing outside out is written."""
+    T, Hq, H, D = 700, 3, 1, 64
+    g = torch.Generator().manual_seed(8)
+    q, k, v = (_rand((T, h, D), dtype, i) for i, h in enumerate((Hq, H, H)))
+    for n in (129, 300, 1000):
+        starts = torch.randint(-50, T + 50, (n + 1,), generator=g)
+        starts[::17], starts[5::23] = 2 ** 31 - 1, -2 ** 31
+        raw = torch.full((T + 400, Hq, D), 3.0, dtype=dtype, device="cuda")
+        gbe.gbe_attn_prompt(q, k, v, raw[200:200 + T], starts.to(torch.int32).cuda(), 0.125)
+        torch.cuda.synchronize()
+        assert bool((raw[:200] == 3.0).all()) and bool((raw[200 + T:] == 3.0).all())
+        assert bool(torch.isfinite(raw).all())
