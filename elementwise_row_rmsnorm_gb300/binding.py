@@ -81,6 +81,14 @@ def lib() -> ctypes.CDLL:
                 "gbe_attn_decode": [vp, i64, vp, i64, i64, i64, vp, vp, i64, vp, f32, vp, i64, i32, vp],
                 "gbe_attn_decode_workspace": [i64, i64, i64, i64, i64, i64],
                 "gbe_attn_prompt": [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, f32, i32, vp],
+                "gbe_rope_kv_write": [vp, vp, i64, i64, vp, i64, vp, i64, vp, vp, i64, i64, vp, vp, i64, f32, i32, vp, vp,
+                                      i32, vp],
+                "gbe_attn_decode_window": [vp, i64, vp, i64, i64, i64, vp, vp, i64, vp, i64, i64, f32, vp, i64, i32, vp],
+                "gbe_attn_decode_window_workspace": [i64, i64, i64, i64, i64, i64, i64, i64],
+                "gbe_attn_prompt_window": [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, i64, i64, f32,
+                                           i32, vp],
+                "gbe_attn_chunk": [vp, i64, vp, i64, vp, i64, i64, i64, vp, vp, i64, vp, i64, i64, f32, vp, i64, i32, vp],
+                "gbe_attn_chunk_workspace": [i64, i64, i64, i64, i64, i64, i64, i64, i64],
                 "gbe_version": [],
                 "gbe_last_cuda_error": [],
                 "gbe_status_string": [i32],
@@ -88,8 +96,8 @@ def lib() -> ctypes.CDLL:
             for name, args in sigs.items():
                 fn = getattr(L, name)
                 fn.argtypes = args
-                fn.restype = {"gbe_status_string": ctypes.c_char_p,
-                              "gbe_attn_decode_workspace": i64}.get(name, ctypes.c_int)
+                fn.restype = (ctypes.c_char_p if name == "gbe_status_string" else
+                              i64 if name.endswith("_workspace") else ctypes.c_int)
             _lib = L
     return _lib
 
@@ -521,54 +529,147 @@ def gbe_kv_read(k, v, slots, cache: KvCache, bad_slot_count=None, stream=None) -
                                             _stream(stream)))
 
 
-def attn_decode_workspace(B: int, Hq: int, cache: KvCache, max_pages: int) -> int:
-    """Bytes of workspace of gbe_attn_decode for B sequences of at most max_pages pages."""
+def gbe_rope_kv_write(q, q_out, k, v, pos, slots, cache: KvCache, inv_freq, r: int, mu: float = 1.0, layout: int = 0,
+                      cos_sin=None, bad_slot_count=None, stream=None) -> None:
+    """q (may be None), q_out, pos, inv_freq, r, mu, layout, cos_sin as for gbe_rope_qk, k, v, slots and bad_slot_count
+    as for gbe_kv_write: q_out is q rotated, and k rotated and v are stored; k is not changed."""
+    kp, sk, vp, sv, slots_p, T, desc, bad, _ = _kv_sides("rope_kv_write", k, v, cache, slots, bad_slot_count)
+    qp = op = None
+    sq = Hq = 0
+    if q is not None:
+        Tq, Hq, sq = _rows_view(q, cache.shape[3], "rope_kv_write")
+        if Tq != T or q_out.shape != q.shape or _rows_view(q_out, cache.shape[3], "rope_kv_write")[2] != sq:
+            raise ValueError("rope_kv_write: q is [T, Hq, D], and q_out has its shape and token stride")
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    if pos.dtype != torch.int32 or pos.numel() != T or not pos.is_contiguous():
+        raise ValueError("rope_kv_write: pos is int32[T]")
+    if inv_freq.dtype != torch.float32 or inv_freq.numel() < r // 2 or not inv_freq.is_contiguous():
+        raise ValueError("rope_kv_write: inv_freq is float32[r/2]")
+    cache_len = 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous() or (r and cos_sin.numel() % r):
+            raise ValueError("rope_kv_write: cos_sin is float32[cache_len, r/2, 2]")
+        cache_len = cos_sin.numel() // r if r else 0
+    _where(q, q_out, pos, inv_freq, cos_sin)
+    dtype = _dt(k, v) if q is None else _dt(q, q_out, k, v)
+    _check("gbe_rope_kv_write", lib().gbe_rope_kv_write(
+        qp, op, sq, Hq, kp, sk, vp, sv, pos.data_ptr(), slots_p, T, r, inv_freq.data_ptr(), _ptr(cos_sin), cache_len, mu,
+        layout, desc, bad, dtype, _stream(stream)))
+
+
+def attn_decode_workspace(B: int, Hq: int, cache: KvCache, max_pages: int, window: int = 0, sinks: int = 0) -> int:
+    """Bytes of workspace of gbe_attn_decode (of gbe_attn_decode_window, given a window) for B sequences of at most
+    max_pages pages."""
     _, H, P, D = cache.shape
-    n = lib().gbe_attn_decode_workspace(B, Hq, H, D, P, max_pages)
+    n = lib().gbe_attn_decode_window_workspace(B, Hq, H, D, P, max_pages, window, sinks)
     if n < 0:
         raise ValueError("attn_decode: sizes out of range (Hq a multiple of Hkv, D a multiple of 8 up to 256, ...)")
     return n
 
 
+def _decode_sides(what, q, out, cache, table, lens, workspace):
+    B, Hq, sq = _rows_view(q, cache.shape[3], what)
+    if out.shape != q.shape:
+        raise ValueError(f"{what}: out has q's shape")
+    so = sq if out.stride() == q.stride() else _rows_view(out, cache.shape[3], what)[2]
+    rows = table.shape
+    if table.dtype != torch.int32 or len(rows) != 2 or rows[0] != B or not table.is_contiguous():
+        raise ValueError(f"{what}: table is int32[B, max_pages]")
+    if lens.dtype != torch.int32 or lens.numel() != B or not lens.is_contiguous():
+        raise ValueError(f"{what}: lens is int32[B]")
+    if not (q.is_cuda and out.is_cuda and table.is_cuda and lens.is_cuda):
+        _where(q, out, table, lens)
+    at, room = _room(workspace)
+    return (q.data_ptr(), sq, out.data_ptr(), so, B, Hq, cache.desc, table.data_ptr(), rows[1], lens.data_ptr()), at, room
+
+
+def _room(workspace):
+    if workspace is None:
+        return None, 0
+    _dev(workspace)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def gbe_attn_decode(q, out, cache: KvCache, table, lens, scale: float, workspace=None, stream=None) -> None:
     """q, out: [B, Hq, D]; table: int32[B, max_pages]; lens: int32[B], the new token included; workspace: any tensor
     of attn_decode_workspace bytes (None when that is 0)."""
-    B, Hq, sq = _rows_view(q, cache.shape[3], "attn_decode")
+    args, at, room = _decode_sides("attn_decode", q, out, cache, table, lens, workspace)
+    _check("gbe_attn_decode", lib().gbe_attn_decode(*args, scale, at, room, _dt(q, out), _stream(stream)))
+
+
+def gbe_attn_decode_window(q, out, cache: KvCache, table, lens, window: int, sinks: int, scale: float, workspace=None,
+                           stream=None) -> None:
+    """As gbe_attn_decode, of the last `window` tokens (0: all) and the first `sinks`; workspace: attn_decode_workspace
+    bytes for them."""
+    args, at, room = _decode_sides("attn_decode_window", q, out, cache, table, lens, workspace)
+    _check("gbe_attn_decode_window", lib().gbe_attn_decode_window(*args, window, sinks, scale, at, room, _dt(q, out),
+                                                                  _stream(stream)))
+
+
+def attn_chunk_workspace(n_seqs: int, T: int, Hq: int, cache: KvCache, max_pages: int, window: int = 0,
+                         sinks: int = 0) -> int:
+    """Bytes of workspace of gbe_attn_chunk for T new tokens of n_seqs sequences of at most max_pages pages."""
+    _, H, P, D = cache.shape
+    n = lib().gbe_attn_chunk_workspace(n_seqs, T, Hq, H, D, P, max_pages, window, sinks)
+    if n < 0:
+        raise ValueError("attn_chunk: sizes out of range (Hq a multiple of Hkv, D a multiple of 8 up to 256, ...)")
+    return n
+
+
+def gbe_attn_chunk(q, out, cache: KvCache, starts, table, lens, scale: float, window: int = 0, sinks: int = 0,
+                   workspace=None, stream=None) -> None:
+    """q, out: [T, Hq, D] views with contiguous heads, the new tokens packed; starts: int32[n_seqs + 1]; table:
+    int32[n_seqs, max_pages]; lens: int32[n_seqs], the new tokens included; window 0: none; workspace: any tensor of
+    attn_chunk_workspace bytes (None when that is 0).  Rows outside [starts[0], starts[-1]) of out are left as they
+    were."""
+    D = cache.shape[3]
+    T, Hq, sq = _rows_view(q, D, "attn_chunk")
     if out.shape != q.shape:
-        raise ValueError("attn_decode: out has q's shape")
-    so = sq if out.stride() == q.stride() else _rows_view(out, cache.shape[3], "attn_decode")[2]
+        raise ValueError("attn_chunk: out has q's shape")
+    so = sq if out.stride() == q.stride() else _rows_view(out, D, "attn_chunk")[2]
+    n = lens.numel()
+    if starts.dtype != torch.int32 or starts.numel() != n + 1 or not starts.is_contiguous():
+        raise ValueError("attn_chunk: starts is int32[n_seqs + 1]")
+    if lens.dtype != torch.int32 or not lens.is_contiguous():
+        raise ValueError("attn_chunk: lens is int32[n_seqs]")
     rows = table.shape
-    if table.dtype != torch.int32 or len(rows) != 2 or rows[0] != B or not table.is_contiguous():
-        raise ValueError("attn_decode: table is int32[B, max_pages]")
-    if lens.dtype != torch.int32 or lens.numel() != B or not lens.is_contiguous():
-        raise ValueError("attn_decode: lens is int32[B]")
-    if not (q.is_cuda and out.is_cuda and table.is_cuda and lens.is_cuda):
-        _where(q, out, table, lens)
-    room = 0
-    if workspace is not None:
-        _dev(workspace)
-        room = workspace.numel() * workspace.element_size()
-    _check("gbe_attn_decode", lib().gbe_attn_decode(
-        q.data_ptr(), sq, out.data_ptr(), so, B, Hq, cache.desc, table.data_ptr(), rows[1], lens.data_ptr(), scale,
-        None if workspace is None else workspace.data_ptr(), room, _dt(q, out), _stream(stream)))
+    if table.dtype != torch.int32 or len(rows) != 2 or rows[0] != n or not table.is_contiguous():
+        raise ValueError("attn_chunk: table is int32[n_seqs, max_pages]")
+    if not (q.is_cuda and out.is_cuda and starts.is_cuda and table.is_cuda and lens.is_cuda):
+        _where(q, out, starts, table, lens)
+    at, room = _room(workspace)
+    _check("gbe_attn_chunk", lib().gbe_attn_chunk(
+        q.data_ptr(), sq, out.data_ptr(), so, starts.data_ptr(), n, T, Hq, cache.desc, table.data_ptr(), rows[1],
+        lens.data_ptr(), window, sinks, scale, at, room, _dt(q, out), _stream(stream)))
+
+
+def _prompt_sides(what, q, k, v, out, starts):
+    D = q.shape[-1]
+    T, Hq, sq = _rows_view(q, D, what)
+    Tk, Hkv, sk = _rows_view(k, D, what)
+    Tv, Hv, sv = _rows_view(v, D, what)
+    _, _, so = _rows_view(out, D, what)
+    if Tk != T or Tv != T or Hv != Hkv or out.shape != q.shape:
+        raise ValueError(f"{what}: q and out are [T, Hq, D], k and v [T, Hkv, D]")
+    if starts.dtype != torch.int32 or starts.numel() < 1 or not starts.is_contiguous():
+        raise ValueError(f"{what}: starts is int32[n_seqs + 1]")
+    _where(q, k, v, out, starts)
+    return (q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, out.data_ptr(), so, starts.data_ptr(),
+            starts.numel() - 1, T, Hq, Hkv, D)
 
 
 def gbe_attn_prompt(q, k, v, out, starts, scale: float, stream=None) -> None:
     """q, out: [T, Hq, D], k, v: [T, Hkv, D] views with contiguous heads; starts: int32[n_seqs + 1]; rows outside
     [starts[0], starts[-1]) of out are left as they were."""
-    D = q.shape[-1]
-    T, Hq, sq = _rows_view(q, D, "attn_prompt")
-    Tk, Hkv, sk = _rows_view(k, D, "attn_prompt")
-    Tv, Hv, sv = _rows_view(v, D, "attn_prompt")
-    _, _, so = _rows_view(out, D, "attn_prompt")
-    if Tk != T or Tv != T or Hv != Hkv or out.shape != q.shape:
-        raise ValueError("attn_prompt: q and out are [T, Hq, D], k and v [T, Hkv, D]")
-    if starts.dtype != torch.int32 or starts.numel() < 1 or not starts.is_contiguous():
-        raise ValueError("attn_prompt: starts is int32[n_seqs + 1]")
-    _where(q, k, v, out, starts)
-    _check("gbe_attn_prompt", lib().gbe_attn_prompt(
-        q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, out.data_ptr(), so, starts.data_ptr(),
-        starts.numel() - 1, T, Hq, Hkv, D, scale, _dt(q, k, v, out), _stream(stream)))
+    _check("gbe_attn_prompt", lib().gbe_attn_prompt(*_prompt_sides("attn_prompt", q, k, v, out, starts), scale,
+                                                    _dt(q, k, v, out), _stream(stream)))
+
+
+def gbe_attn_prompt_window(q, k, v, out, starts, window: int, sinks: int, scale: float, stream=None) -> None:
+    """As gbe_attn_prompt, a row seeing the last `window` rows up to itself (0: all) and the first `sinks`."""
+    _check("gbe_attn_prompt_window", lib().gbe_attn_prompt_window(
+        *_prompt_sides("attn_prompt_window", q, k, v, out, starts), window, sinks, scale, _dt(q, k, v, out),
+        _stream(stream)))
 
 
 # ---- conveniences that allocate the outputs -------------------------------------------
@@ -636,6 +737,43 @@ def attn_prompt(q, k, v, starts, scale: float | None = None, stream=None):
     """[T, Hq, D]; rows outside [starts[0], starts[-1]) are not written."""
     out = _like(q, stream)
     gbe_attn_prompt(q, k, v, out, starts, 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale, stream)
+    return out
+
+
+def attn_decode_window(q, cache: KvCache, table, lens, window: int, sinks: int = 0, scale: float | None = None,
+                       workspace=None, stream=None):
+    """[B, Hq, D], of the last `window` tokens (0: all) and the first `sinks`; allocates the workspace unless one is
+    given."""
+    out = _like(q, stream)
+    if workspace is None:
+        n = attn_decode_workspace(q.shape[0], q.shape[1], cache, table.shape[1], window, sinks)
+        if n:
+            workspace = _scratch(stream, n, torch.uint8, q.device)
+    gbe_attn_decode_window(q, out, cache, table, lens, window, sinks,
+                           1.0 / math.sqrt(q.shape[-1]) if scale is None else scale, workspace, stream)
+    return out
+
+
+def attn_prompt_window(q, k, v, starts, window: int, sinks: int = 0, scale: float | None = None, stream=None):
+    """[T, Hq, D], a row seeing the last `window` rows up to itself (0: all) and the first `sinks`; rows outside
+    [starts[0], starts[-1]) are not written."""
+    out = _like(q, stream)
+    gbe_attn_prompt_window(q, k, v, out, starts, window, sinks, 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale,
+                           stream)
+    return out
+
+
+def attn_chunk(q, cache: KvCache, starts, table, lens, scale: float | None = None, window: int = 0, sinks: int = 0,
+               workspace=None, stream=None):
+    """[T, Hq, D] of the new tokens packed in q; rows outside [starts[0], starts[-1]) are not written; allocates the
+    workspace unless one is given."""
+    out = _like(q, stream)
+    if workspace is None:
+        n = attn_chunk_workspace(lens.numel(), q.shape[0], q.shape[1], cache, table.shape[1], window, sinks)
+        if n:
+            workspace = _scratch(stream, n, torch.uint8, q.device)
+    gbe_attn_chunk(q, out, cache, starts, table, lens, 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale, window,
+                   sinks, workspace, stream)
     return out
 
 

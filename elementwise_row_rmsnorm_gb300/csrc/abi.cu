@@ -756,28 +756,102 @@ int gbe_kv_read(void* k, int64_t k_stride, void* v, int64_t v_stride, const int3
     return kv_rows(k, k_stride, v, v_stride, slots, T, cache, bad_slot_count, dtype, stream, false);
 }
 
+int gbe_rope_kv_write(const void* q, void* q_out, int64_t q_stride, int64_t Hq, const void* k, int64_t k_stride,
+                      const void* v, int64_t v_stride, const int32_t* pos, const int32_t* slots, int64_t T, int64_t r,
+                      const float* inv_freq, const float* cos_sin, int64_t cache_len, float mu, int layout,
+                      const gbe_kv_cache* cache, int32_t* bad_slot_count, int dtype, gbe_stream stream) {
+    const int es = elem_size(dtype);
+    if (!es) return GBE_ERR_DTYPE;
+    if (layout != 0 && layout != 1) return GBE_ERR_LAYOUT;
+    gbe::RopeKvArgs a = {};
+    Rows pages[2];
+    Buf cb[4];
+    int st = cache_form(cache, dtype, &a.c, pages, cb);
+    if (st != GBE_OK) return st;
+    const int64_t Hkv = a.c.Hkv, D = a.c.D;
+    if (Hq < 0 || Hq > 65536 || T < 0 || T > (1LL << 30) / (Hq + 2 * Hkv)) return GBE_ERR_SHAPE;
+    if ((Hq > 0 && rows_form(T, Hq, D, q_stride, es)) || rows_form(T, Hkv, D, k_stride, es) ||
+        rows_form(T, Hkv, D, v_stride, es))
+        return GBE_ERR_SHAPE;
+    if (r < 0 || r > D || (r & 1) || !std::isfinite(mu)) return GBE_ERR_ROTARY;
+    if (cos_sin != nullptr && cache_len < 0) return GBE_ERR_SHAPE;
+    if (T == 0) return GBE_OK;
+    int64_t nc = 0;
+    uint64_t bc = 0;
+    if (cos_sin != nullptr && (!mul_ok(cache_len, r / 2, &nc) || !extent(nc, 8, &bc))) return GBE_ERR_SHAPE;
+    const int64_t kv_width = Hkv * D * es, nq = Hq > 0 ? T : 0;
+    const Rows qi = {q, nq, q_stride * es, Hq * D * es}, qo = {q_out, nq, q_stride * es, Hq * D * es};
+    const Rows kr = {k, T, k_stride * es, kv_width}, vr = {v, T, v_stride * es, kv_width};
+    // 0 .. 5 = what is written: q_out, the cache, the counter; 6 .. 12 = what is read
+    Buf bufs[13] = {qo.extent(), cb[0], cb[1], cb[2], cb[3], {bad_slot_count, bad_slot_count ? 4u : 0u, 4},
+                    qi.extent(), kr.extent(), vr.extent(), {pos, (uint64_t)T * 4, 4}, {slots, (uint64_t)T * 4, 4},
+                    {inv_freq, (uint64_t)(r / 2) * 4, 4}, {cos_sin, bc, 8}};
+    bufs[0].align = bufs[6].align = bufs[7].align = bufs[8].align = (uint64_t)es;
+    for (const Buf& b : bufs)
+        if ((st = check_form(b)) != GBE_OK) return st;
+    // what is written shares no byte with anything else, but q_out may be q; q, k and v may interleave row by row
+    // (columns of one buffer), and so may the halves of the cache's pages
+    if (rows_overlap(pages[0], pages[1])) return GBE_ERR_ALIAS;
+    if (rows_overlap(qo, qi) && !rows_same(qo, qi)) return GBE_ERR_ALIAS;
+    if (rows_overlap(qo, kr) || rows_overlap(qo, vr)) return GBE_ERR_ALIAS;
+    for (int o = 0; o < 6; ++o)
+        for (int j = o + 1; j < 13; ++j) {
+            if ((o == 0 && j >= 6 && j <= 8) || (o == 1 && j == 2)) continue;  // (by rows, above)
+            if (overlaps(bufs[o], bufs[j])) return GBE_ERR_ALIAS;
+        }
+    Checker chk;
+    if ((st = chk.begin()) != GBE_OK) return st;
+    for (const Buf& b : bufs)
+        if ((st = chk.check(b)) != GBE_OK) return st;
+    const bool q_vec = Hq == 0 || (aligned16(q) && aligned16(q_out) && (q_stride * es) % 16 == 0);
+    const bool vec = q_vec && aligned16(k) && aligned16(v) && (k_stride * es) % 16 == 0 && (v_stride * es) % 16 == 0;
+    a.q = q, a.q_out = q_out, a.k = k, a.v = v;
+    a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+    a.pos = pos, a.slots = slots, a.T = T, a.Hq = (int)Hq, a.r = (int)r;
+    a.inv_freq = inv_freq, a.cos_sin = reinterpret_cast<const float2*>(cos_sin), a.cache_len = cos_sin ? cache_len : 0;
+    a.mu = mu, a.bad = bad_slot_count;
+    return finish(gbe::launch_rope_kv_write(a, layout, dtype, vec, as_stream(stream)));
+}
+
+// A window and its sinks as the kernels take them: no sequence has 2^31 tokens.
+static bool window_form(int64_t* window, int64_t* sinks) {
+    if (*window < 0 || *sinks < 0) return false;
+    *window = *window < (1LL << 30) ? *window : (1LL << 30);
+    *sinks = *window == 0 ? 0 : *sinks < (1LL << 30) ? *sinks : (1LL << 30);
+    return true;
+}
+
 // The sizes of a decode call that decide its workspace.
-static bool decode_sizes_ok(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size, int64_t max_pages) {
+static bool decode_sizes_ok(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size, int64_t max_pages,
+                            int64_t window, int64_t sinks) {
     if (B < 0 || B > (1 << 20) || Hkv < 1 || Hkv > 4096 || Hq < Hkv || Hq > 65536 || Hq % Hkv) return false;
     if (D < 8 || D > 256 || D % 8 || page_size < 1 || page_size > (1 << 20) || max_pages < 0) return false;
     if (max_pages > (1 << 30) / page_size) return false;
-    return B * gbe::decode_split(page_size, max_pages).split <= INT32_MAX / Hq;
+    return B * gbe::decode_split(page_size, max_pages, window, sinks).split <= INT32_MAX / Hq;
 }
 
-static uint64_t decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size, int64_t max_pages) {
-    const int64_t split = gbe::decode_split(page_size, max_pages).split;
+static uint64_t decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size, int64_t max_pages,
+                                 int64_t window, int64_t sinks) {
+    const int64_t split = gbe::decode_split(page_size, max_pages, window, sinks).split;
     return split == 1 ? 0u : (uint64_t)B * Hq * split * (D + 2) * 4;
+}
+
+int64_t gbe_attn_decode_window_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,
+                                         int64_t max_pages, int64_t window, int64_t sinks) {
+    if (!window_form(&window, &sinks)) return -1;
+    if (!decode_sizes_ok(B, Hq, Hkv, D, page_size, max_pages, window, sinks)) return -1;
+    return (int64_t)decode_workspace(B, Hq, Hkv, D, page_size, max_pages, window, sinks);
 }
 
 int64_t gbe_attn_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,
                                   int64_t max_pages) {
-    if (!decode_sizes_ok(B, Hq, Hkv, D, page_size, max_pages)) return -1;
-    return (int64_t)decode_workspace(B, Hq, Hkv, D, page_size, max_pages);
+    return gbe_attn_decode_window_workspace(B, Hq, Hkv, D, page_size, max_pages, 0, 0);
 }
 
-int gbe_attn_decode(const void* q, int64_t q_stride, void* out, int64_t out_stride, int64_t B, int64_t Hq,
-                    const gbe_kv_cache* cache, const int32_t* table, int64_t max_pages, const int32_t* lens,
-                    float scale, void* workspace, int64_t workspace_bytes, int dtype, gbe_stream stream) {
+int gbe_attn_decode_window(const void* q, int64_t q_stride, void* out, int64_t out_stride, int64_t B, int64_t Hq,
+                           const gbe_kv_cache* cache, const int32_t* table, int64_t max_pages, const int32_t* lens,
+                           int64_t window, int64_t sinks, float scale, void* workspace, int64_t workspace_bytes,
+                           int dtype, gbe_stream stream) {
     const int es = elem_size(dtype);
     if (!es) return GBE_ERR_DTYPE;
     gbe::KvCacheArgs c;
@@ -785,11 +859,12 @@ int gbe_attn_decode(const void* q, int64_t q_stride, void* out, int64_t out_stri
     Buf cb[4];
     int st = cache_form(cache, dtype, &c, pages, cb);
     if (st != GBE_OK) return st;
-    if (!decode_sizes_ok(B, Hq, c.Hkv, c.D, c.page_size, max_pages)) return GBE_ERR_SHAPE;
+    if (!window_form(&window, &sinks)) return GBE_ERR_SHAPE;
+    if (!decode_sizes_ok(B, Hq, c.Hkv, c.D, c.page_size, max_pages, window, sinks)) return GBE_ERR_SHAPE;
     if ((st = rows_form(B, Hq, c.D, q_stride, es)) || (st = rows_form(B, Hq, c.D, out_stride, es))) return st;
     if (!std::isfinite(scale)) return GBE_ERR_SCALE;
     if (B == 0) return GBE_OK;
-    const uint64_t need = decode_workspace(B, Hq, c.Hkv, c.D, c.page_size, max_pages);
+    const uint64_t need = decode_workspace(B, Hq, c.Hkv, c.D, c.page_size, max_pages, window, sinks);
     if (workspace_bytes < 0 || (uint64_t)workspace_bytes < need) return GBE_ERR_WORKSPACE;
     const Rows qr = {q, B, q_stride * es, Hq * c.D * es}, orow = {out, B, out_stride * es, Hq * c.D * es};
     Buf bufs[9] = {orow.extent(), {workspace, need, 16}, qr.extent(), cb[0], cb[1], cb[2], cb[3],
@@ -805,15 +880,25 @@ int gbe_attn_decode(const void* q, int64_t q_stride, void* out, int64_t out_stri
     if ((st = chk.begin()) != GBE_OK) return st;
     for (const Buf& b : bufs)
         if ((st = chk.check(b)) != GBE_OK) return st;
-    const gbe::DecodeArgs a = {q, out, q_stride, out_stride, c, table, lens, B, Hq, max_pages, scale, workspace};
+    const gbe::DecodeArgs a = {q, out, q_stride, out_stride, c, table, lens, B, Hq, max_pages, window, sinks, scale,
+                               workspace};
     return finish(gbe::launch_attn_decode(a, dtype, as_stream(stream)));
 }
 
-int gbe_attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
-                    void* out, int64_t out_stride, const int32_t* starts, int64_t n_seqs, int64_t T, int64_t Hq,
-                    int64_t Hkv, int64_t D, float scale, int dtype, gbe_stream stream) {
+int gbe_attn_decode(const void* q, int64_t q_stride, void* out, int64_t out_stride, int64_t B, int64_t Hq,
+                    const gbe_kv_cache* cache, const int32_t* table, int64_t max_pages, const int32_t* lens,
+                    float scale, void* workspace, int64_t workspace_bytes, int dtype, gbe_stream stream) {
+    return gbe_attn_decode_window(q, q_stride, out, out_stride, B, Hq, cache, table, max_pages, lens, 0, 0, scale,
+                                  workspace, workspace_bytes, dtype, stream);
+}
+
+int gbe_attn_prompt_window(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, void* out, int64_t out_stride, const int32_t* starts, int64_t n_seqs,
+                           int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t window, int64_t sinks, float scale,
+                           int dtype, gbe_stream stream) {
     const int es = elem_size(dtype);
     if (!es) return GBE_ERR_DTYPE;
+    if (!window_form(&window, &sinks)) return GBE_ERR_SHAPE;
     if (n_seqs < 0 || n_seqs > (1 << 24) || T < 0 || T > (1 << 28) || Hkv < 1 || Hq < Hkv || Hq > 65536 || Hq % Hkv)
         return GBE_ERR_SHAPE;
     if (D < 8 || D > 256 || D % 8) return GBE_ERR_SHAPE;
@@ -844,11 +929,92 @@ int gbe_attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_st
     for (const Rows& x : r) vec = vec && aligned16(x.p) && x.stride % 16 == 0;
     // (with more than one row a stride is bounded by its buffer's extent, checked above)
     if (T == 1) q_stride = out_stride = Hq * D, k_stride = v_stride = Hkv * D;
+    if (window > 0) {
+        gbe::ChunkArgs a = {};
+        a.q = q, a.k = k, a.v = v, a.out = out;
+        a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride, a.out_stride = out_stride;
+        a.starts = starts;
+        a.n_seqs = n_seqs, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.D = D;
+        a.window = window, a.sinks = sinks, a.scale = scale;
+        return finish(gbe::launch_attn_chunk(a, dtype, vec, !chk.off_device(), as_stream(stream)));
+    }
     const gbe::PromptArgs a = {q, k, v, out, q_stride, k_stride, v_stride, out_stride, starts, n_seqs, T, Hq, Hkv, D,
                                scale};
     // the tensor copies of the bf16 kernel are for device memory; elsewhere rows are read one by one
     if (chk.off_device() && dtype == GBE_BF16) vec = vec && D > 128;
     return finish(gbe::launch_attn_prompt(a, dtype, vec, as_stream(stream)));
+}
+
+int gbe_attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                    void* out, int64_t out_stride, const int32_t* starts, int64_t n_seqs, int64_t T, int64_t Hq,
+                    int64_t Hkv, int64_t D, float scale, int dtype, gbe_stream stream) {
+    return gbe_attn_prompt_window(q, q_stride, k, k_stride, v, v_stride, out, out_stride, starts, n_seqs, T, Hq, Hkv, D,
+                                  0, 0, scale, dtype, stream);
+}
+
+// The sizes of a chunk call that decide its workspace.
+static bool chunk_sizes_ok(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,
+                           int64_t max_pages) {
+    if (n_seqs < 0 || n_seqs > (1 << 24) || T < 0 || T > (1 << 28)) return false;
+    if (Hkv < 1 || Hkv > 4096 || Hq < Hkv || Hq > 65536 || Hq % Hkv) return false;
+    if (D < 8 || D > 256 || D % 8 || page_size < 1 || page_size > (1 << 20) || max_pages < 0) return false;
+    return max_pages <= (1 << 30) / page_size && T / 32 + n_seqs <= INT32_MAX / Hq;
+}
+
+static uint64_t chunk_workspace(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t keys,
+                                int64_t window, int64_t sinks) {
+    return n_seqs == 0 || T == 0
+               ? 0u : (uint64_t)gbe::chunk_room(n_seqs, T, Hq, Hkv, keys, window, sinks).entries * (D + 2) * 4;
+}
+
+int64_t gbe_attn_chunk_workspace(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,
+                                 int64_t max_pages, int64_t window, int64_t sinks) {
+    if (!window_form(&window, &sinks) || !chunk_sizes_ok(n_seqs, T, Hq, Hkv, D, page_size, max_pages)) return -1;
+    return (int64_t)chunk_workspace(n_seqs, T, Hq, Hkv, D, page_size * max_pages, window, sinks);
+}
+
+int gbe_attn_chunk(const void* q, int64_t q_stride, void* out, int64_t out_stride, const int32_t* starts,
+                   int64_t n_seqs, int64_t T, int64_t Hq, const gbe_kv_cache* cache, const int32_t* table,
+                   int64_t max_pages, const int32_t* lens, int64_t window, int64_t sinks, float scale,
+                   void* workspace, int64_t workspace_bytes, int dtype, gbe_stream stream) {
+    const int es = elem_size(dtype);
+    if (!es) return GBE_ERR_DTYPE;
+    gbe::ChunkArgs a = {};
+    Rows pages[2];
+    Buf cb[4];
+    int st = cache_form(cache, dtype, &a.c, pages, cb);
+    if (st != GBE_OK) return st;
+    const int64_t Hkv = a.c.Hkv, D = a.c.D;
+    if (!window_form(&window, &sinks)) return GBE_ERR_SHAPE;
+    if (!chunk_sizes_ok(n_seqs, T, Hq, Hkv, D, a.c.page_size, max_pages)) return GBE_ERR_SHAPE;
+    if ((st = rows_form(T, Hq, D, q_stride, es)) || (st = rows_form(T, Hq, D, out_stride, es))) return st;
+    if (!std::isfinite(scale)) return GBE_ERR_SCALE;
+    if (T == 0 || n_seqs == 0) return GBE_OK;
+    const uint64_t need = chunk_workspace(n_seqs, T, Hq, Hkv, D, a.c.page_size * max_pages, window, sinks);
+    if (workspace_bytes < 0 || (uint64_t)workspace_bytes < need) return GBE_ERR_WORKSPACE;
+    const Rows qr = {q, T, q_stride * es, Hq * D * es}, orow = {out, T, out_stride * es, Hq * D * es};
+    // 0, 1 = what is written; 2 = q; 3 .. 6 = the cache; 7 .. 9 = starts, table, lens
+    Buf bufs[10] = {orow.extent(), {workspace, need, 16}, qr.extent(), cb[0], cb[1], cb[2], cb[3],
+                    {starts, (uint64_t)(n_seqs + 1) * 4, 4}, {table, (uint64_t)(n_seqs * max_pages) * 4, 4},
+                    {lens, (uint64_t)n_seqs * 4, 4}};
+    bufs[0].align = bufs[2].align = (uint64_t)es;
+    for (const Buf& b : bufs)
+        if ((st = check_form(b)) != GBE_OK) return st;
+    for (int o = 0; o < 2; ++o)
+        for (int j = o + 1; j < 10; ++j)
+            if (o == 0 && j == 2 ? rows_overlap(orow, qr) : overlaps(bufs[o], bufs[j])) return GBE_ERR_ALIAS;
+    Checker chk;
+    if ((st = chk.begin()) != GBE_OK) return st;
+    for (const Buf& b : bufs)
+        if ((st = chk.check(b)) != GBE_OK) return st;
+    const bool vec = aligned16(q) && aligned16(out) && (q_stride * es) % 16 == 0 && (out_stride * es) % 16 == 0;
+    if (T == 1) q_stride = out_stride = Hq * D;
+    a.q = q, a.out = out, a.q_stride = q_stride, a.out_stride = out_stride;
+    a.table = table, a.lens = lens, a.max_pages = max_pages;
+    a.starts = starts, a.n_seqs = n_seqs, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.D = D;
+    a.window = window, a.sinks = sinks, a.scale = scale;
+    a.workspace = workspace;
+    return finish(gbe::launch_attn_chunk(a, dtype, vec, !chk.off_device(), as_stream(stream)));
 }
 
 }  // extern "C"

@@ -1,9 +1,10 @@
 // attn_decode.cu -- attention of one new token per sequence over the paged
 // key-value cache, split over the cache's length and joined.
 //
-//   out[b, h] = sum_j p_j v_j,  p = softmax_j(scale * q[b, h] . k_j),  j < lens[b]
+//   out[b, h] = sum_j p_j v_j,  p = softmax_j(scale * q[b, h] . k_j),  j < lens[b],
 //
-// with k_j, v_j the cached rows of kv head h / (Hq / Hkv).  One CTA takes one
+// under a window j >= lens[b] - window or j < sinks (attn_decode.cuh says how the
+// tokens between are passed over); with k_j, v_j the cached rows of kv head h / (Hq / Hkv).  One CTA takes one
 // chunk of one sequence's tokens for one kv head and up to H of its query
 // heads; the chunk's length is a function of the sequence's length alone
 // (chunk_tokens below), so a sequence's result has the same bits in a batch
@@ -52,7 +53,7 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void* p, bool ther
 // Measured on a GB300: 64 x 4096 tokens, 32 heads of 128 over 8 kv heads, 523 us
 // (4.1 TB/s, bound by instructions, shuffles foremost; over e4m3 320 us); 17 x
 // up to 2000 tokens, 7 heads a kv head, 19 us (latency of a chunk and the join).
-template <int KV, int H, int LG>
+template <int KV, int H, int LG, bool WINDOW>
 __global__ void __launch_bounds__(kThreadsOf<KV>, kResident<KV, H>) decode_rows(Args a) {
     constexpr bool E4 = KV == GBE_KV_E4M3;
     constexpr int kThreads = kThreadsOf<KV>, kWarps = kThreads / 32;
@@ -72,7 +73,12 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, kResident<KV, H>) decode_rows(
     const bool mine = d0 < D;
 
     // the stream's token that is fetched next, and its page
-    int tok = p.t0 + threadIdx.x / G, page_i = tok / c.page_size, row = tok - page_i * c.page_size;
+    int tok = p.t0 + threadIdx.x / G, page_i, row;
+    auto place = [&] {
+        const int t = WINDOW ? p.seen.token(tok) : tok;
+        page_i = t / c.page_size, row = t - page_i * c.page_size;
+    };
+    place();
     const int hop_pages = streams / c.page_size, hop_rows = streams - hop_pages * c.page_size;
     const int32_t* pages = a.table + (int64_t)p.b * a.max_pages;
     auto page_of = [&] { return tok < p.t1 ? pages[page_i] : -1; };
@@ -81,7 +87,7 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, kResident<KV, H>) decode_rows(
     uint32_t live = 0;  // bit i: the stream's token i steps ahead is there
     float scales[kDepth][2];
     auto fetch = [&](int slot, float (&sc)[2]) {
-        const bool good = page >= 0 && page < c.n_pages;
+        const bool good = page >= 0 && page < c.n_pages && (!WINDOW || p.seen.sees(p.seen.token(tok), a.sinks));
         int64_t at = 0;
         if (good) {
             at = page * c.page_stride + ((int64_t)p.kvh * c.page_size + row) * D + d0;
@@ -107,6 +113,7 @@ __global__ void __launch_bounds__(kThreadsOf<KV>, kResident<KV, H>) decode_rows(
         page_i += hop_pages;
         row += hop_rows;
         if (row >= c.page_size) row -= c.page_size, ++page_i;
+        if (WINDOW && tok >= p.seen.from && tok - streams < p.seen.from) place();  // past the gap
         page = page_of();
         return good;
     };
@@ -282,9 +289,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join(Args a) {
     const int64_t r = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.c.D;
     const int64_t b = r / a.Hq, h = r - b * a.Hq;
-    const int64_t capacity = (int64_t)a.max_pages * a.c.page_size;
-    const int32_t len = a.lens[b];
-    const int n = len < 0 ? 0 : (int)(len < capacity ? len : capacity);
+    const int n = find_seen(a, (int)b).n;
     const int C = chunk_tokens(n, a.split, a.least);
     if (C >= n) return;  // one chunk: already written
     const int chunks = (n + C - 1) / C;
@@ -337,33 +342,38 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join(Args a) {
     }
 }
 
-template <int KV, int H, int LG>
+template <int KV, int H, int LG, bool WINDOW>
 cudaError_t run(Args a, int64_t B, cudaStream_t st) {
     constexpr int kThreads = kThreadsOf<KV>, kWarps = kThreads / 32;
     constexpr int rings = kWarps * (KV == GBE_KV_E4M3 ? 8 * 512 : 4 * 2048);
     static FunctionLimit limit;
-    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(decode_rows<KV, H, LG>),
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(decode_rows<KV, H, LG, WINDOW>),
                                       rings + kWarps * H * ((8 << LG) + 2) * 4);
     if (e != cudaSuccess) return e;
     a.parts = (a.group + H - 1) / H;
     const int smem = rings + kWarps * (a.group < H ? a.group : H) * (a.c.D + 2) * 4;
-    return launch(decode_rows<KV, H, LG>, dim3((unsigned)(B * a.split * a.c.Hkv * a.parts)), dim3(kThreads), smem, st,
+    return launch(decode_rows<KV, H, LG, WINDOW>, dim3((unsigned)(B * a.split * a.c.Hkv * a.parts)), dim3(kThreads), smem, st,
                   a);
 }
 
-template <int KV, int H>
+template <int KV, int H, bool WINDOW>
 cudaError_t go(const Args& a, int64_t B, cudaStream_t st) {
-    if (a.c.D <= 64) return run<KV, H, 3>(a, B, st);
-    if (a.c.D <= 128) return run<KV, H, 4>(a, B, st);
-    return run<KV, H, 5>(a, B, st);
+    if (a.c.D <= 64) return run<KV, H, 3, WINDOW>(a, B, st);
+    if (a.c.D <= 128) return run<KV, H, 4, WINDOW>(a, B, st);
+    return run<KV, H, 5, WINDOW>(a, B, st);
+}
+
+template <int KV, bool WINDOW>
+cudaError_t pick_heads(const Args& a, int64_t B, cudaStream_t st) {
+    if (a.group == 1) return go<KV, 1, WINDOW>(a, B, st);
+    if (a.group == 2) return go<KV, 2, WINDOW>(a, B, st);
+    if (a.group <= 4) return go<KV, 4, WINDOW>(a, B, st);
+    return go<KV, 8, WINDOW>(a, B, st);
 }
 
 template <int KV>
 cudaError_t pick(const Args& a, int64_t B, cudaStream_t st) {
-    if (a.group == 1) return go<KV, 1>(a, B, st);
-    if (a.group == 2) return go<KV, 2>(a, B, st);
-    if (a.group <= 4) return go<KV, 4>(a, B, st);
-    return go<KV, 8>(a, B, st);
+    return a.window > 0 ? pick_heads<KV, true>(a, B, st) : pick_heads<KV, false>(a, B, st);
 }
 
 }  // namespace
@@ -372,20 +382,23 @@ cudaError_t pick(const Args& a, int64_t B, cudaStream_t st) {
 // partial results (4 * Hq / Hkv bytes written and read for every token and kv
 // head) than the SMs they bring in are worth.  128 chunks at most, so that two
 // sequences of 131072 tokens make 2048 CTAs.
-DecodeSplit decode_split(int64_t page_size, int64_t max_pages) {
+DecodeSplit decode_split(int64_t page_size, int64_t max_pages, int64_t window, int64_t sinks) {
     DecodeSplit s;
     s.least = 512;
-    const int64_t most = (page_size * max_pages + s.least - 1) / s.least;
+    int64_t tokens = page_size * max_pages;
+    if (window > 0 && window + sinks + 30 < tokens) tokens = window + sinks + 30;  // (both ends on 16 tokens' grid)
+    const int64_t most = (tokens + s.least - 1) / s.least;
     s.split = (int)(most < 1 ? 1 : most > kMostChunks ? kMostChunks : most);
     return s;
 }
 
 cudaError_t launch_attn_decode(const DecodeArgs& d, int dtype, cudaStream_t st) {
     Args a = {};
-    const DecodeSplit s = decode_split(d.c.page_size, d.max_pages);
+    const DecodeSplit s = decode_split(d.c.page_size, d.max_pages, d.window, d.sinks);
     a.q = d.q, a.out = d.out, a.q_stride = d.q_stride, a.out_stride = d.out_stride;
     a.c = d.c, a.table = d.table, a.lens = d.lens;
     a.Hq = (int)d.Hq, a.group = (int)(d.Hq / d.c.Hkv), a.max_pages = (int)d.max_pages;
+    a.window = (int)d.window, a.sinks = (int)d.sinks;
     a.split = s.split, a.least = s.least, a.run = 1;
     a.scale = d.scale * kLog2e;
     a.part_o = static_cast<float*>(d.workspace);

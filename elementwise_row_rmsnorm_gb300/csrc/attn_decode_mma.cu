@@ -131,7 +131,7 @@ struct Shape {
     }
 };
 
-template <int KV, int DP>
+template <int KV, int DP, bool WINDOW>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) decode_mma(Args a) {
     using S = Shape<KV, DP>;
     constexpr bool E4 = KV == GBE_KV_E4M3;
@@ -152,7 +152,12 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) decode_mma(Args a
     // every step: its page (-1: none) ...
     const int32_t* pages = a.table + (int64_t)p.b * a.max_pages;
     const int mine = lane & (S::kStep - 1);
-    int tok = p.t0 + warp * S::kStep + mine, page_i = tok / c.page_size, row = tok - page_i * c.page_size;
+    int tok = p.t0 + warp * S::kStep + mine, page_i, row;
+    auto place = [&] {
+        const int t = WINDOW ? p.seen.token(tok) : tok;
+        page_i = t / c.page_size, row = t - page_i * c.page_size;
+    };
+    place();
     const int hop_pages = S::kStride / c.page_size, hop_rows = S::kStride - hop_pages * c.page_size;
     auto page_of = [&] { return tok < p.t1 ? pages[page_i] : -1; };
     int32_t page = page_of();
@@ -165,7 +170,8 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) decode_mma(Args a
     // ... and, a step later, its rows on their way into stage `into`, entry `q` of the above
     auto fetch = [&](int into, uint32_t& lives, uint32_t& sc) {
         int64_t at = 0;
-        const bool here = page >= 0 && page < c.n_pages;
+        bool here = page >= 0 && page < c.n_pages;
+        if (WINDOW) here = here && p.seen.sees(p.seen.token(tok), a.sinks);
         sc = 0;
         if (here) {
             at = (page * c.page_stride + ((int64_t)p.kvh * c.page_size + row) * D) * es;
@@ -179,6 +185,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) decode_mma(Args a
         page_i += hop_pages;
         row += hop_rows;
         if (row >= c.page_size) row -= c.page_size, ++page_i;
+        if (WINDOW && tok >= p.seen.from && tok - S::kStride < p.seen.from) place();  // past the gap
         page = page_of();
         if (lives == 0) {  // nothing to copy, and the step will be passed over
             copies_commit();
@@ -526,14 +533,14 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 3 : 1) decode_mma(Args a
     copies_wait<0>();
 }
 
-template <int KV, int DP>
+template <int KV, int DP, bool WINDOW>
 cudaError_t go(Args a, int64_t B, cudaStream_t st) {
     using S = Shape<KV, DP>;
     const int heads = a.group < kHeads ? a.group : kHeads;
     const int smem = S::kRing + kWarps * heads * (DP + 2) * 4;
     constexpr int most = S::kRing + kWarps * kHeads * (DP + 2) * 4;
     static FunctionLimit limit;
-    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(decode_mma<KV, DP>), most);
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(decode_mma<KV, DP, WINDOW>), most);
     if (e != cudaSuccess) return e;
     a.parts = (a.group + kHeads - 1) / kHeads;
     // Several chunks to a CTA while that leaves eight waves of CTAs, of e4m3 four
@@ -543,20 +550,22 @@ cudaError_t go(Args a, int64_t B, cudaStream_t st) {
     const int64_t rows = B * a.c.Hkv * a.parts, want = rows * a.split / (kWaves * 3 * (int64_t)sm_count());
     a.run = (int)(want < 1 ? 1 : want > a.split ? a.split : want);
     const int64_t runs = (a.split + a.run - 1) / a.run;
-    return launch(decode_mma<KV, DP>, dim3((unsigned)(rows * runs)), dim3(kThreads), smem, st, a);
+    return launch(decode_mma<KV, DP, WINDOW>, dim3((unsigned)(rows * runs)), dim3(kThreads), smem, st, a);
 }
 
-template <int KV>
+template <int KV, bool WINDOW>
 cudaError_t pick(const Args& a, int64_t B, cudaStream_t st) {
-    if (a.c.D <= 64) return go<KV, 64>(a, B, st);
-    if (a.c.D <= 128) return go<KV, 128>(a, B, st);
-    return go<KV, 256>(a, B, st);
+    if (a.c.D <= 64) return go<KV, 64, WINDOW>(a, B, st);
+    if (a.c.D <= 128) return go<KV, 128, WINDOW>(a, B, st);
+    return go<KV, 256, WINDOW>(a, B, st);
 }
 
 }  // namespace
 
 cudaError_t launch_mma(Args a, int64_t B, cudaStream_t st) {
-    return a.c.dtype == GBE_KV_E4M3 ? pick<GBE_KV_E4M3>(a, B, st) : pick<GBE_KV_BF16>(a, B, st);
+    if (a.window > 0)
+        return a.c.dtype == GBE_KV_E4M3 ? pick<GBE_KV_E4M3, true>(a, B, st) : pick<GBE_KV_BF16, true>(a, B, st);
+    return a.c.dtype == GBE_KV_E4M3 ? pick<GBE_KV_E4M3, false>(a, B, st) : pick<GBE_KV_BF16, false>(a, B, st);
 }
 
 }  // namespace decode

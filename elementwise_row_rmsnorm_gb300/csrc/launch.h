@@ -117,12 +117,34 @@ cudaError_t launch_kv_write(const void* k, int64_t k_stride, const void* v, int6
 cudaError_t launch_kv_read(void* k, int64_t k_stride, void* v, int64_t v_stride, const int32_t* slots, int64_t T,
                            const KvCacheArgs& c, int32_t* bad, int dtype, bool vec, cudaStream_t st);
 
+// q turned into q_out, k turned and v as it is into the cache.
+struct RopeKvArgs {
+    const void* q;
+    void* q_out;
+    const void* k;
+    const void* v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t* pos;
+    const int32_t* slots;
+    int64_t T;
+    int Hq, r;
+    const float* inv_freq;
+    const float2* cos_sin;
+    int64_t cache_len;
+    float mu;
+    KvCacheArgs c;
+    int32_t* bad;
+};
+
+// vec: rows on the 16-byte grid.
+cudaError_t launch_rope_kv_write(const RopeKvArgs& a, int layout, int dtype, bool vec, cudaStream_t st);
+
 // How a sequence's tokens are cut into chunks that are attended to apart:
 // at most `split` chunks of at least `least` tokens.
 struct DecodeSplit {
     int split, least;
 };
-DecodeSplit decode_split(int64_t page_size, int64_t max_pages);
+DecodeSplit decode_split(int64_t page_size, int64_t max_pages, int64_t window, int64_t sinks);
 
 struct DecodeArgs {
     const void* q;
@@ -132,6 +154,7 @@ struct DecodeArgs {
     const int32_t* table;
     const int32_t* lens;
     int64_t B, Hq, max_pages;
+    int64_t window, sinks;  // window 0: every token
     float scale;
     void* workspace;
 };
@@ -153,5 +176,37 @@ struct PromptArgs {
 cudaError_t launch_attn_prompt(const PromptArgs& a, int dtype, bool vec, cudaStream_t st);
 // bf16 on the tensor cores: D <= 128, rows on the 16-byte grid.
 cudaError_t launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t st);
+
+// New rows of each sequence against the keys that they see: of a paged cache, or
+// (table == nullptr) of packed rows k and v of their own.
+struct ChunkArgs {
+    const void* q;
+    void* out;
+    int64_t q_stride, out_stride;
+    KvCacheArgs c;
+    const int32_t* table;
+    const int32_t* lens;
+    int64_t max_pages;
+    const void* k;
+    const void* v;
+    int64_t k_stride, v_stride;
+    const int32_t* starts;
+    int64_t n_seqs, T, Hq, Hkv, D;
+    int64_t window, sinks;  // window 0: every key up to the row's own place
+    float scale;
+    void* workspace;
+};
+
+// Partial results that a call may leave: at most `most` of a row, in `entries`
+// places of D + 2 floats each; per_seq places for each sequence, or (0) `most`
+// for each row of the packed buffers.
+struct ChunkRoom {
+    int most;
+    int64_t per_seq, entries;
+};
+ChunkRoom chunk_room(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t keys, int64_t window, int64_t sinks);
+
+// vec: rows on the 16-byte grid; tensor: and all of them in device memory.
+cudaError_t launch_attn_chunk(const ChunkArgs& a, int dtype, bool vec, bool tensor, cudaStream_t st);
 
 }  // namespace gbe

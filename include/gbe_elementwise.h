@@ -3,7 +3,8 @@
  * row-wise transformer ops: RMSNorm, fused residual add + RMSNorm, RoPE,
  * SiLU-mul, embedding gather, residual add, greedy argmax and sampling, and
  * the attention between them: the paged key-value cache and causal attention
- * over prompts and over that cache.
+ * over prompts, of one new token or a chunk of them over that cache, with or
+ * without a sliding window.
  *
  * Sources of the definitions (cited per entry point below):
  *   "Operations" -- the op math spec of the glia runtime (sections 1 to 10);
@@ -447,6 +448,28 @@ int gbe_kv_read(void *k, int64_t k_stride, void *v, int64_t v_stride, const int3
                 const gbe_kv_cache *cache, int32_t *bad_slot_count, int dtype, gbe_stream stream);
 
 /*
+ * gbe_rope_kv_write -- rotate q and k by their positions, write q, and store k
+ * and v into their slots, in one launch.
+ *   "Operations", section 3 (Rope) and KvCache append.  The results, q_out and
+ *   the bytes of the cache, are those of gbe_rope_qk of q and k (k rounded to
+ *   dtype) followed by gbe_kv_write, bit for bit; k itself is not changed.
+ * q, q_out : [T, Hq, D], both with token stride q_stride (q_out == q: in place;
+ *   then entries r .. D-1 are not touched).  Hq = 0: no q.  Rows of q are
+ *   rotated and written whatever their slot.
+ * k, v, k_stride, v_stride, slots, cache, bad_slot_count, dtype : as for
+ *   gbe_kv_write (-1: a token that is not stored; a bad one is not either, and
+ *   counted once).
+ * pos, inv_freq, r, mu, layout, cos_sin, cache_len : as for gbe_rope_qk; D is the
+ *   cache's.
+ * Alias: q_out == q; q, k and v may interleave in one buffer.  Nothing else.
+ * T * (Hq + 2 Hkv) is at most 2^30, Hq at most 65536.
+ */
+int gbe_rope_kv_write(const void *q, void *q_out, int64_t q_stride, int64_t Hq, const void *k, int64_t k_stride,
+                      const void *v, int64_t v_stride, const int32_t *pos, const int32_t *slots, int64_t T, int64_t r,
+                      const float *inv_freq, const float *cos_sin, int64_t cache_len, float mu, int layout,
+                      const gbe_kv_cache *cache, int32_t *bad_slot_count, int dtype, gbe_stream stream);
+
+/*
  * gbe_attn_decode -- attention of one new token of each of B sequences over
  * the paged cache.
  *   "Operations" (Sdpa with grouped heads), for one query token:
@@ -493,6 +516,27 @@ int64_t gbe_attn_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
                                   int64_t max_pages);
 
 /*
+ * gbe_attn_decode_window -- gbe_attn_decode under a sliding window: of the
+ * lens[b] = n tokens of sequence b the new one sees the last `window`, itself
+ * among them, and the first `sinks` (token j: j >= n - window or j < sinks).
+ *   "Operations" (SdpaWindow), with first tokens that stay visible.
+ * window : >= 0; 0 is none (then sinks mean nothing).  sinks : >= 0.
+ * The rest as for gbe_attn_decode, whose bits a window of n or more need not
+ * have.  What the cache holds between the sinks and the window is not looked at
+ * (pages there may have been given back, whatever their table entries say).
+ * workspace : gbe_attn_decode_window_workspace bytes; a narrow window needs
+ * fewer than a long table without one.
+ * A row's bits depend on what gbe_attn_decode's depend on, window and sinks.
+ */
+int gbe_attn_decode_window(const void *q, int64_t q_stride, void *out, int64_t out_stride, int64_t B, int64_t Hq,
+                           const gbe_kv_cache *cache, const int32_t *table, int64_t max_pages, const int32_t *lens,
+                           int64_t window, int64_t sinks, float scale, void *workspace, int64_t workspace_bytes,
+                           int dtype, gbe_stream stream);
+
+int64_t gbe_attn_decode_window_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,
+                                         int64_t max_pages, int64_t window, int64_t sinks);
+
+/*
  * gbe_attn_prompt -- causal attention over whole prompts, packed one behind
  * the other.
  *   "Operations" (Sdpa, causal mask, grouped heads): for row i of a
@@ -522,6 +566,62 @@ int64_t gbe_attn_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
 int gbe_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                     void *out, int64_t out_stride, const int32_t *starts, int64_t n_seqs, int64_t T, int64_t Hq,
                     int64_t Hkv, int64_t D, float scale, int dtype, gbe_stream stream);
+
+/*
+ * gbe_attn_prompt_window -- gbe_attn_prompt under a sliding window: row i of a
+ * sequence sees rows j <= i with j > i - window or j < sinks.
+ *   "Operations" (SdpaWindow, causal), with first tokens that stay visible.
+ * window, sinks : as for gbe_attn_decode_window; window 0 is gbe_attn_prompt.
+ * The rest as for gbe_attn_prompt; what lies outside a row's window stays there,
+ * infinities and NaN too.
+ */
+int gbe_attn_prompt_window(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                           int64_t v_stride, void *out, int64_t out_stride, const int32_t *starts, int64_t n_seqs,
+                           int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t window, int64_t sinks, float scale,
+                           int dtype, gbe_stream stream);
+
+/*
+ * gbe_attn_chunk -- attention of the new tokens of each of n_seqs sequences over
+ * the paged cache that holds their prefix and them: the next chunk of a long
+ * prompt, a prompt behind a shared prefix, drafts to be verified, or all of
+ * these and single tokens in one batch.
+ *   "Operations" (Sdpa with grouped heads, causal mask, KvCache).  Sequence s
+ *   has n = starts[s + 1] - starts[s] new tokens, the last n of the lens[s]
+ *   tokens in its pages (gbe_kv_write or gbe_rope_kv_write ahead of the call);
+ *   row i of them is at place p = lens[s] - n + i and sees tokens j <= p, under
+ *   a window j > p - window or j < sinks:
+ *   out[i, h] = sum_j p_j v_j, p = softmax over these j of scale * (q[i, h] . k_j),
+ *   k_j and v_j the rows of kv head h / (Hq / Hkv) as in gbe_attn_decode.
+ * q, out : [T, Hq, D] packed one sequence behind the other, each with its token
+ *   stride in elements; dtype.  out overlaps nothing.
+ * starts : device int32[n_seqs + 1] as for gbe_attn_prompt: none is allowed, rows
+ *   outside [starts[0], starts[n_seqs]) are left as they were.
+ * table  : device int32[n_seqs, max_pages]; lens : device int32[n_seqs].  As for
+ *   gbe_attn_decode: a token on a page outside the cache takes no part, a length
+ *   outside [0, max_pages * page_size] counts as the nearer end.  Rows at places
+ *   below 0 (a sequence of fewer cached than new tokens) see nothing: zeros.
+ * window, sinks : as for gbe_attn_decode_window; 0, 0: none.
+ * workspace : device memory of gbe_attn_chunk_workspace bytes at least, 16-byte
+ *   aligned, as for gbe_attn_decode.  May be NULL when 0 bytes are needed.
+ * Sums, maxima and the softmax are f32; results are rounded once at the end.
+ * Masked places take no part at all, whatever they hold; infinities, NaN and the
+ * range of f32 in attended places as in gbe_attn_prompt and gbe_attn_decode.
+ * A row's bits depend on its own sequence, on Hq, Hkv, D, page_size, max_pages,
+ * window and sinks: the same in a batch of any size and at any place in it.
+ * bf16 with D up to 128, q and out on the 16-byte grid, everything in device
+ * memory, goes through the tensor cores, the weights rounded to bf16 for the
+ * second product; other calls do not, and bf16 ones differ within that rounding.
+ * Errors : as for gbe_attn_decode.  Hq is a multiple of Hkv, at most 65536; T at
+ * most 2^28, n_seqs at most 2^24, max_pages * page_size at most 2^30.
+ */
+int gbe_attn_chunk(const void *q, int64_t q_stride, void *out, int64_t out_stride, const int32_t *starts,
+                   int64_t n_seqs, int64_t T, int64_t Hq, const gbe_kv_cache *cache, const int32_t *table,
+                   int64_t max_pages, const int32_t *lens, int64_t window, int64_t sinks, float scale,
+                   void *workspace, int64_t workspace_bytes, int dtype, gbe_stream stream);
+
+/* The bytes of workspace that gbe_attn_chunk needs; -1 when it would refuse the sizes. */
+int64_t gbe_attn_chunk_workspace(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,
+                                 int64_t max_pages, int64_t window, int64_t sinks);
 
 #ifdef __cplusplus
 }
