@@ -1,0 +1,817 @@
+// attn_chunk_tc.cu -- attention of new rows behind a cached prefix, and of packed
+// prompts under a sliding window, on the tensor cores: bf16 rows, D up to 128,
+// on the 16-byte grid.
+//
+//   S = q k^T (f32, in tensor memory), p = 2^(c S - c m), c = |scale| log2(e),
+//   O = sum p v, out = O / sum p
+//
+// over the keys that a row sees (attn_chunk.cuh).  A CTA goes from item to item:
+// one or two tiles of 128 rows -- tokens and the query heads of a kv head, so
+// that a few new tokens fill a tile and their keys are read once for all heads --
+// and a split of the blocks of 128 keys that they see.  Three warpgroups, as
+// attn_prompt_tc.cu has them: one of softmax for each tile (a thread owns a
+// row), and one of which a warp finds the items, another issues the tensor
+// copies, and two the products, each of a tile.  Tensor memory (512 columns)
+// holds one S for both tiles, the weights of each, rounded to bf16, and O of
+// each; the products follow one another as
+//
+//   S0 = q0 k(j+1)^T, O0 += p0 v(j), S1 = q1 k(j+1)^T, O1 += p1 v(j)
+//
+// Both tiles of an item walk the same blocks, so the one with the earlier rows
+// may meet a block that none of them sees: its weights are zeros.
+//
+// Pages come by tensor copies too, of as many rows as divide a page and a block;
+// each lane of the copying warp looks up the pages of its boxes a block ahead.
+// Rows of v that no row of the sequence may look at -- behind its end, on pages
+// that are not in the cache -- are zeros (from behind the tensor's end), since
+// a weight of zero times an infinity or a NaN would reach the sum; keys among
+// them are masked.  Within the sequence, a row that comes out not finite is
+// looked at once more (repair_row).
+//
+// O is rescaled only when a row's maximum has grown by more than 2^8 over the
+// one in use, as in attn_prompt_tc.cu.
+#include "attn_chunk.cuh"
+#include "gbe_elementwise.h"
+#include "kv_cache.cuh"
+#include "tensor_core.cuh"
+#include "tensor_map.h"
+
+namespace gbe {
+namespace chunk {
+namespace {
+
+constexpr int kM = 128, kN = 128;
+constexpr int kThreads = 384;  // three warpgroups: softmax of each tile, and the issuing warps
+constexpr int kLoadWarp = 8, kItemWarp = 9, kMmaWarp = 10;  // products: a warp for each tile
+constexpr float kGrowth = 8.0f;  // a maximum may lag this many powers of two
+constexpr int kPacked = -1;      // KV of rows that are not in a cache
+
+// What the item warp hands out; item.splits 0: nothing more.
+struct Todo {
+    Item item;
+    int kvh;
+};
+constexpr int kTodos = 4, kReaders = 11;  // items in hand; warps that read one: softmax, copies, products
+
+struct Control {
+    uint64_t q_full[2], q_empty, kv_full[8], kv_empty[8], s_full[2], s_free[2], p_ready[2], o_done[2], o_free[2];
+    uint64_t drained[2];
+    uint64_t todo_full[kTodos], todo_empty[kTodos];
+    Todo todo[kTodos];
+    uint32_t tmem;
+    int abort;
+};
+
+template <int DP>
+struct Shape {
+    static constexpr int kPanel = 128 * 128;              // 128 rows of 64 bf16
+    static constexpr int kTile = kPanel * (DP / 64);      // 128 rows of DP
+    static constexpr int kStages = DP == 128 ? 4 : 8;
+    static constexpr int kOut = 8 * 32 * 128;             // 32 rows of 128 bytes for each softmax warp
+    static constexpr int kBytes = kTile * (2 + kStages) + kOut + 1024 + (int)sizeof(Control);
+};
+
+// The copies of a call: q; k and v in boxes of `rows` keys, and v in smaller ones
+// (of 32, 8 and 1) where a sequence ends.
+struct Maps {
+    CUtensorMap q, k, v, v32, v8, v1;
+};
+
+// Row r of tile u: its token and head, and whether there is such a row.
+struct Row {
+    int token, head;
+    bool there;
+};
+__device__ __forceinline__ Row row_of(const Args& g, const Item& it, int u, int r) {
+    Row x;
+    const int token0 = u / g.parts * g.tokens, head0 = u % g.parts * g.heads;
+    x.token = token0 + r / g.heads;
+    x.head = head0 + r % g.heads;
+    x.there = r < g.tokens * g.heads && x.token < it.s.n && x.head < g.group;
+    return x;
+}
+
+// The row of key j in k and v; -1: it lies on no page of the cache.
+template <int KV>
+__device__ __forceinline__ int64_t key_at(const ChunkArgs& a, const Item& it, int kvh, int j) {
+    if constexpr (KV == kPacked) return it.s.begin + (int64_t)j;
+    const int page_i = j / a.c.page_size, row = j - page_i * a.c.page_size;
+    const int32_t page = a.table[it.seq * a.max_pages + page_i];
+    if (page < 0 || page >= a.c.n_pages) return -1;
+    return page * a.c.page_stride + ((int64_t)kvh * a.c.page_size + row) * a.D;
+}
+
+// Four consecutive values of a bf16 row, widened.
+__device__ __forceinline__ float4 load4(const void* base, int64_t i) {
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xFFFF0000u));
+}
+template <int KV, bool V>
+__device__ __forceinline__ float4 load_kv(const ChunkArgs& a, int kvh, int64_t at, int d) {
+    if constexpr (KV == kPacked)
+        return load4(V ? a.v : a.k, at * (V ? a.v_stride : a.k_stride) + (int64_t)kvh * a.D + d);
+    return load4(V ? a.c.v : a.c.k, at + d);
+}
+
+__device__ __forceinline__ uint32_t not_finite(float4 x) {
+    auto bad = [](float f) { return (__float_as_uint(f) & 0x7F800000u) == 0x7F800000u; };
+    return (bad(x.x) ? 1u : 0u) | (bad(x.y) ? 2u : 0u) | (bad(x.z) ? 4u : 0u) | (bad(x.w) ? 8u : 0u);
+}
+
+// Which keys of a block, as bits, a row at `place` sees: word x is of keys
+// k0 + 32 x and on.
+__device__ __forceinline__ uint32_t first_bits(int64_t n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+__device__ __forceinline__ uint32_t seen_word(const ChunkArgs& a, int place, int k0, int x) {
+    const int64_t at = k0 + 32 * x;
+    uint32_t m = first_bits(place + 1 - at);
+    if (a.window > 0) m &= ~first_bits(place + 1 - a.window - at) | first_bits(a.sinks - at);
+    return m;
+}
+
+// One row of an item in f32 from the keys that it sees alone, by a whole warp: 32
+// keys at a time, a lane a key for the logits, a lane four entries for the output.
+template <int KV>
+__device__ __noinline__ void exact_row(const Args& g, const Item& it, int kvh, int token, int head) {
+    const ChunkArgs& a = g.a;
+    const int lane = threadIdx.x & 31, D = (int)a.D, place = it.s.len - it.s.n + token;
+    const float c = a.scale * kLog2e;
+    const Walk w = walk(g, it, kN);
+    const int64_t row = (it.s.begin + (int64_t)token) * a.q_stride + ((int64_t)kvh * g.group + head) * D;
+    float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f), o = q;
+    if (lane * 4 < D) q = load4(a.q, row + lane * 4);
+    float m = -INFINITY, l = 0.0f;
+    for (int i = w.from * 4; i < w.to * 4; ++i) {
+        const int k0 = w.block(i >> 2) * kN + (i & 3) * 32, j = k0 + lane;
+        bool seen = seen_word(a, place, w.block(i >> 2) * kN, i & 3) >> lane & 1u;
+        const int64_t at = seen ? key_at<KV>(a, it, kvh, j) : -1;
+        seen = at >= 0;
+        if (!__any_sync(0xFFFFFFFFu, seen)) continue;
+        float s = 0.0f;
+        for (int d = 0; d < D; d += 4) {
+            const float4 k = seen ? load_kv<KV, false>(a, kvh, at, d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            s = fmaf(__shfl_sync(0xFFFFFFFFu, q.x, d >> 2), k.x, s);
+            s = fmaf(__shfl_sync(0xFFFFFFFFu, q.y, d >> 2), k.y, s);
+            s = fmaf(__shfl_sync(0xFFFFFFFFu, q.z, d >> 2), k.z, s);
+            s = fmaf(__shfl_sync(0xFFFFFFFFu, q.w, d >> 2), k.w, s);
+        }
+        s *= c;
+        // a NaN logit leaves a finite maximum, so that its NaN weight reaches the result
+        float mx = seen ? fmaxf(m, s == s ? s : -3.0e38f) : m;
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+        const float r = m == -INFINITY ? 0.0f : ex2(m - mx);
+        const float p = !seen || s == -INFINITY ? 0.0f : ex2(s - mx);
+        m = mx;
+        float sum = p;
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+        l = fmaf(l, r, sum);
+        o.x *= r, o.y *= r, o.z *= r, o.w *= r;
+        for (uint32_t left = __ballot_sync(0xFFFFFFFFu, seen); left; left &= left - 1) {
+            const int t = __ffs((int)left) - 1;
+            const float weight = __shfl_sync(0xFFFFFFFFu, p, t);
+            const int64_t from = __shfl_sync(0xFFFFFFFFu, at, t);
+            if (lane * 4 < D) {
+                const float4 v = load_kv<KV, true>(a, kvh, from, lane * 4);
+                o.x = fmaf(weight, v.x, o.x);
+                o.y = fmaf(weight, v.y, o.y);
+                o.z = fmaf(weight, v.z, o.z);
+                o.w = fmaf(weight, v.w, o.w);
+            }
+        }
+    }
+    const float y[4] = {o.x, o.y, o.z, o.w};
+    if (it.splits > 1) {
+        const int64_t part = part_at(g, it, token, kvh * g.group + head);
+        if (lane * 4 < D) *reinterpret_cast<float4*>(g.part_o + part * D + lane * 4) = o;
+        if (lane == 0) g.part_ml[part] = make_float2(m, l);
+    } else if (lane * 4 < D) {
+        const int64_t at = (it.s.begin + (int64_t)token) * a.out_stride + ((int64_t)kvh * g.group + head) * D + lane * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) Store<kBF16>::store1(a.out, at + e, m == -INFINITY ? 0.0f : y[e] / l);
+    }
+}
+
+// A row that came out not finite: right as it is where the keys that it sees
+// made it so, but a weight of zero may also have met an infinity or a NaN of v
+// in a key of its blocks that it does not see.  Computed again only if an entry
+// is not finite, has such a value there, and has none among the keys that it
+// sees.  By a whole warp; the row has been written.
+template <int KV>
+__device__ __noinline__ void repair_row(const Args& g, const Item& it, int kvh, int token, int head) {
+    const ChunkArgs& a = g.a;
+    const int lane = threadIdx.x & 31, D = (int)a.D, place = it.s.len - it.s.n + token;
+    const bool mine = lane * 4 < D;
+    const Walk w = walk(g, it, kN);
+    uint32_t open = 0;  // entries that may have to be computed again
+    if (mine) {
+        if (it.splits > 1)
+            open = not_finite(*reinterpret_cast<const float4*>(
+                g.part_o + part_at(g, it, token, kvh * g.group + head) * D + lane * 4));
+        else
+            open = not_finite(load4(a.out, (it.s.begin + (int64_t)token) * a.out_stride +
+                                               ((int64_t)kvh * g.group + head) * D + lane * 4));
+    }
+    // entries that a key of the blocks, seen or not, has no finite value in
+    auto among = [&](bool seen, uint32_t until) {
+        uint32_t bad = 0;
+        for (int i = (w.to - w.from) * 4 - 1; i >= 0; --i) {
+            if (!__any_sync(0xFFFFFFFFu, until & ~bad)) break;
+            const int k0 = w.block(w.from + (i >> 2)) * kN;
+            uint32_t keys = seen_word(a, place, k0, i & 3);
+            if (!seen) keys = ~keys & first_bits((int64_t)it.s.len - k0 - 32 * (i & 3));
+            for (; keys; keys &= keys - 1) {
+                const int64_t at = key_at<KV>(a, it, kvh, k0 + 32 * (i & 3) + __ffs((int)keys) - 1);
+                if (at >= 0 && mine) bad |= not_finite(load_kv<KV, true>(a, kvh, at, lane * 4));
+            }
+        }
+        return bad;
+    };
+    open &= among(false, open);
+    open &= ~among(true, open);
+    if (__any_sync(0xFFFFFFFFu, open)) exact_row<KV>(g, it, kvh, token, head);
+}
+
+// Work item `round` of this CTA: rounds go back and forth over the CTAs, so that
+// no CTA always gets the larger one.
+__device__ __forceinline__ uint64_t id_of(uint64_t round) {
+    return round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+// After a wait that gave up: NaN in every row of this CTA's items, done or not.
+// By one warp.
+__device__ __noinline__ void give_up(const Args& g) {
+    const ChunkArgs& a = g.a;
+    Finder finder(g);
+    for (uint64_t round = 0;; ++round) {
+        const uint64_t id = id_of(round);
+        const Item it = finder.find(id / (uint32_t)a.Hkv);
+        if (it.splits == 0) return;
+        const int kvh = (int)(id % (uint32_t)a.Hkv);
+        for (int r = threadIdx.x & 31; r < it.tiles * kM; r += 32) {
+            const Row x = row_of(g, it, it.tile + r / kM, r % kM);
+            if (!x.there) continue;
+            const int head = kvh * g.group + x.head;
+            if (it.splits > 1)
+                g.part_ml[part_at(g, it, x.token, head)] = make_float2(0.0f, __uint_as_float(0x7FC00000u));
+            uint16_t* const out =
+                static_cast<uint16_t*>(a.out) + (it.s.begin + (int64_t)x.token) * a.out_stride + (int64_t)head * a.D;
+            for (int d = 0; d < a.D; ++d) out[d] = 0x7FC0;
+        }
+    }
+}
+
+template <int KV, int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_tc(const __grid_constant__ Maps maps, const __grid_constant__ Args g, int box) {
+    using S = Shape<DP>;
+    extern __shared__ uint8_t raw[];
+    const ChunkArgs& a = g.a;
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    Control& ctl = *reinterpret_cast<Control*>(raw + (base - smem_addr(raw)) + S::kTile * (2 + S::kStages) + S::kOut);
+    const uint32_t q_smem = base, kv_smem = base + 2 * S::kTile;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* const abort = &ctl.abort;
+
+    if (threadIdx.x == 0) {
+        mbar_init(smem_addr(&ctl.q_empty), 2);
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(smem_addr(&ctl.kv_full[i]), 1);
+            mbar_init(smem_addr(&ctl.kv_empty[i]), 2);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_addr(&ctl.q_full[t]), 1);
+            mbar_init(smem_addr(&ctl.s_full[t]), 1);
+            mbar_init(smem_addr(&ctl.p_ready[t]), 4);
+            mbar_init(smem_addr(&ctl.s_free[t]), 4);
+            mbar_init(smem_addr(&ctl.o_done[t]), 1);
+            mbar_init(smem_addr(&ctl.o_free[t]), 4);
+            mbar_init(smem_addr(&ctl.drained[t]), 1);
+        }
+        for (int i = 0; i < kTodos; ++i) {
+            mbar_init(smem_addr(&ctl.todo_full[i]), 1);
+            mbar_init(smem_addr(&ctl.todo_empty[i]), kReaders);
+        }
+        ctl.abort = 0;
+        mbar_init_fence();
+        tma_prefetch(&maps.q);
+        tma_prefetch(&maps.k);
+        tma_prefetch(&maps.v);
+    }
+    pdl_begin();
+    // (not ahead of it: a kernel before this one may have yet to take its share)
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(&ctl.tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem;
+
+    // false: a wait gave up
+    auto todo_ready = [&](int i) { return mbar_wait(smem_addr(&ctl.todo_full[i % kTodos]), i / kTodos & 1, abort); };
+    auto todo_read = [&](int i) { mbar_arrive(smem_addr(&ctl.todo_empty[i % kTodos])); };
+
+    // Registers: 384 threads were launched with 168 each (64512); the softmax
+    // warpgroups take 208, the issuing one keeps 80 (63488 in all).
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == kItemWarp) {
+            Finder finder(g);
+            bool ok = true;
+            for (int i = 0; ok; ++i) {
+                const uint64_t id = id_of(i);
+                const Item it = finder.find(id / (uint32_t)a.Hkv);
+                ok = __all_sync(0xFFFFFFFFu,
+                                mbar_wait(smem_addr(&ctl.todo_empty[i % kTodos]), (i / kTodos & 1) ^ 1, abort));
+                if (!ok) break;
+                if (lane == 0) {
+                    ctl.todo[i % kTodos].item = it;
+                    ctl.todo[i % kTodos].kvh = (int)(id % (uint32_t)a.Hkv);
+                    mbar_arrive(smem_addr(&ctl.todo_full[i % kTodos]));
+                }
+                if (it.splits == 0) break;
+            }
+        } else if (warp == kLoadWarp) {
+            int loads = 0, tiles[2] = {0, 0};  // of the ring and tiles of q so far
+            int items = 0;                     // with a block
+            bool ok = true;
+            const int boxes = kN / box;        // of a block; a power of two
+            for (int i = 0; ok; ++i) {
+                if (!(ok = __all_sync(0xFFFFFFFFu, todo_ready(i)))) break;
+                const Item it = ctl.todo[i % kTodos].item;
+                const int kvh = ctl.todo[i % kTodos].kvh;
+                __syncwarp();
+                if (lane == 0) todo_read(i);
+                if (it.splits == 0) break;
+                const Walk w = walk(g, it, kN);
+                if (w.from == w.to) continue;
+                // box b of the walk's block x: the page (from n_pages on: zeros) and the row in it
+                auto look_up = [&](int x, int b, int& page, int& row) {
+                    const int j = w.block(x) * kN + b * box;
+                    if constexpr (KV == kPacked) {
+                        page = 0, row = it.s.begin + j;
+                    } else {
+                        page = (int)a.c.n_pages, row = 0;
+                        if (x < w.to && b < boxes && j < it.s.len) {
+                            const int page_i = j / a.c.page_size;
+                            const int32_t p = a.table[it.seq * a.max_pages + page_i];
+                            if (p >= 0 && p < a.c.n_pages) page = p, row = j - page_i * a.c.page_size;
+                        }
+                    }
+                };
+                auto copy = [&](uint32_t to, const CUtensorMap* m, uint32_t full, int page, int row) {
+#pragma unroll
+                    for (int p = 0; p < DP / 64; ++p) {
+                        if constexpr (KV == kPacked)
+                            tma_load_3d(to + p * S::kPanel, m, full, p * 64, kvh, row);
+                        else
+                            tma_load_4d(to + p * S::kPanel, m, full, p * 64, row, kvh, page);
+                    }
+                };
+                int page, row;
+                look_up(w.from, lane, page, row);
+                for (int x = w.from; ok && x < w.to; ++x) {
+                    const int have0 = it.s.len - w.block(x) * kN;  // of the block's rows
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const int stage = loads % S::kStages;
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.kv_empty[stage]),
+                                                               (loads / S::kStages & 1) ^ 1, abort));
+                        if (!ok) break;
+                        const uint32_t full = smem_addr(&ctl.kv_full[stage]), to = kv_smem + stage * S::kTile;
+                        if (lane == 0) mbar_arrive_tx(full, S::kTile);
+                        __syncwarp();
+                        for (int b = lane; b < boxes; b += 32) {
+                            if (b >= 32) look_up(x, b, page, row);
+                            const int have = have0 - b * box;
+                            const uint32_t at = to + b * box * 128;
+                            if (kv == 0 || have >= box || (KV != kPacked && (have <= 0 || page == a.c.n_pages))) {
+                                copy(at, kv == 0 ? &maps.k : &maps.v, full, page, row);
+                                continue;
+                            }
+                            // v where the sequence ends within the box: zeros from there on
+                            for (int r = 0; r < box;) {
+                                const int left = have - r;
+                                auto part = [&](const CUtensorMap* m, int rows) {
+                                    const bool zeros = left <= 0;
+                                    copy(at + r * 128, m, full, zeros ? (int)a.c.n_pages : page,
+                                         zeros && KV == kPacked ? (int)a.T : row + r);
+                                    r += rows;
+                                };
+                                if (r % 32 == 0 && box >= 32 && (left >= 32 || left <= 0))
+                                    part(&maps.v32, 32);
+                                else if (r % 8 == 0 && box >= 8 && (left >= 8 || left <= 0))
+                                    part(&maps.v8, 8);
+                                else
+                                    part(&maps.v1, 1);
+                            }
+                        }
+                        if (boxes > 32) look_up(x, lane, page, row);  // (the last one of these was looked up last)
+                        ++loads;
+                        if (kv == 0 && x == w.from) {  // q, once the last item's is done with
+                            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.q_empty), (items & 1) ^ 1, abort));
+                            if (!ok) break;
+                            ++items;
+                            for (int t = 0; t < it.tiles; ++t) {
+                                const int u = it.tile + t;
+                                if (lane == 0) {
+                                    const uint32_t qb = smem_addr(&ctl.q_full[t]);
+                                    mbar_arrive_tx(qb, (DP / 64) * 128 * g.heads * g.tokens);
+#pragma unroll
+                                    for (int p = 0; p < DP / 64; ++p)
+                                        tma_load_3d(q_smem + t * S::kTile + p * S::kPanel, &maps.q, qb, p * 64,
+                                                    kvh * g.group + u % g.parts * g.heads,
+                                                    it.s.begin + u / g.parts * g.tokens);
+                                }
+                                ++tiles[t];
+                            }
+                        }
+                    }
+                    look_up(x + 1, lane, page, row);
+                }
+            }
+            __syncwarp();
+            if (*abort && lane == 0) {  // nothing may still be on its way when the CTA ends
+                int none = 0;
+                for (int t = 0; t < 2; ++t)
+                    if (tiles[t] > 0) mbar_wait(smem_addr(&ctl.q_full[t]), (tiles[t] - 1) & 1, &none);
+                for (int x = max(0, loads - S::kStages); x < loads; ++x)
+                    mbar_wait(smem_addr(&ctl.kv_full[x % S::kStages]), x / S::kStages & 1, &none);
+            }
+        } else if (elect_one()) {
+            const int t = warp - kMmaWarp;
+            const uint32_t idesc_s = bf16_idesc(kM, kN, false) | (a.scale < 0.0f ? 1u << 13 : 0u);
+            constexpr uint32_t idesc_o = bf16_idesc(kM, DP, true), hi = smem_desc_hi(1024);
+            const uint32_t q_lo = smem_desc_lo(q_smem + t * S::kTile, 16), k_lo = smem_desc_lo(kv_smem, 16);
+            const uint32_t v_lo = smem_desc_lo(kv_smem, S::kPanel);
+            const uint32_t o = tmem + 256 + t * 128, pw = tmem + 128 + t * 64;
+            bool ok = true;
+            int loads = 0;          // the ring's before this item: k of block j is load loads + 2 j
+            int done[2] = {0, 0};   // blocks of each tile before this item
+            int items = 0;          // items with a tile t and a block
+            int every = 0;          // items with a block
+            int last_t = -1;        // the tile that S was last written for in the item before
+            for (int i = 0; ok; ++i) {
+                if (!(ok = todo_ready(i))) break;
+                const Item it = ctl.todo[i % kTodos].item;
+                todo_read(i);
+                if (it.splits == 0) break;
+                const Walk w = walk(g, it, kN);
+                const int n = w.to - w.from;
+                if (n == 0) continue;
+                const bool two = it.tiles == 2, mine = t == 0 || two;
+                auto loaded = [&](int x) {
+                    ok = ok && mbar_wait(smem_addr(&ctl.kv_full[x % S::kStages]), x / S::kStages & 1, abort);
+                };
+                // S is free once the block before in the order (0, j), (1, j), (0, j + 1), ... has been read
+                auto s_free = [&](int j) {
+                    const int pt = t == 1 ? 0 : j > 0 ? (two ? 1 : 0) : last_t, pj = t == 1 ? j : j - 1;
+                    // A wait by parity holds only where the phase before has completed.  The second tile's thread has
+                    // passed over the blocks of items before that have no second tile: S of this item's first block,
+                    // once it is there, says that those have been read.
+                    if (t == 1 && j == 0 && last_t == 0)
+                        ok = ok && mbar_wait(smem_addr(&ctl.s_full[0]), done[0] & 1, abort);
+                    if (pt >= 0) ok = ok && mbar_wait(smem_addr(&ctl.s_free[pt]), (done[pt] + pj) & 1, abort);
+                };
+                auto scores = [&](int j) {
+                    loaded(loads + 2 * j);
+                    s_free(j);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const int stage = (loads + 2 * j) % S::kStages;
+                    const uint32_t k0 = k_lo + stage * (S::kTile >> 4);
+#pragma unroll
+                    for (int x = 0; x < DP / 16; ++x) {
+                        const uint32_t off = ((x / 4) * S::kPanel + (x % 4) * 32) >> 4;
+                        mma_ss(tmem, q_lo + off, hi, k0 + off, hi, idesc_s, x > 0);
+                    }
+                    mma_commit(smem_addr(&ctl.s_full[t]));
+                    mma_commit(smem_addr(&ctl.kv_empty[stage]));
+                    if (j + 1 == n) mma_commit(smem_addr(&ctl.q_empty));
+                };
+                // (an item has a first tile always, a second one not)
+                ok = mine ? mbar_wait(smem_addr(&ctl.q_full[t]), items & 1, abort)
+                          : mbar_wait(smem_addr(&ctl.q_full[0]), every & 1, abort);
+                if (mine)
+                    scores(0);
+                else if (ok)
+                    mbar_arrive(smem_addr(&ctl.q_empty));
+                for (int j = 0; ok && mine && j < n; ++j) {
+                    if (j + 1 < n) scores(j + 1);
+                    loaded(loads + 2 * j + 1);
+                    ok = ok && mbar_wait(smem_addr(&ctl.p_ready[t]), (done[t] + j) & 1, abort);
+                    // O has been read for the last item
+                    if (j == 0 && items > 0) ok = ok && mbar_wait(smem_addr(&ctl.o_free[t]), (items - 1) & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int stage = (loads + 2 * j + 1) % S::kStages;
+                    const uint32_t v0 = v_lo + stage * (S::kTile >> 4);
+#pragma unroll
+                    for (int x = 0; x < kN / 16; ++x)
+                        mma_ts(o, pw + x * 8, v0 + x * (2048 >> 4), hi, idesc_o, j > 0 || x > 0);
+                    mma_commit(smem_addr(&ctl.o_done[t]));
+                    mma_commit(smem_addr(&ctl.kv_empty[stage]));
+                }
+                // blocks that only the other tile works on
+                for (int x = 0; ok && !mine && x < 2 * n; ++x) {
+                    loaded(loads + x);
+                    if (ok) mbar_arrive(smem_addr(&ctl.kv_empty[(loads + x) % S::kStages]));
+                }
+                loads += 2 * n;
+                done[0] += n;
+                if (two) done[1] += n;
+                items += mine;
+                ++every;
+                last_t = two ? 1 : 0;
+            }
+            // every product is done before tensor memory is given back
+            mma_commit(smem_addr(&ctl.drained[t]));
+            int none = 0;
+            mbar_wait(smem_addr(&ctl.drained[t]), 0, &none);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int t = warp >> 2;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
+        const uint32_t ts = tmem + lanes, tp = tmem + 128 + t * 64 + lanes, to = tmem + 256 + t * 128 + lanes;
+        // (never 0, so that c times the -inf of a masked place stays -inf)
+        const float c = fmaxf(fabsf(a.scale) * kLog2e, __uint_as_float(1u));
+        uint8_t* const stage = raw + (base - smem_addr(raw)) + S::kTile * (2 + S::kStages) + warp * (S::kOut / 8);
+        bool ok = true;
+        int done = 0;  // blocks of this tile before this item
+        for (int i = 0; ok; ++i) {
+            ok = __all_sync(0xFFFFFFFFu, todo_ready(i));
+            if (!ok) break;
+            const Item it = ctl.todo[i % kTodos].item;
+            const int kvh = ctl.todo[i % kTodos].kvh;
+            __syncwarp();
+            if (lane == 0) todo_read(i);
+            if (it.splits == 0) break;
+            if (t >= it.tiles) continue;
+            const Walk w = walk(g, it, kN);
+            const int u = it.tile + t;
+            const Row mine = row_of(g, it, u, threadIdx.x & 127);
+            const int place = it.s.len - it.s.n + mine.token;
+            // the places of the warp's rows: from .. to
+            const int place_from = __shfl_sync(0xFFFFFFFFu, place, 0), place_to = __shfl_sync(0xFFFFFFFFu, place, 31);
+            float m = -INFINITY, l = 0.0f;
+            for (int x = w.from; x < w.to; ++x) {
+                const int j = x - w.from, k0 = w.block(x) * kN;
+                // pages of the block that are not in the cache
+                bool gone = false;
+                if constexpr (KV != kPacked) {
+                    const int first = k0 / a.c.page_size, last = min(k0 + kN, it.s.len) - 1;
+                    for (int p = first + lane; p * (int64_t)a.c.page_size <= last; p += 32) {
+                        const int32_t page = a.table[it.seq * a.max_pages + p];
+                        gone = gone || page < 0 || page >= a.c.n_pages;
+                    }
+                    gone = __any_sync(0xFFFFFFFFu, gone);
+                }
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.s_full[t]), (done + j) & 1, abort));
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t s[128];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) tmem_ld32(ts + y * 32, s + y * 32);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) tmem_wait_ld32(s + y * 32);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ctl.s_free[t]));
+                // whether a row of the warp does not see a key of the block
+                if (gone || k0 + kN - 1 > place_from ||
+                    (a.window > 0 && k0 <= place_to - a.window && k0 + kN > a.sinks)) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        uint32_t seen = seen_word(a, place, k0, y);
+                        if (KV != kPacked && gone) {
+                            const int key = k0 + 32 * y + lane;
+                            const bool here = key < it.s.len && key_at<KV>(a, it, kvh, key) >= 0;
+                            seen &= __ballot_sync(0xFFFFFFFFu, here);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[32 * y + e] = seen >> e & 1u ? s[32 * y + e] : 0xFF800000u;
+                    }
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int y = 0; y < 128; y += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[y + e]), __uint_as_float(s[y + 4 + e])));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const bool grow = m == -INFINITY ? top > m : (top - m) * c > kGrowth;
+                auto last_done = [&] {  // the product with the last weights is done
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.o_done[t]), (done + j - 1) & 1, abort));
+                    tc_fence_after();
+                };
+                if (__any_sync(0xFFFFFFFFu, grow)) {
+                    const float m2 = grow ? top : m;
+                    if (j > 0) {
+                        last_done();
+                        if (!ok) break;
+                        const float r = m == -INFINITY ? 0.0f : ex2((m - m2) * c);
+                        l *= r;
+#pragma unroll
+                        for (int y = 0; y < DP / 32; ++y) {
+                            uint32_t o[32];
+                            tmem_ld32(to + y * 32, o);
+                            tmem_wait_ld32(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
+                            tmem_st32(to + y * 32, o);
+                        }
+                    }
+                    m = m2;
+                }
+                const float shift = m == -INFINITY ? 0.0f : -m * c;
+                const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+                float2 sum[4] = {};
+                uint32_t p[64];
+#pragma unroll
+                for (int e = 0; e < 64; ++e) {
+                    float2 y = fma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2,
+                                       shift2);
+                    y.x = ex2(y.x), y.y = ex2(y.y);
+                    sum[e & 3] = add2_rn(sum[e & 3], y);
+                    p[e] = f32x2_to_bf16x2_bits(y.x, y.y);
+                }
+                const float2 add = add2_rn(add2_rn(sum[0], sum[1]), add2_rn(sum[2], sum[3]));
+                l += add.x + add.y;
+                if (j > 0) {
+                    last_done();
+                    if (!ok) break;
+                }
+                tmem_st32(tp, p);
+                tmem_st32(tp + 32, p + 32);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[t]));
+            }
+            const int n = w.to - w.from;
+            done += n;
+            if (n > 0) ok = ok && mbar_wait(smem_addr(&ctl.o_done[t]), (done - 1) & 1, abort);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            // nothing but NaN: a finite maximum, so that it reaches the join
+            if (m == -INFINITY && l != l) m = -3.0e38f;
+            const bool split = it.splits > 1;
+            // where the row lies, of the partial results or of out; -1: there is none
+            const int head = kvh * g.group + mine.head;
+            const int64_t row = !mine.there ? -1
+                                : split     ? part_at(g, it, mine.token, head) * a.D
+                                            : (it.s.begin + (int64_t)mine.token) * a.out_stride + (int64_t)head * a.D;
+            float2 bad = make_float2(0.0f, 0.0f);
+            // 128 bytes of the warp's rows at a time by way of shared memory, so
+            // that a store covers 128 bytes of each of four rows
+            if (split) {
+                if (mine.there) g.part_ml[row / a.D] = make_float2(m == -INFINITY || m == -3.0e38f ? m : m * c, l);
+#pragma unroll
+                for (int x = 0; x < DP / 32; ++x) {
+                    uint32_t o[32];
+                    if (n > 0) {
+                        tmem_ld32(to + x * 32, o);
+                        tmem_wait_ld32(o);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        Vec16 v;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) v.w[y] = o[e * 4 + y];
+#pragma unroll
+                        for (int y = 0; y < 4; y += 2)
+                            bad = fma2_rn(make_float2(__uint_as_float(v.w[y]), __uint_as_float(v.w[y + 1])),
+                                          make_float2(0.0f, 0.0f), bad);  // 0, or NaN
+                        *reinterpret_cast<Vec16*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = v;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = e * 4 + (lane >> 3), piece = lane & 7, d = x * 32 + piece * 4;
+                        const int64_t at = __shfl_sync(0xFFFFFFFFu, row, r);
+                        const Vec16 v = *reinterpret_cast<const Vec16*>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
+                        if (at >= 0 && d < a.D) *reinterpret_cast<Vec16*>(g.part_o + at + d) = v;
+                    }
+                }
+            } else {
+                const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
+                uint16_t* const out = static_cast<uint16_t*>(a.out);
+#pragma unroll
+                for (int x = 0; x < DP / 64; ++x) {
+                    uint32_t o[64];
+                    if (n > 0) {
+                        tmem_ld32(to + x * 64, o);
+                        tmem_ld32(to + x * 64 + 32, o + 32);
+                        tmem_wait_ld32(o);
+                        tmem_wait_ld32(o + 32);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) o[e] = 0;
+                    }
+                    if (x == DP / 64 - 1 && n > 0) {  // the next item may have O
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&ctl.o_free[t]));
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        Vec16 v;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const float2 f = mul2_rn(make_float2(__uint_as_float(o[e * 8 + 2 * y]),
+                                                                 __uint_as_float(o[e * 8 + 2 * y + 1])),
+                                                     make_float2(inv, inv));
+                            bad = fma2_rn(f, make_float2(0.0f, 0.0f), bad);  // 0, or NaN
+                            v.w[y] = f32x2_to_bf16x2_bits(f.x, f.y);
+                        }
+                        *reinterpret_cast<Vec16*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = v;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = e * 4 + (lane >> 3), piece = lane & 7, d = x * 64 + piece * 8;
+                        const int64_t at = __shfl_sync(0xFFFFFFFFu, row, r);
+                        const Vec16 v = *reinterpret_cast<const Vec16*>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
+                        if (at >= 0 && d < a.D) *reinterpret_cast<Vec16*>(out + at + d) = v;
+                    }
+                }
+            }
+            if (split && n > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ctl.o_free[t]));
+            }
+            uint32_t again = __ballot_sync(0xFFFFFFFFu, mine.there && bad.x + bad.y != 0.0f);
+            __syncwarp();
+            while (again) {
+                const int r = __ffs((int)again) - 1;
+                again &= again - 1;
+                repair_row<KV>(g, it, kvh, __shfl_sync(0xFFFFFFFFu, mine.token, r),
+                               __shfl_sync(0xFFFFFFFFu, mine.head, r));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_free(tmem, 512);
+    if (*abort && warp == 0) give_up(g);
+}
+
+// k or v: pages of a cache, or packed rows; in boxes of `rows` keys of one head.
+bool encode_kv(CUtensorMap* m, const ChunkArgs& a, bool second, cuuint32_t rows) {
+    if (a.table == nullptr) {
+        const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hkv, (cuuint64_t)a.T};
+        const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)(second ? a.v_stride : a.k_stride) * 2};
+        const cuuint32_t box[3] = {64, 1, rows};
+        return encode_bf16(m, second ? a.v : a.k, 3, dims, strides, box);
+    }
+    const KvCacheArgs& c = a.c;
+    const cuuint64_t page = (cuuint64_t)c.page_size * c.D * 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.page_size, (cuuint64_t)c.Hkv, (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.D * 2, page,
+                                   c.n_pages > 1 ? (cuuint64_t)c.page_stride * 2 : page * c.Hkv};
+    const cuuint32_t box[4] = {64, rows, 1, 1};
+    return encode_bf16(m, second ? c.v : c.k, 4, dims, strides, box);
+}
+
+template <int KV, int DP>
+cudaError_t go(const ChunkArgs& a, cudaStream_t st) {
+    const Args g = make_args(a, kM, 2);
+    cuuint32_t box = kN;  // keys of a copy: the largest power of two that divides a page, and at most a block
+    if (KV != kPacked)
+        while (a.c.page_size % box) box /= 2;
+    Maps maps;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t q_box[3] = {64, (cuuint32_t)g.heads, (cuuint32_t)g.tokens};
+    if (!encode_bf16(&maps.q, a.q, 3, dims, strides, q_box) || !encode_kv(&maps.k, a, false, box) ||
+        !encode_kv(&maps.v, a, true, box) || !encode_kv(&maps.v32, a, true, box < 32 ? box : 32) ||
+        !encode_kv(&maps.v8, a, true, box < 8 ? box : 8) || !encode_kv(&maps.v1, a, true, 1))
+        return cudaErrorNotSupported;
+    constexpr int smem = Shape<DP>::kBytes;
+    static FunctionLimit limit;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(chunk_tc<KV, DP>), smem);
+    if (e != cudaSuccess) return e;
+    const int64_t seqs = a.n_seqs < a.T ? a.n_seqs : a.T, sms = sm_count();
+    const int64_t items = (a.T / g.tokens + seqs) * g.parts * g.most * a.Hkv;
+    const cudaError_t f = launch(chunk_tc<KV, DP>, dim3((unsigned)(items < sms ? items : sms)), dim3(kThreads), smem, st,
+                                 maps, g, (int)box);
+    return f != cudaSuccess ? f : launch_join(g, kBF16, st);
+}
+
+}  // namespace
+
+cudaError_t launch_tc(const ChunkArgs& a, cudaStream_t st) {
+    if (a.table == nullptr) return a.D <= 64 ? go<kPacked, 64>(a, st) : go<kPacked, 128>(a, st);
+    return a.D <= 64 ? go<GBE_KV_BF16, 64>(a, st) : go<GBE_KV_BF16, 128>(a, st);
+}
+
+}  // namespace chunk
+}  // namespace gbe

@@ -56,6 +56,7 @@
 #include "gbe_elementwise.h"
 #include "launch.h"
 #include "tensor_core.cuh"
+#include "tensor_map.h"
 
 namespace gbe {
 namespace {
@@ -641,36 +642,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tmem_free(tmem, 512);
 }
 
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-    static const EncodeFn fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<EncodeFn>(p);
-        cudaGetLastError();
-        return static_cast<EncodeFn>(nullptr);
-    }();
-    return fn;
-}
-
 // [T, H, D] bf16 with a token stride, copied in boxes of `rows` tokens of one
 // head and 64 entries (128 bytes, swizzled by the place in shared memory, so
 // that a box may begin at any row of a tile); zeros outside.
 bool encode(CUtensorMap* m, const void* p, int64_t T, int64_t H, int64_t D, int64_t stride, cuuint32_t rows) {
-    const EncodeFn fn = encode_fn();
-    if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {64, 1, rows}, step[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, step,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t box[3] = {64, 1, rows};
+    return encode_bf16(m, p, 3, dims, strides, box);
 }
 
 template <int DP>
