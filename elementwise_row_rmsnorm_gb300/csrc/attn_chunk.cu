@@ -513,7 +513,7 @@ ChunkRoom chunk_room(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t
 cudaError_t launch_attn_chunk(const ChunkArgs& a, int dtype, bool vec, bool tensor, cudaStream_t st) {
     using namespace chunk;
     if (tensor && vec && dtype == GBE_BF16 && a.D <= 128 &&
-        (a.table == nullptr || (a.c.dtype == GBE_KV_BF16 && a.c.n_pages > 0)))
+        (a.table == nullptr || a.c.n_pages > 0))
         return launch_tc(a, st);
     if (a.table == nullptr) {
         if (dtype == GBE_F32) return vec ? pick<kF32, kPacked, true>(a, st) : pick<kF32, kPacked, false>(a, st);

@@ -218,8 +218,8 @@ __device__ __forceinline__ int64_t part_at(const Args& g, const Item& it, int to
     return ((int64_t)(it.s.begin + token) * g.a.Hq + head) * g.most + it.split;
 }
 
-// The tensor-core form: bf16 rows and, where there is a cache, a bf16 cache of one
-// page at least; D <= 128, rows on the 16-byte grid, all in device memory.
+// The tensor-core form: bf16 rows and, where there is a cache, one of a page at
+// least; D <= 128, rows on the 16-byte grid, all in device memory.
 cudaError_t launch_tc(const ChunkArgs& a, cudaStream_t st);
 
 // The splits of every row added in order.

@@ -41,8 +41,8 @@ namespace chunk {
 namespace {
 
 constexpr int kM = 128, kN = 128;
-constexpr int kThreads = 384;  // three warpgroups: softmax of each tile, and the issuing warps
 constexpr int kLoadWarp = 8, kItemWarp = 9, kMmaWarp = 10;  // products: a warp for each tile
+constexpr int kWidenWarp = 12;   // over an 8-bit cache, and the three after it
 constexpr float kGrowth = 8.0f;  // a maximum may lag this many powers of two
 constexpr int kPacked = -1;      // KV of rows that are not in a cache
 
@@ -51,7 +51,7 @@ struct Todo {
     Item item;
     int kvh;
 };
-constexpr int kTodos = 4, kReaders = 11;  // items in hand; warps that read one: softmax, copies, products
+constexpr int kTodos = 4;  // in hand
 
 struct Control {
     uint64_t q_full[2], q_empty, kv_full[8], kv_empty[8], s_full[2], s_free[2], p_ready[2], o_done[2], o_free[2];
@@ -62,13 +62,30 @@ struct Control {
     int abort;
 };
 
-template <int DP>
+template <int KV, int DP>
 struct Shape {
+    static constexpr bool kE4 = KV == GBE_KV_E4M3;
+    static constexpr int kThreads = kE4 ? 512 : 384;
+    // Registers of a thread: 384 threads were launched with 168 each (64512), the
+    // softmax warpgroups take 208 and the issuing one keeps 80 (63488); 512 threads
+    // with 128 (65536): 200, and 56 of the issuing and the widening one (65536).
+    static constexpr int kSoftmaxRegs = kE4 ? 200 : 208, kOtherRegs = kE4 ? 56 : 80;
+    static constexpr int kReaders = kE4 ? 15 : 11;        // warps that read an item: all but the one that finds it
     static constexpr int kPanel = 128 * 128;              // 128 rows of 64 bf16
     static constexpr int kTile = kPanel * (DP / 64);      // 128 rows of DP
-    static constexpr int kStages = DP == 128 ? 4 : 8;
-    static constexpr int kOut = 8 * 32 * 128;             // 32 rows of 128 bytes for each softmax warp
-    static constexpr int kBytes = kTile * (2 + kStages) + kOut + 1024 + (int)sizeof(Control);
+    static constexpr int kStages = (kE4 ? 3 : 4) * (128 / DP);
+    static constexpr int kOutRow = kE4 ? 32 : 128;        // bytes of a row on their way out
+    static constexpr int kOut = 8 * 32 * kOutRow;         // 32 rows for each softmax warp
+    // 8-bit rows on their way in, where they lie and their scales
+    static constexpr int kRaw = kE4 ? kN * DP : 0, kRaws = 3;
+    static constexpr int kPlaces = kE4 ? 2 * kN * 8 + 4 * kN * 2 : 0;
+    static constexpr int kControlAt = kTile * (2 + kStages) + kOut + kRaws * kRaw + kPlaces;
+    static constexpr int kBytes = kControlAt + 1024 + (int)sizeof(Control);
+    // where piece c (16 bytes) of row r of a warp's rows lies on its way out
+    __device__ static __forceinline__ int out_at(int r, int c) {
+        constexpr int kPieces = kOutRow / 16, kSide = 8 / kPieces;  // rows side by side
+        return r / kSide * 128 + ((((r % kSide) * kPieces + c) ^ (r / kSide & 7)) << 4);
+    }
 };
 
 // The copies of a call: q; k and v in boxes of `rows` keys, and v in smaller ones
@@ -109,9 +126,22 @@ __device__ __forceinline__ float4 load4(const void* base, int64_t i) {
 }
 template <int KV, bool V>
 __device__ __forceinline__ float4 load_kv(const ChunkArgs& a, int kvh, int64_t at, int d) {
-    if constexpr (KV == kPacked)
+    if constexpr (KV == kPacked) {
         return load4(V ? a.v : a.k, at * (V ? a.v_stride : a.k_stride) + (int64_t)kvh * a.D + d);
-    return load4(V ? a.c.v : a.c.k, at + d);
+    } else if constexpr (KV == GBE_KV_E4M3) {
+        const int64_t page = at / a.c.page_stride, row = (at - page * a.c.page_stride) / a.D;
+        const uint8_t byte = (V ? a.c.v_scale : a.c.k_scale)[page * a.c.Hkv * a.c.page_size + row];
+        float f[4] = {};
+        if (byte != 0) {  // (0: zeros, whatever the codes)
+            e4m3x4_to_f32(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(V ? a.c.v : a.c.k) + at + d), f);
+            const float scale = __uint_as_float((uint32_t)byte << 23);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] *= scale;
+        }
+        return make_float4(f[0], f[1], f[2], f[3]);
+    } else {
+        return load4(V ? a.c.v : a.c.k, at + d);
+    }
 }
 
 __device__ __forceinline__ uint32_t not_finite(float4 x) {
@@ -262,14 +292,201 @@ __device__ __noinline__ void give_up(const Args& g) {
     }
 }
 
+// ---- an 8-bit cache's rows -----------------------------------------------------------
+
+// 16 bytes into shared memory, the first `from` of them from memory and zeros
+// behind them; rows off the 16-byte grid in two halves.
+__device__ __forceinline__ void copy_async(uint32_t to, const uint8_t* p, int from, bool grid16) {
+    if (grid16) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(from) : "memory");
+        return;
+    }
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(p), "r"(min(from, 8)) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + 8), "l"(from > 8 ? p + 8 : p),
+                 "r"(max(from - 8, 0))
+                 : "memory");
+}
+
+// Sixteen codes times 2^(byte - 127), exact in bf16 from 2^-126 on; byte 0:
+// zeros.  A code's bits, its exponent and mantissa moved to where bf16 has them,
+// are 2^-120 of its value; one product brings that and the scale.  Rows of byte
+// 135 and above (2^(byte - 7) is past bf16's range), and NaN codes, which that way
+// would come out as 480, go through f32.
+__device__ __forceinline__ void widen16(const Vec16& codes, uint32_t byte, Vec16& lo, Vec16& hi) {
+    uint32_t nan = 0, w[8];
+    const uint32_t field = byte == 0 ? 0u : (byte + 120u) << 7, scale = field | field << 16;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        nan |= (codes.w[x] & 0x7F7F7F7Fu) + 0x01010101u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t y = __byte_perm(codes.w[x], 0, h == 0 ? 0x1404 : 0x3424);
+            const uint32_t z = (y >> 4 & 0x07F007F0u) | (y & 0x80008000u);
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w[2 * x + h]) : "r"(z), "r"(scale));
+        }
+    }
+    if (byte != 0 && ((nan & 0x80808080u) || byte > 134u)) {
+        const float s = __uint_as_float(byte << 23);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            float f[4];
+            e4m3x4_to_f32(codes.w[x], f);
+            w[2 * x] = f32x2_to_bf16x2_bits(f[0] * s, f[1] * s);
+            w[2 * x + 1] = f32x2_to_bf16x2_bits(f[2] * s, f[3] * s);
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) lo.w[x] = w[x], hi.w[x] = w[4 + x];
+}
+
+// The warps that bring an 8-bit cache's rows into the ring as bf16.  Blocks are
+// counted over all items; of block B, k is load 2 B and v load 2 B + 1.  A thread
+// copies pieces of 16 codes into places of its own and widens them itself, so
+// that it waits for nobody but its own copies; two loads are on their way while
+// one is widened.  Where a block's rows lie is looked up by a thread a row, two
+// blocks ahead.
+template <int DP>
+__device__ __forceinline__ void widen_rows(const Args& g, Control& ctl, uint8_t* const smem, uint32_t kv_smem) {
+    using S = Shape<GBE_KV_E4M3, DP>;
+    constexpr int kPieces = DP / 16, kRows = 128 / kPieces, kTurns = kN / kRows;
+    const ChunkArgs& a = g.a;
+    const int tid = threadIdx.x - kWidenWarp * 32, lane = threadIdx.x & 31;
+    volatile int* const abort = &ctl.abort;
+    uint8_t* const raw = smem + S::kTile * (2 + S::kStages) + S::kOut;
+    int64_t* const places = reinterpret_cast<int64_t*>(raw + S::kRaws * S::kRaw);  // [2][kN], of block B in B & 1
+    uint8_t* const scales = reinterpret_cast<uint8_t*>(places + 2 * kN);           // [4][k, v][kN], in B & 3
+    const int piece = tid % kPieces, r0 = tid / kPieces;
+    const int size = min(max((int)a.D - piece * 16, 0), 16);
+    const bool grid16 = a.D % 16 == 0 && a.c.page_stride % 16 == 0;
+    auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+
+    // the walk over all items' blocks
+    int todo = 0, x = 0, seq = 0, len = 0, kvh = 0;
+    Walk w = {};
+    bool end = false;
+    // the next block: false behind the last one.  Asks for the page of the thread's
+    // row of it; `locate` says where it lies and its scales' index, -1: nowhere.
+    int32_t page = -1;
+    int row = 0;
+    auto next = [&] {
+        page = -1;
+        while (!end && x == w.to) {
+            const bool ok = mbar_wait(smem_addr(&ctl.todo_full[todo % kTodos]), todo / kTodos & 1, abort);
+            end = !__all_sync(0xFFFFFFFFu, ok);
+            if (end) break;
+            const Item it = ctl.todo[todo % kTodos].item;
+            kvh = ctl.todo[todo % kTodos].kvh;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&ctl.todo_empty[todo % kTodos]));
+            ++todo;
+            end = it.splits == 0;
+            if (end) break;
+            w = walk(g, it, kN);
+            x = w.from, seq = it.seq, len = it.s.len;
+        }
+        if (end) return false;
+        const int j = w.block(x++) * kN + tid;
+        if (j < len) {
+            const int page_i = j / a.c.page_size;
+            row = j - page_i * a.c.page_size;
+            page = a.table[seq * a.max_pages + page_i];
+        }
+        return true;
+    };
+    int64_t at = -1, scale_at = -1;
+    auto locate = [&] {
+        const bool there = page >= 0 && page < a.c.n_pages;
+        at = there ? page * a.c.page_stride + ((int64_t)kvh * a.c.page_size + row) * a.D : -1;
+        scale_at = there ? ((int64_t)page * a.c.Hkv + kvh) * a.c.page_size + row : -1;
+    };
+    auto keep_places = [&](int block) { places[(block & 1) * kN + tid] = at; };
+    uint32_t bytes = 0;
+    auto load_scales = [&] {
+        bytes = scale_at < 0 ? 0u : (uint32_t)a.c.k_scale[scale_at] | (uint32_t)a.c.v_scale[scale_at] << 8;
+    };
+    auto keep_scales = [&](int block) {
+        scales[((block & 3) * 2) * kN + tid] = (uint8_t)bytes;
+        scales[((block & 3) * 2 + 1) * kN + tid] = (uint8_t)(bytes >> 8);
+    };
+    auto fetch = [&](int load, bool there) {  // (an empty group behind the last one)
+        if (there) {
+            const uint8_t* const src = static_cast<const uint8_t*>(load & 1 ? a.c.v : a.c.k);
+            const uint32_t to = smem_addr(raw + load % S::kRaws * S::kRaw + tid * 16);
+            const int64_t* const place = places + (load >> 1 & 1) * kN + r0;
+#pragma unroll
+            for (int i = 0; i < kTurns; ++i) {
+                const int64_t p = place[i * kRows];
+                const bool here = p >= 0 && size > 0;
+                copy_async(to + i * 2048, src + (here ? p + piece * 16 : 0), here ? size : 0, grid16);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto widen = [&](int load) {
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        const int stage = load % S::kStages;
+        const bool ok = mbar_wait(smem_addr(&ctl.kv_empty[stage]), (load / S::kStages & 1) ^ 1, abort);
+        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+        const uint8_t* const from = raw + load % S::kRaws * S::kRaw + tid * 16;
+        const uint8_t* const scale = scales + ((load >> 1 & 3) * 2 + (load & 1)) * kN + r0;
+        uint8_t* const to = smem + (kv_smem - smem_addr(smem)) + stage * S::kTile + (piece >> 2) * S::kPanel;
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            const int r = i * kRows + r0, c = (piece & 3) * 2;
+            Vec16 lo, hi;
+            widen16(*reinterpret_cast<const Vec16*>(from + i * 2048), scale[i * kRows], lo, hi);
+            // (lanes of the second panel write their upper half first: eight lanes then meet eight bank groups)
+            const bool second = piece >> 2;
+            uint8_t* const line = to + r * 128;
+            *reinterpret_cast<Vec16*>(line + (((c + second) ^ (r & 7)) << 4)) = second ? hi : lo;
+            *reinterpret_cast<Vec16*>(line + (((c + !second) ^ (r & 7)) << 4)) = second ? lo : hi;
+        }
+        async_proxy_fence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&ctl.kv_full[stage]));
+        return true;
+    };
+
+    bool have0 = next();
+    locate();
+    keep_places(0);
+    load_scales();
+    keep_scales(0);
+    bool have1 = next();
+    locate();
+    keep_places(1);
+    load_scales();
+    keep_scales(1);
+    sync();
+    fetch(0, have0);
+    fetch(1, have0);
+    fetch(2, have1);
+    for (int b = 0; have0; ++b) {
+        // (places of block b + 2 take those of block b, whose last use, the fetch of its v, was ahead of the last sync)
+        const bool have2 = next();
+        if (!widen(2 * b)) break;
+        fetch(2 * b + 3, have1);
+        locate();
+        keep_places(b + 2);
+        load_scales();
+        sync();
+        if (!widen(2 * b + 1)) break;
+        keep_scales(b + 2);
+        fetch(2 * b + 4, have2);
+        have0 = have1, have1 = have2;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
 template <int KV, int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
     chunk_tc(const __grid_constant__ Maps maps, const __grid_constant__ Args g, int box) {
-    using S = Shape<DP>;
+    using S = Shape<KV, DP>;
     extern __shared__ uint8_t raw[];
     const ChunkArgs& a = g.a;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
-    Control& ctl = *reinterpret_cast<Control*>(raw + (base - smem_addr(raw)) + S::kTile * (2 + S::kStages) + S::kOut);
+    uint8_t* const smem = raw + (base - smem_addr(raw));
+    Control& ctl = *reinterpret_cast<Control*>(smem + S::kControlAt);
     const uint32_t q_smem = base, kv_smem = base + 2 * S::kTile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* const abort = &ctl.abort;
@@ -277,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(smem_addr(&ctl.q_empty), 2);
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(smem_addr(&ctl.kv_full[i]), 1);
+            mbar_init(smem_addr(&ctl.kv_full[i]), S::kE4 ? 4 : 1);
             mbar_init(smem_addr(&ctl.kv_empty[i]), 2);
         }
         for (int t = 0; t < 2; ++t) {
@@ -291,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kTodos; ++i) {
             mbar_init(smem_addr(&ctl.todo_full[i]), 1);
-            mbar_init(smem_addr(&ctl.todo_empty[i]), kReaders);
+            mbar_init(smem_addr(&ctl.todo_empty[i]), S::kReaders);
         }
         ctl.abort = 0;
         mbar_init_fence();
@@ -311,11 +528,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto todo_ready = [&](int i) { return mbar_wait(smem_addr(&ctl.todo_full[i % kTodos]), i / kTodos & 1, abort); };
     auto todo_read = [&](int i) { mbar_arrive(smem_addr(&ctl.todo_empty[i % kTodos])); };
 
-    // Registers: 384 threads were launched with 168 each (64512); the softmax
-    // warpgroups take 208, the issuing one keeps 80 (63488 in all).
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        if (warp == kItemWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOtherRegs));
+        if (warp >= kWidenWarp) {
+            if constexpr (S::kE4) widen_rows<DP>(g, ctl, smem, kv_smem);
+        } else if (warp == kItemWarp) {
             Finder finder(g);
             bool ok = true;
             for (int i = 0; ok; ++i) {
@@ -345,6 +562,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (it.splits == 0) break;
                 const Walk w = walk(g, it, kN);
                 if (w.from == w.to) continue;
+                auto load_q = [&] {  // once the last item's is done with
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.q_empty), (items & 1) ^ 1, abort));
+                    if (!ok) return;
+                    ++items;
+                    for (int t = 0; t < it.tiles; ++t) {
+                        const int u = it.tile + t;
+                        if (lane == 0) {
+                            const uint32_t qb = smem_addr(&ctl.q_full[t]);
+                            mbar_arrive_tx(qb, (DP / 64) * 128 * g.heads * g.tokens);
+#pragma unroll
+                            for (int p = 0; p < DP / 64; ++p)
+                                tma_load_3d(q_smem + t * S::kTile + p * S::kPanel, &maps.q, qb, p * 64,
+                                            kvh * g.group + u % g.parts * g.heads, it.s.begin + u / g.parts * g.tokens);
+                        }
+                        ++tiles[t];
+                    }
+                };
+                if constexpr (S::kE4) {
+                    load_q();
+                    continue;
+                }
                 // box b of the walk's block x: the page (from n_pages on: zeros) and the row in it
                 auto look_up = [&](int x, int b, int& page, int& row) {
                     const int j = w.block(x) * kN + b * box;
@@ -407,24 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (boxes > 32) look_up(x, lane, page, row);  // (the last one of these was looked up last)
                         ++loads;
-                        if (kv == 0 && x == w.from) {  // q, once the last item's is done with
-                            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.q_empty), (items & 1) ^ 1, abort));
-                            if (!ok) break;
-                            ++items;
-                            for (int t = 0; t < it.tiles; ++t) {
-                                const int u = it.tile + t;
-                                if (lane == 0) {
-                                    const uint32_t qb = smem_addr(&ctl.q_full[t]);
-                                    mbar_arrive_tx(qb, (DP / 64) * 128 * g.heads * g.tokens);
-#pragma unroll
-                                    for (int p = 0; p < DP / 64; ++p)
-                                        tma_load_3d(q_smem + t * S::kTile + p * S::kPanel, &maps.q, qb, p * 64,
-                                                    kvh * g.group + u % g.parts * g.heads,
-                                                    it.s.begin + u / g.parts * g.tokens);
-                                }
-                                ++tiles[t];
-                            }
-                        }
+                        if (kv == 0 && x == w.from) load_q();
+                        if (!ok) break;
                     }
                     look_up(x + 1, lane, page, row);
                 }
@@ -434,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int none = 0;
                 for (int t = 0; t < 2; ++t)
                     if (tiles[t] > 0) mbar_wait(smem_addr(&ctl.q_full[t]), (tiles[t] - 1) & 1, &none);
-                for (int x = max(0, loads - S::kStages); x < loads; ++x)
+                for (int x = max(0, loads - S::kStages); x < loads; ++x)  // (0 of them over an 8-bit cache)
                     mbar_wait(smem_addr(&ctl.kv_full[x % S::kStages]), x / S::kStages & 1, &none);
             }
         } else if (elect_one()) {
@@ -529,13 +751,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(smem_addr(&ctl.drained[t]), 0, &none);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftmaxRegs));
         const int t = warp >> 2;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
         const uint32_t ts = tmem + lanes, tp = tmem + 128 + t * 64 + lanes, to = tmem + 256 + t * 128 + lanes;
         // (never 0, so that c times the -inf of a masked place stays -inf)
         const float c = fmaxf(fabsf(a.scale) * kLog2e, __uint_as_float(1u));
-        uint8_t* const stage = raw + (base - smem_addr(raw)) + S::kTile * (2 + S::kStages) + warp * (S::kOut / 8);
+        uint8_t* const stage = smem + S::kTile * (2 + S::kStages) + warp * (S::kOut / 8);
         bool ok = true;
         int done = 0;  // blocks of this tile before this item
         for (int i = 0; ok; ++i) {
@@ -663,89 +885,69 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 : split     ? part_at(g, it, mine.token, head) * a.D
                                             : (it.s.begin + (int64_t)mine.token) * a.out_stride + (int64_t)head * a.D;
             float2 bad = make_float2(0.0f, 0.0f);
-            // 128 bytes of the warp's rows at a time by way of shared memory, so
-            // that a store covers 128 bytes of each of four rows
-            if (split) {
-                if (mine.there) g.part_ml[row / a.D] = make_float2(m == -INFINITY || m == -3.0e38f ? m : m * c, l);
+            // Some bytes of the warp's rows at a time by way of shared memory, so that
+            // a store covers all of them in several rows; 16 bytes a piece, which `piece`
+            // makes of the row's entries at d
+            constexpr int kPieces = S::kOutRow / 16, kSide = 32 / kPieces;  // rows that a store covers
+            auto write = [&](char* base, int es, int d0, auto piece) {
+                __syncwarp();
 #pragma unroll
-                for (int x = 0; x < DP / 32; ++x) {
-                    uint32_t o[32];
-                    if (n > 0) {
-                        tmem_ld32(to + x * 32, o);
-                        tmem_wait_ld32(o);
-                    } else {
+                for (int e = 0; e < kPieces; ++e)
+                    *reinterpret_cast<Vec16*>(stage + S::out_at(lane, e)) = piece(e);
+                __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0;
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        Vec16 v;
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) v.w[y] = o[e * 4 + y];
-#pragma unroll
-                        for (int y = 0; y < 4; y += 2)
-                            bad = fma2_rn(make_float2(__uint_as_float(v.w[y]), __uint_as_float(v.w[y + 1])),
-                                          make_float2(0.0f, 0.0f), bad);  // 0, or NaN
-                        *reinterpret_cast<Vec16*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = v;
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int r = e * 4 + (lane >> 3), piece = lane & 7, d = x * 32 + piece * 4;
-                        const int64_t at = __shfl_sync(0xFFFFFFFFu, row, r);
-                        const Vec16 v = *reinterpret_cast<const Vec16*>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
-                        if (at >= 0 && d < a.D) *reinterpret_cast<Vec16*>(g.part_o + at + d) = v;
-                    }
+                for (int e = 0; e < kPieces; ++e) {
+                    const int r = e * kSide + lane / kPieces, d = d0 + lane % kPieces * (16 / es);
+                    const int64_t at = __shfl_sync(0xFFFFFFFFu, row, r);
+                    const Vec16 v = *reinterpret_cast<const Vec16*>(stage + S::out_at(r, lane % kPieces));
+                    if (at >= 0 && d < a.D) *reinterpret_cast<Vec16*>(base + (at + d) * es) = v;
                 }
-            } else {
-                const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
-                uint16_t* const out = static_cast<uint16_t*>(a.out);
+            };
+            constexpr int kCols = S::kOutRow >= 64 ? S::kOutRow / 2 : 32;  // of O at a time
+            if (split && mine.there) g.part_ml[row / a.D] = make_float2(m == -INFINITY || m == -3.0e38f ? m : m * c, l);
+            const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
 #pragma unroll
-                for (int x = 0; x < DP / 64; ++x) {
-                    uint32_t o[64];
-                    if (n > 0) {
-                        tmem_ld32(to + x * 64, o);
-                        tmem_ld32(to + x * 64 + 32, o + 32);
-                        tmem_wait_ld32(o);
-                        tmem_wait_ld32(o + 32);
-                    } else {
+            for (int x = 0; x < DP / kCols; ++x) {
+                uint32_t o[kCols] = {};
+                if (n > 0) {
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) o[e] = 0;
-                    }
-                    if (x == DP / 64 - 1 && n > 0) {  // the next item may have O
+                    for (int y = 0; y < kCols / 32; ++y) tmem_ld32(to + x * kCols + y * 32, o + y * 32);
+#pragma unroll
+                    for (int y = 0; y < kCols / 32; ++y) tmem_wait_ld32(o + y * 32);
+                    if (x == DP / kCols - 1) {  // the next item may have O
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_addr(&ctl.o_free[t]));
                     }
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        Vec16 v;
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const float2 f = mul2_rn(make_float2(__uint_as_float(o[e * 8 + 2 * y]),
-                                                                 __uint_as_float(o[e * 8 + 2 * y + 1])),
-                                                     make_float2(inv, inv));
-                            bad = fma2_rn(f, make_float2(0.0f, 0.0f), bad);  // 0, or NaN
-                            v.w[y] = f32x2_to_bf16x2_bits(f.x, f.y);
-                        }
-                        *reinterpret_cast<Vec16*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = v;
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int r = e * 4 + (lane >> 3), piece = lane & 7, d = x * 64 + piece * 8;
-                        const int64_t at = __shfl_sync(0xFFFFFFFFu, row, r);
-                        const Vec16 v = *reinterpret_cast<const Vec16*>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
-                        if (at >= 0 && d < a.D) *reinterpret_cast<Vec16*>(out + at + d) = v;
-                    }
                 }
-            }
-            if (split && n > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&ctl.o_free[t]));
+                if (split) {
+                    constexpr int kEntries = S::kOutRow / 4;
+#pragma unroll
+                    for (int e = 0; e < kCols; e += 2)
+                        bad = fma2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
+                                      make_float2(0.0f, 0.0f), bad);  // 0, or NaN
+#pragma unroll
+                    for (int y = 0; y < kCols / kEntries; ++y)
+                        write(reinterpret_cast<char*>(g.part_o), 4, x * kCols + y * kEntries, [&](int e) {
+                            const uint32_t* const z = o + y * kEntries + 4 * e;
+                            return Vec16{{z[0], z[1], z[2], z[3]}};
+                        });
+                } else {
+                    constexpr int kEntries = S::kOutRow / 2;
+#pragma unroll
+                    for (int e = 0; e < kCols; e += 2) {
+                        const float2 f = mul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
+                                                 make_float2(inv, inv));
+                        bad = fma2_rn(f, make_float2(0.0f, 0.0f), bad);
+                        o[e / 2] = f32x2_to_bf16x2_bits(f.x, f.y);
+                    }
+#pragma unroll
+                    for (int y = 0; y < kCols / kEntries; ++y)
+                        write(static_cast<char*>(a.out), 2, x * kCols + y * kEntries, [&](int e) {
+                            const uint32_t* const z = o + y * kEntries / 2 + 4 * e;
+                            return Vec16{{z[0], z[1], z[2], z[3]}};
+                        });
+                }
             }
             uint32_t again = __ballot_sync(0xFFFFFFFFu, mine.there && bad.x + bad.y != 0.0f);
             __syncwarp();
@@ -783,26 +985,32 @@ bool encode_kv(CUtensorMap* m, const ChunkArgs& a, bool second, cuuint32_t rows)
 
 template <int KV, int DP>
 cudaError_t go(const ChunkArgs& a, cudaStream_t st) {
+    using S = Shape<KV, DP>;
     const Args g = make_args(a, kM, 2);
     cuuint32_t box = kN;  // keys of a copy: the largest power of two that divides a page, and at most a block
-    if (KV != kPacked)
+    if (KV == GBE_KV_BF16)
         while (a.c.page_size % box) box /= 2;
     Maps maps;
     const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
     const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.q_stride * 2};
     const cuuint32_t q_box[3] = {64, (cuuint32_t)g.heads, (cuuint32_t)g.tokens};
-    if (!encode_bf16(&maps.q, a.q, 3, dims, strides, q_box) || !encode_kv(&maps.k, a, false, box) ||
-        !encode_kv(&maps.v, a, true, box) || !encode_kv(&maps.v32, a, true, box < 32 ? box : 32) ||
-        !encode_kv(&maps.v8, a, true, box < 8 ? box : 8) || !encode_kv(&maps.v1, a, true, 1))
+    if (!encode_bf16(&maps.q, a.q, 3, dims, strides, q_box)) return cudaErrorNotSupported;
+    if constexpr (S::kE4) {
+        maps.k = maps.v = maps.v32 = maps.v8 = maps.v1 = maps.q;  // (not used)
+    } else if (!encode_kv(&maps.k, a, false, box) || !encode_kv(&maps.v, a, true, box) ||
+               !encode_kv(&maps.v32, a, true, box < 32 ? box : 32) || !encode_kv(&maps.v8, a, true, box < 8 ? box : 8) ||
+               !encode_kv(&maps.v1, a, true, 1)) {
         return cudaErrorNotSupported;
-    constexpr int smem = Shape<DP>::kBytes;
+    }
+    constexpr int smem = S::kBytes;
+    static_assert(smem <= 227 * 1024);
     static FunctionLimit limit;
     const cudaError_t e = limit.raise(reinterpret_cast<const void*>(chunk_tc<KV, DP>), smem);
     if (e != cudaSuccess) return e;
     const int64_t seqs = a.n_seqs < a.T ? a.n_seqs : a.T, sms = sm_count();
     const int64_t items = (a.T / g.tokens + seqs) * g.parts * g.most * a.Hkv;
-    const cudaError_t f = launch(chunk_tc<KV, DP>, dim3((unsigned)(items < sms ? items : sms)), dim3(kThreads), smem, st,
-                                 maps, g, (int)box);
+    const cudaError_t f = launch(chunk_tc<KV, DP>, dim3((unsigned)(items < sms ? items : sms)), dim3(S::kThreads), smem,
+                                 st, maps, g, (int)box);
     return f != cudaSuccess ? f : launch_join(g, kBF16, st);
 }
 
@@ -810,6 +1018,7 @@ cudaError_t go(const ChunkArgs& a, cudaStream_t st) {
 
 cudaError_t launch_tc(const ChunkArgs& a, cudaStream_t st) {
     if (a.table == nullptr) return a.D <= 64 ? go<kPacked, 64>(a, st) : go<kPacked, 128>(a, st);
+    if (a.c.dtype == GBE_KV_E4M3) return a.D <= 64 ? go<GBE_KV_E4M3, 64>(a, st) : go<GBE_KV_E4M3, 128>(a, st);
     return a.D <= 64 ? go<GBE_KV_BF16, 64>(a, st) : go<GBE_KV_BF16, 128>(a, st);
 }
 
