@@ -963,8 +963,8 @@ static bool chunk_sizes_ok(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hkv, i
 
 static uint64_t chunk_workspace(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t keys,
                                 int64_t window, int64_t sinks) {
-    return n_seqs == 0 || T == 0
-               ? 0u : (uint64_t)gbe::chunk_room(n_seqs, T, Hq, Hkv, keys, window, sinks).entries * (D + 2) * 4;
+    if (n_seqs == 0 || T == 0) return 0;
+    return (uint64_t)gbe::chunk_room(n_seqs, T, Hq, Hkv, keys, window, sinks).entries * (D + 2) * 4;
 }
 
 int64_t gbe_attn_chunk_workspace(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,

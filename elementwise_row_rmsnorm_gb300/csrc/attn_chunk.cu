@@ -1,18 +1,18 @@
 // attn_chunk.cu -- attention of new rows behind a cached prefix, and of packed
 // prompts under a sliding window: f32, and what attn_chunk_tc.cu does not take;
-// and the join of splits, of both.
+// and the join of partial results, of both.
 //
 //   out[i, h] = sum_j p_ij v_j,  p_i = softmax_j(scale * q[i, h] . k_j)
 //
 // over the keys that row i sees (attn_chunk.cuh).  On the CUDA cores, f32
 // throughout.  A CTA goes from item to item: 32 rows -- tokens and the query
-// heads of a kv head -- and a split of their keys, walked in tiles of 64 with
-// the running maximum and sum of the softmax (base 2: scale * log2(e) is folded
+// heads of a kv head -- and their keys, or a part of these, in tiles of 64 with the running maximum and sum of the softmax (base 2: scale * log2(e) is folded
 // into q).  Eight by sixteen threads, a thread holding 4 x 4 logits and 4 x D/16
 // of the output, two multiply-adds an instruction; up to D = 128 two groups of
 // threads take every other tile and join their sums.  f32 rows come by
 // asynchronous copies, v while the logits are formed and the next k while the
 // output is; where a row lies is looked up a tile ahead.
+#include <new>
 #include <type_traits>
 
 #include "attn_chunk.cuh"
@@ -114,24 +114,28 @@ __global__ void __launch_bounds__(kThreads* kGroups<DP>, 1) chunk_rows(const __g
     auto sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kThreads) : "memory"); };
     __shared__ struct {
         Item item;
-        int kvh;
+        int kvh;  // -1: nothing more
     } todo;
     pdl_begin();
-    Finder finder(g);  // (of the first warp; the others' is not asked)
+    int kvh = 0;
     const int D = (int)a.D, ty = tid >> 4, tx = tid & 15;
     const int kv_heads = (int)a.Hkv;
+    __shared__ alignas(8) unsigned char source_at[32][sizeof(Source)];  // the first warp's, out of its registers
+    Source& source = *reinterpret_cast<Source*>(source_at[threadIdx.x & 31]);
+    if (threadIdx.x < 32) new (&source) Source(g, false);
 
-    for (uint64_t id = blockIdx.x;; id += gridDim.x) {
+    for (;;) {
         __syncthreads();  // the last item is done with
         if (threadIdx.x < 32) {
-            const Item it = finder.find(id / (uint32_t)kv_heads);
-            if (threadIdx.x == 0) todo.item = it, todo.kvh = (int)(id % (uint32_t)kv_heads);
+            Item it;
+            if (!source.next(it, kvh)) kvh = -1;
+            if (threadIdx.x == 0) todo.item = it, todo.kvh = kvh;
         }
         __syncthreads();
         const Item it = todo.item;
-        const int kvh = todo.kvh;
-        if (it.splits == 0) break;
-        const Walk w = walk(g, it, kN);
+        kvh = todo.kvh;
+        if (kvh < 0) break;
+        const Walk w = walk(g, it);
         const int token0 = it.tile / g.parts * g.tokens, head0 = it.tile % g.parts * g.heads;
         const int rows = g.tokens * g.heads;
         // row r of the tile: token and head of the group; false: the tile has no such row
@@ -381,9 +385,10 @@ __global__ void __launch_bounds__(kThreads* kGroups<DP>, 1) chunk_rows(const __g
             if (!row_of(ty * R + i, token, head)) continue;
             head += kvh * g.group;
             const int64_t out = (it.s.begin + (int64_t)token) * a.out_stride + (int64_t)head * D;
-            const int64_t part = it.splits > 1 ? part_at(g, it, token, head) : 0;
+            const bool is_part = it.splits > 1;
+            const int64_t part = is_part ? part_at(g, it, token, head) : 0;
             const float inv = m[i] == -INFINITY ? 0.0f : 1.0f / l[i];
-            if (it.splits > 1 && tx == 0) g.part_ml[part] = make_float2(m[i], l[i]);
+            if (is_part && tx == 0) g.part_ml[part] = make_float2(m[i], l[i]);
 #pragma unroll
             for (int c = 0; c < Q4; ++c)
 #pragma unroll
@@ -391,7 +396,7 @@ __global__ void __launch_bounds__(kThreads* kGroups<DP>, 1) chunk_rows(const __g
                     const int d = tx * 4 + 64 * c + e;
                     const float y = e & 1 ? o[i][2 * c + e / 2].y : o[i][2 * c + e / 2].x;
                     if (d >= D) continue;
-                    if (it.splits > 1)
+                    if (is_part)
                         g.part_o[part * D + d] = y;
                     else
                         Store<DT>::store1(a.out, out + d, m[i] == -INFINITY ? 0.0f : y * inv);
@@ -400,8 +405,8 @@ __global__ void __launch_bounds__(kThreads* kGroups<DP>, 1) chunk_rows(const __g
     }
 }
 
-// A warp a row, its splits in order, four entries a lane; 0 where nothing was
-// seen (a weight of 0 still carries NaN on).
+// A warp a row, its partial results in order, four entries a lane; 0 where nothing
+// was seen (a weight of 0 still carries NaN on).
 constexpr int kJoinWarps = 8;
 template <int DT>
 __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join(const __grid_constant__ Args g) {
@@ -412,24 +417,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join(const __grid_const
         Item it = {};
         it.s = sequence(a, b);
         it.seq = (int)b;
-        if (it.s.n == 0) continue;
-        it.splits = splits_of(g, it.s);
+        it.splits = cut_of(g, it.s).splits;
         if (it.splits == 1) continue;
-        const int64_t rows = (int64_t)it.s.n * a.Hq;
-        for (int64_t r = (int64_t)blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < rows;
-             r += (int64_t)gridDim.y * kJoinWarps) {
-            const int token = (int)(r / a.Hq), head = (int)(r - token * a.Hq);
-            const int64_t at = part_at(g, it, token, head);
+        const int Hq = (int)a.Hq, rows = it.s.n * Hq;  // (of fewer than kWave kRounds units)
+        for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < rows; r += gridDim.y * kJoinWarps) {
+            const int token = r / Hq, head = r - token * Hq;
+            const int n = it.splits;
+            const int64_t at = parts_at(g, it, token, head);
             const float2* const ml = g.part_ml + at;
             float mx = -INFINITY;
-            for (int s = lane; s < it.splits; s += 32) mx = fmaxf(mx, ml[s].x);
+            for (int s = lane; s < n; s += 32) mx = fmaxf(mx, ml[s].x);
 #pragma unroll
             for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
             float l = 0.0f;
             float4 o[2] = {};
             const float* const from = g.part_o + at * D + lane * 4;
 #pragma unroll 4
-            for (int s = 0; s < it.splits; ++s) {
+            for (int s = 0; s < n; ++s) {
                 const float2 v = ml[s];
                 const bool any = v.x != -INFINITY;
                 const float w = any ? ex2(v.x - mx) : 0.0f;
@@ -460,14 +464,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join(const __grid_const
 
 template <int DT, int KV, int DP, bool VEC>
 cudaError_t go(const ChunkArgs& a, cudaStream_t st) {
-    const Args g = make_args(a, kM, 1);
+    const Args g = make_args(a, kM, 1, kN);
     constexpr int smem = (kM * (DP + 4) + kGroups<DP> * kGroupFloats<DP>) * 4;
     static FunctionLimit limit;
     const cudaError_t e = limit.raise(reinterpret_cast<const void*>(chunk_rows<DT, KV, DP, VEC>), smem);
     if (e != cudaSuccess) return e;
     const int64_t seqs = a.n_seqs < a.T ? a.n_seqs : a.T;
-    const int64_t items = (a.T / g.tokens + seqs) * g.parts * g.most * a.Hkv, most = 2 * (int64_t)sm_count();
-    const cudaError_t f = launch(chunk_rows<DT, KV, DP, VEC>, dim3((unsigned)(items < most ? items : most)),
+    const int64_t pieces = (a.T / g.tokens + seqs) * g.parts * a.Hkv * g.most;
+    const int64_t most = 2 * (int64_t)sm_count();
+    const cudaError_t f = launch(chunk_rows<DT, KV, DP, VEC>, dim3((unsigned)(pieces < most ? pieces : most)),
                                  dim3(kThreads * kGroups<DP>), smem, st, g);
     return f != cudaSuccess ? f : launch_join(g, DT, st);
 }
@@ -495,17 +500,15 @@ cudaError_t launch_join(const Args& g, int dtype, cudaStream_t st) {
 ChunkRoom chunk_room(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t keys, int64_t window, int64_t sinks) {
     using namespace chunk;
     ChunkRoom r = {1, 0, 0};
-    if (window > 0 && window + sinks + T < keys) keys = window + sinks + T;
-    int64_t most = (keys + kBlock - 1) / kBlock / kLeast;
-    if (most > kMostSplits) most = kMostSplits;
+    if (window > 0 && window + sinks + kUnitRows < keys) keys = window + sinks + kUnitRows;
+    int64_t most = (keys + 127) / 128 / (kLeast / 128);
     if (most > kWave * kRounds / Hkv) most = kWave * kRounds / Hkv;
     if (most < 2) return r;
     r.most = (int)most;
-    // splits_of gives a sequence of n rows a head at most kWave * kRounds / items splits, and has at least
-    // n * group / kPairRows * Hkv items
-    const int64_t by_row = T * Hq * most, of_seq = (int64_t)kWave * kRounds * kPairRows;
+    // cut_of gives a sequence at most kWave kRounds items, of kUnitRows rows each
+    const int64_t by_row = T * Hq * most, of_seq = (int64_t)kUnitRows * kWave * kRounds;
     const int64_t per_seq = of_seq < by_row ? of_seq : by_row;
-    if (n_seqs < by_row / per_seq + 1 && n_seqs * per_seq < by_row) r.per_seq = per_seq;
+    if (n_seqs * per_seq < by_row) r.per_seq = per_seq;
     r.entries = r.per_seq > 0 ? n_seqs * per_seq : by_row;
     return r;
 }
@@ -513,7 +516,8 @@ ChunkRoom chunk_room(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t
 cudaError_t launch_attn_chunk(const ChunkArgs& a, int dtype, bool vec, bool tensor, cudaStream_t st) {
     using namespace chunk;
     if (tensor && vec && dtype == GBE_BF16 && a.D <= 128 &&
-        (a.table == nullptr || a.c.n_pages > 0))
+        (a.table == nullptr || (a.c.n_pages > 0 && (a.c.dtype == GBE_KV_BF16 ||
+                                                    (a.D % 16 == 0 && a.c.page_stride % 16 == 0)))))
         return launch_tc(a, st);
     if (a.table == nullptr) {
         if (dtype == GBE_F32) return vec ? pick<kF32, kPacked, true>(a, st) : pick<kF32, kPacked, false>(a, st);

@@ -1,6 +1,5 @@
 // attn_chunk.cuh -- what the kernels of new rows behind a cached prefix share:
-// which keys a tile of rows sees, how its walk over them is cut, and how pieces
-// of work are found.
+// which keys a tile of rows sees, how the work is cut, and how it is found.
 //
 // Sequence s holds n new rows and `len` keys, the rows' own keys last: row i is
 // at place p = len - n + i and sees the keys
@@ -8,51 +7,56 @@
 //   j <= p,  and under a window  j > p - window  or  j < sinks.
 //
 // Query heads that share a kv head share its keys, so a tile of rows is made of
-// tokens and heads: row r is token r / heads, head r % heads.
+// tokens and heads: row r is token r / heads, head r % heads.  A unit, one or two
+// tiles, walks the list of the blocks of keys that its rows see.
 //
-// With few rows and many keys a tile's walk is cut into splits whose partial
-// sums are joined afterwards.  How many is a function of the sequence and the
-// call's head counts alone, so that a row's bits do not depend on the batch: a
-// sequence is taken to have the GPU for itself, and gets the number at which
-// kWave CTAs -- one to four rounds of them -- would be done soonest, an item
-// costing its blocks of keys and kEnds more (its first copies, its join).
+// Where a sequence's units are few, or do not fill the GPU's last round, each
+// unit's list is cut into as many splits as would be done soonest; their partial
+// results are joined in order.  How many is a function of the sequence and the
+// call's sizes alone -- a sequence is taken to have the GPU for itself --, so that
+// a row's bits do not depend on the batch.
 #pragma once
 
 #include <stdint.h>
 
 #include "attn_common.cuh"
+#include "gbe_elementwise.h"
 #include "launch.h"
 
 namespace gbe {
 namespace chunk {
 
-constexpr int kBlock = 128;        // keys that a split counts in
-constexpr int kPairRows = 256;     // rows that it takes an item to have
-constexpr int kWave = 152, kRounds = 4, kEnds = 3;
-constexpr int kLeast = 8;          // blocks of a split at least
-constexpr int kMostSplits = 128;
+constexpr int kWave = 152;       // items at a time, which a sequence's splits are to fill
+constexpr int kRounds = 8;       // once at least, and at most as often
+constexpr int kLeast = 1024;     // keys of a split at least
+constexpr int kEnds = 4;         // what an item's first copies, last rows and join cost, in blocks of 128 keys
+constexpr int kUnitRows = 256;   // at most
 
 struct Args {
     ChunkArgs a;
     int group;             // query heads of a kv head
     int heads, parts;      // of a tile, and tiles that a group is cut into
     int tokens;            // of a tile
-    int tiles_per_item;
-    float* part_o;         // [entries, D]
-    float2* part_ml;       // [entries]: running maximum (base 2), running sum
-    int64_t per_seq;
-    int most;
+    int tiles;             // of a unit
+    int width;             // keys of a block
+    int window, sinks;     // a's
+    int most;              // splits at most; 1: nothing is cut
+    int64_t per_seq;       // places for each sequence's; 0: `most` for each row
+    float* part_o;         // [places, D]
+    float2* part_ml;       // [places]: running maximum (base 2), running sum
 };
 
-// The geometry of tiles of `rows` rows.
-inline Args make_args(const ChunkArgs& a, int rows, int tiles_per_item) {
+// The geometry of units of `tiles` tiles of `rows` rows.
+inline Args make_args(const ChunkArgs& a, int rows, int tiles, int width) {
     Args g = {};
     g.a = a;
     g.group = (int)(a.Hq / a.Hkv);
     g.heads = g.group < rows ? g.group : rows;
     g.parts = (g.group + g.heads - 1) / g.heads;
     g.tokens = rows / g.heads;
-    g.tiles_per_item = tiles_per_item;
+    g.tiles = tiles;
+    g.width = width;
+    g.window = (int)a.window, g.sinks = (int)a.sinks;  // (2^30 at most)
     const int64_t keys = a.table == nullptr ? 0 : a.max_pages * a.c.page_size;
     const ChunkRoom r = chunk_room(a.n_seqs, a.T, a.Hq, a.Hkv, keys, a.window, a.sinks);
     g.most = r.most;
@@ -78,116 +82,125 @@ __device__ __forceinline__ Seq sequence(const ChunkArgs& a, int64_t b) {
     return s;
 }
 
-__device__ __forceinline__ int splits_of(const Args& g, const Seq& s) {
-    if (g.most == 1) return 1;
+// How a sequence is cut: its units, and the splits of each.
+struct Cut {
+    int units, splits;
+};
+static __device__ __noinline__ Cut cut_of(const Args& g, const Seq& s) {
     const ChunkArgs& a = g.a;
+    const int Hkv = (int)a.Hkv;
+    Cut c = {0, 1};
+    if (s.n == 0) return c;
+    c.units = ((s.n + g.tokens - 1) / g.tokens * g.parts + g.tiles - 1) / g.tiles;
+    if (g.most == 1 || c.units >= kWave * kRounds) return c;
     int64_t keys = s.len;
-    if (a.window > 0) keys = min(keys, a.window + a.sinks + s.n);
-    const int blocks = (int)((keys + kBlock - 1) / kBlock);
-    const int64_t items = ((int64_t)s.n * g.group + kPairRows - 1) / kPairRows * a.Hkv;
-    const int cap = min(g.most, blocks / kLeast);
-    if (cap < 2 || items < 1 || items >= kWave * kRounds) return 1;
-    const float u = (float)items;
-    int best = 1, cost = ((int)items + kWave - 1) / kWave * (blocks + kEnds);
-#pragma unroll
-    for (int w = 1; w <= kRounds; ++w) {
-        const int n = min(cap, (int)__fdividef((float)(w * kWave) + 0.5f, u));
-        if (n < 2) continue;
-        const int rounds = ((int)items * n + kWave - 1) / kWave;
-        const int c = rounds * ((int)__fdividef((float)(blocks + n - 1) + 0.5f, (float)n) + kEnds);
-        if (c < cost) cost = c, best = n;
+    if (a.window > 0) keys = min(keys, a.window + a.sinks + g.tiles * g.tokens);
+    const int blocks = (int)((keys + 127) / 128), all = c.units * Hkv;
+    const int cap = min(g.most, blocks / (kLeast / 128));
+    if (all >= kWave * kRounds || cap < 2) return c;
+    // what one round, two, ... make possible; worth it from a 16th on
+    float cost = (float)((all + kWave - 1) / kWave * (blocks + kEnds)) * 0.9375f;
+#pragma unroll 1
+    for (int w = kWave; w <= kRounds * kWave; w += kWave) {
+        const int n = min(cap, w / all), rounds = (all * n + kWave - 1) / kWave;
+        const float t = (float)rounds * (__fdividef((float)blocks, (float)n) + kEnds);
+        if (n > 1 && t < cost) cost = t, c.splits = n;
     }
-    return best;
+    return c;
 }
 
-// An item of work: tiles tile, tile + 1, ... (tiles_per_item of them, as far as
-// there are) of a sequence, and one of the splits of their walk.
+// A unit, or a split of it.
 struct Item {
     Seq s;
-    int seq, tile, tiles, split, splits;  // splits 0: no such item
+    int seq, tile, tiles;  // its tiles: tile, tile + 1, ...
+    int split, splits;
 };
 
-// Finds items by their number, asked for in ascending order, by one whole warp:
-// four sequences a lane, the next 128 when the number is past these.
-class Finder {
+// The items of a CTA, one behind the other, by one whole warp: pieces blockIdx.x,
+// blockIdx.x + gridDim.x, ... of all; `zigzag`: every other step in the other
+// direction.  A lane looks up a piece, 32 at a time, in sequences of which a lane
+// holds one, the next 32 when a piece is past these.  (The code is short on
+// purpose: it runs while much else does, and is fetched again each time.)
+class Source {
   public:
-    __device__ __forceinline__ explicit Finder(const Args& g) : g_(g) { load(); }
+    __device__ __forceinline__ Source(const Args& g, bool zigzag) : g_(g), zigzag_(zigzag) {}
 
-    __device__ __forceinline__ Item find(uint64_t index) {
-        Item it = {};
-        while (index >= base_ + total_) {
-            first_ += 128;
-            base_ += total_;
-            if (first_ >= g_.a.n_seqs) {
-                total_ = 0;
-                first_ -= 128;
-                return it;
-            }
-            load();
-        }
-        uint32_t left = (uint32_t)(index - base_);
-        const int lane = threadIdx.x & 31;
-        bool found = false;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            if (found) continue;
-            if (left >= sum_[x]) {
-                left -= sum_[x];
-                continue;
-            }
-            uint32_t upto = count_[x];  // items of this lane's sequence and those before it
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-                if (lane >= d) upto += y;
-            }
-            const int who = __ffs((int)__ballot_sync(0xFFFFFFFFu, upto > left)) - 1;
-            it.s.begin = __shfl_sync(0xFFFFFFFFu, s_[x].begin, who);
-            it.s.n = __shfl_sync(0xFFFFFFFFu, s_[x].n, who);
-            it.s.len = __shfl_sync(0xFFFFFFFFu, s_[x].len, who);
-            it.splits = __shfl_sync(0xFFFFFFFFu, splits_[x], who);
-            left -= __shfl_sync(0xFFFFFFFFu, upto - count_[x], who);
-            it.seq = (int)first_ + x * 32 + who;
-            found = true;
-        }
-        const int tiles = tiles_of(it.s.n), items = (tiles + g_.tiles_per_item - 1) / g_.tiles_per_item;
-        const int k = (int)(left / (uint32_t)it.splits);
-        it.split = (int)(left - (uint32_t)k * (uint32_t)it.splits);
-        it.tile = (items - 1 - k) * g_.tiles_per_item;  // the last rows, which see the most, first
-        it.tiles = min(g_.tiles_per_item, tiles - it.tile);
-        return it;
+    __device__ __forceinline__ bool next(Item& it, int& kvh) {
+        const int from = turn_ & 31;
+        if (from == 0) look_up();
+        ++turn_;
+        it.splits = __shfl_sync(0xFFFFFFFFu, splits_, from);
+        if (it.splits == 0) return false;
+        it.s.begin = __shfl_sync(0xFFFFFFFFu, s_.begin, from);
+        it.s.n = __shfl_sync(0xFFFFFFFFu, s_.n, from);
+        it.s.len = __shfl_sync(0xFFFFFFFFu, s_.len, from);
+        it.seq = __shfl_sync(0xFFFFFFFFu, seq_, from);
+        it.tile = __shfl_sync(0xFFFFFFFFu, unit_, from) * g_.tiles;
+        it.tiles = min(g_.tiles, (it.s.n + g_.tokens - 1) / g_.tokens * g_.parts - it.tile);
+        it.split = __shfl_sync(0xFFFFFFFFu, split_, from);
+        kvh = __shfl_sync(0xFFFFFFFFu, kvh_, from);
+        return true;
     }
 
   private:
-    __device__ __forceinline__ int tiles_of(int n) const { return (n + g_.tokens - 1) / g_.tokens * g_.parts; }
-    __device__ __forceinline__ void load() {
-        total_ = 0;
+    // The lane's piece; splits_ 0: there is none, nor any behind it.
+    __device__ __noinline__ void look_up() {
+        const int lane = threadIdx.x & 31, round = turn_ + lane;
+        const uint64_t index =
+            (uint64_t)round * gridDim.x + (zigzag_ && (round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        splits_ = 0;
+        for (;;) {
+            const uint32_t total = __shfl_sync(0xFFFFFFFFu, upto_, 31);
+            const bool here = splits_ == 0 && index >= base_ && index - base_ < total;
+            const uint32_t at = here ? (uint32_t)(index - base_) : 0u;
+            int who = 0;  // the first lane whose sequences' pieces go up to more than `at`
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            count_[x] = 0, sum_[x] = 0, splits_[x] = 1;
-            s_[x] = {0, 0, 0};
-            if (first_ + x * 32 >= g_.a.n_seqs) continue;
-            s_[x] = sequence(g_.a, first_ + x * 32 + (threadIdx.x & 31));
-            if (s_[x].n > 0) {
-                splits_[x] = splits_of(g_, s_[x]);
-                count_[x] = (uint32_t)((tiles_of(s_[x].n) + g_.tiles_per_item - 1) / g_.tiles_per_item) *
-                            (uint32_t)splits_[x];
+            for (int step = 16; step >= 1; step >>= 1)
+                if (__shfl_sync(0xFFFFFFFFu, upto_, who + step - 1) <= at) who += step;
+            const uint32_t before = __shfl_sync(0xFFFFFFFFu, upto_, who == 0 ? 0 : who - 1);
+            const Seq s = {__shfl_sync(0xFFFFFFFFu, group_.begin, who), __shfl_sync(0xFFFFFFFFu, group_.n, who),
+                           __shfl_sync(0xFFFFFFFFu, group_.len, who)};
+            const int units = __shfl_sync(0xFFFFFFFFu, cut_.units, who);
+            const int splits = __shfl_sync(0xFFFFFFFFu, cut_.splits, who);
+            if (here) {
+                // kv heads innermost, then units, the last rows, which see the most, first; splits outermost, so that
+                // what runs at a time reads the same keys
+                const uint32_t x = at - (who == 0 ? 0u : before), y = x / (uint32_t)g_.a.Hkv;
+                kvh_ = (int)(x - y * (uint32_t)g_.a.Hkv);
+                split_ = (int)(y / (uint32_t)units);
+                unit_ = units - 1 - (int)(y - (uint32_t)split_ * (uint32_t)units);
+                s_ = s, splits_ = splits, seq_ = (int)first_ + who;
             }
-            sum_[x] = __reduce_add_sync(0xFFFFFFFFu, count_[x]);
-            total_ += sum_[x];
+            const bool past = splits_ == 0 && index >= base_ + total;
+            if (!__any_sync(0xFFFFFFFFu, past) || first_ + 32 >= g_.a.n_seqs) return;
+            first_ += 32;
+            base_ += total;
+            group_ = sequence(g_.a, first_ + lane);
+            cut_ = cut_of(g_, group_);
+            upto_ = (uint32_t)cut_.units * (uint32_t)cut_.splits * (uint32_t)g_.a.Hkv;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, upto_, d);
+                if (lane >= d) upto_ += y;
+            }
         }
     }
     const Args& g_;
-    int64_t first_ = 0;
+    const bool zigzag_;
+    // of the sequences at hand, first_ + lane: this one, and the pieces up to it
+    int64_t first_ = -32;
     uint64_t base_ = 0;
-    uint32_t total_ = 0, sum_[4], count_[4];
-    Seq s_[4];
-    int splits_[4];
+    Seq group_ = {0, 0, 0};
+    Cut cut_ = {0, 1};
+    uint32_t upto_ = 0;
+    int turn_ = 0;  // pieces taken so far
+    // the lane's piece
+    Seq s_;
+    int seq_, kvh_, unit_, split_, splits_;
 };
 
-// The blocks of `width` keys that some row of an item's tiles sees, as a list:
-// those that hold a sink, then from the first under the window to the last row's
-// place; and the part of it that is the item's split.
+// An item's walk over the list: blocks that hold a sink, then from the first one
+// under the window to the last row's place.
 struct Walk {
     int first_place, last_place;  // of the item's rows
     int sinks;                    // blocks of sinks ahead of the window
@@ -195,34 +208,40 @@ struct Walk {
     int from, to;                 // the split's part of the list
     __device__ __forceinline__ int block(int i) const { return i < sinks ? i : window + (i - sinks); }
 };
-__device__ __forceinline__ Walk walk(const Args& g, const Item& it, int width) {
+__device__ __forceinline__ Walk walk(const Args& g, const Item& it) {
     Walk w;
     const int last_tile = it.tile + it.tiles - 1;
     w.first_place = it.s.len - it.s.n + it.tile / g.parts * g.tokens;
     w.last_place = it.s.len - it.s.n + min(it.s.n, (last_tile / g.parts + 1) * g.tokens) - 1;
-    const int end = w.last_place < 0 ? 0 : w.last_place / width + 1;
-    const int64_t low = g.a.window > 0 ? max((int64_t)w.first_place - g.a.window + 1, (int64_t)0) : 0;
-    w.window = (int)min(low / width, (int64_t)end);
-    w.sinks = (int)min((min(g.a.sinks, (int64_t)w.last_place + 1) + width - 1) / width, (int64_t)w.window);
-    if (w.sinks < 0) w.sinks = 0;
-    const int64_t n = w.sinks + end - w.window;
-    w.from = (int)(n * it.split / it.splits);
-    w.to = (int)(n * (it.split + 1) / it.splits);
+    const int end = w.last_place < 0 ? 0 : w.last_place / g.width + 1;
+    w.window = w.sinks = 0;
+    if (g.window > 0) {
+        w.window = min(max(w.first_place - g.window + 1, 0) / g.width, end);
+        w.sinks = min((max(min(g.sinks, w.last_place + 1), 0) + g.width - 1) / g.width, w.window);
+    }
+    const int n = w.sinks + end - w.window;
+    w.from = 0, w.to = n;
+    if (it.splits > 1) {
+        w.from = (int)((int64_t)n * it.split / it.splits);
+        w.to = (int)((int64_t)n * (it.split + 1) / it.splits);
+    }
     return w;
 }
 
-// Where a row's partial result of an item lies.
+// Where a row's partial results lie, one behind the other, and where the item's is.
+__device__ __forceinline__ int64_t parts_at(const Args& g, const Item& it, int token, int head) {
+    if (g.per_seq > 0) return it.seq * g.per_seq + ((int64_t)token * g.a.Hq + head) * it.splits;
+    return ((int64_t)(it.s.begin + token) * g.a.Hq + head) * g.most;
+}
 __device__ __forceinline__ int64_t part_at(const Args& g, const Item& it, int token, int head) {
-    if (g.per_seq > 0)
-        return it.seq * g.per_seq + ((int64_t)token * g.a.Hq + head) * it.splits + it.split;
-    return ((int64_t)(it.s.begin + token) * g.a.Hq + head) * g.most + it.split;
+    return parts_at(g, it, token, head) + it.split;
 }
 
 // The tensor-core form: bf16 rows and, where there is a cache, one of a page at
-// least; D <= 128, rows on the 16-byte grid, all in device memory.
+// least; D <= 128, rows, the cache's too, on the 16-byte grid, all in device memory.
 cudaError_t launch_tc(const ChunkArgs& a, cudaStream_t st);
 
-// The splits of every row added in order.
+// The partial results of every row added in order.
 cudaError_t launch_join(const Args& g, int dtype, cudaStream_t st);
 
 }  // namespace chunk

@@ -46,18 +46,28 @@ constexpr int kWidenWarp = 12;   // over an 8-bit cache, and the three after it
 constexpr float kGrowth = 8.0f;  // a maximum may lag this many powers of two
 constexpr int kPacked = -1;      // KV of rows that are not in a cache
 
-// What the item warp hands out; item.splits 0: nothing more.
+// What the item warp hands out.  Of two tiles, tile t goes to slot t -- its
+// softmax warpgroup, its thread of products and their tensor memory --; one alone
+// goes to the other slot than the one before, so that its first products and
+// weights are under way while the last one's rows are written.
 struct Todo {
     Item item;
-    int kvh;
+    Walk walk;
+    int kvh, slot;  // slot -1: nothing more
+    __device__ __forceinline__ int blocks() const { return walk.to - walk.from; }
+    __device__ __forceinline__ bool two() const { return item.tiles == 2; }
+    __device__ __forceinline__ bool has(int t) const { return two() || slot == t; }
+    // the number of slot t's tile
+    __device__ __forceinline__ int tile(int t) const { return item.tile + (two() ? t : 0); }
 };
 constexpr int kTodos = 4;  // in hand
 
 struct Control {
-    uint64_t q_full[2], q_empty, kv_full[8], kv_empty[8], s_full[2], s_free[2], p_ready[2], o_done[2], o_free[2];
-    uint64_t drained[2];
-    uint64_t todo_full[kTodos], todo_empty[kTodos];
+    uint64_t q_full[2], q_empty[2], s_last[2], kv_full[8], kv_empty[8], s_full[2], s_free[2], p_ready[2], o_done[2], o_free[2];
+    uint64_t drained[2], raw_full[3], raw_empty[3];
+    uint64_t todo_full[kTodos], todo_empty[kTodos], todo_checked[kTodos];
     Todo todo[kTodos];
+    int gone[kTodos];  // (once checked) whether a page of the item's walk is not in the cache
     uint32_t tmem;
     int abort;
 };
@@ -69,17 +79,17 @@ struct Shape {
     // Registers of a thread: 384 threads were launched with 168 each (64512), the
     // softmax warpgroups take 208 and the issuing one keeps 80 (63488); 512 threads
     // with 128 (65536): 200, and 56 of the issuing and the widening one (65536).
-    static constexpr int kSoftmaxRegs = kE4 ? 200 : 208, kOtherRegs = kE4 ? 56 : 80;
+    static constexpr int kSoftmaxRegs = kE4 ? 200 : 208, kIssueRegs = kE4 ? 56 : 80, kWidenRegs = 56;
     static constexpr int kReaders = kE4 ? 15 : 11;        // warps that read an item: all but the one that finds it
     static constexpr int kPanel = 128 * 128;              // 128 rows of 64 bf16
     static constexpr int kTile = kPanel * (DP / 64);      // 128 rows of DP
     static constexpr int kStages = (kE4 ? 3 : 4) * (128 / DP);
-    static constexpr int kOutRow = kE4 ? 32 : 128;        // bytes of a row on their way out
+    static constexpr int kOutRow = kE4 ? 32 : 64;         // bytes of a row on their way out
     static constexpr int kOut = 8 * 32 * kOutRow;         // 32 rows for each softmax warp
-    // 8-bit rows on their way in, where they lie and their scales
-    static constexpr int kRaw = kE4 ? kN * DP : 0, kRaws = 3;
-    static constexpr int kPlaces = kE4 ? 2 * kN * 8 + 4 * kN * 2 : 0;
-    static constexpr int kControlAt = kTile * (2 + kStages) + kOut + kRaws * kRaw + kPlaces;
+    // 8-bit rows on their way in, 64 bytes of each in a panel, and the scales of two blocks
+    static constexpr int kRaw = kE4 ? kN * DP : 0, kRaws = 3, kRawPanel = kN * 64;
+    static constexpr int kRawAt = kTile * (2 + kStages) + kOut, kScaleAt = kRawAt + kRaws * kRaw;
+    static constexpr int kControlAt = kScaleAt + (kE4 ? 2 * 2 * kN : 0);
     static constexpr int kBytes = kControlAt + 1024 + (int)sizeof(Control);
     // where piece c (16 bytes) of row r of a warp's rows lies on its way out
     __device__ static __forceinline__ int out_at(int r, int c) {
@@ -150,12 +160,12 @@ __device__ __forceinline__ uint32_t not_finite(float4 x) {
 }
 
 // Which keys of a block, as bits, a row at `place` sees: word x is of keys
-// k0 + 32 x and on.
-__device__ __forceinline__ uint32_t first_bits(int64_t n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
-__device__ __forceinline__ uint32_t seen_word(const ChunkArgs& a, int place, int k0, int x) {
-    const int64_t at = k0 + 32 * x;
+// k0 + 32 x and on.  (Places, windows and sinks are 2^30 at most.)
+__device__ __forceinline__ uint32_t first_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+__device__ __forceinline__ uint32_t seen_word(const Args& g, int place, int k0, int x) {
+    const int at = k0 + 32 * x;
     uint32_t m = first_bits(place + 1 - at);
-    if (a.window > 0) m &= ~first_bits(place + 1 - a.window - at) | first_bits(a.sinks - at);
+    if (g.window > 0) m &= ~first_bits(place + 1 - g.window - at) | first_bits(g.sinks - at);
     return m;
 }
 
@@ -166,14 +176,14 @@ __device__ __noinline__ void exact_row(const Args& g, const Item& it, int kvh, i
     const ChunkArgs& a = g.a;
     const int lane = threadIdx.x & 31, D = (int)a.D, place = it.s.len - it.s.n + token;
     const float c = a.scale * kLog2e;
-    const Walk w = walk(g, it, kN);
+    const Walk w = walk(g, it);
     const int64_t row = (it.s.begin + (int64_t)token) * a.q_stride + ((int64_t)kvh * g.group + head) * D;
     float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f), o = q;
     if (lane * 4 < D) q = load4(a.q, row + lane * 4);
     float m = -INFINITY, l = 0.0f;
     for (int i = w.from * 4; i < w.to * 4; ++i) {
         const int k0 = w.block(i >> 2) * kN + (i & 3) * 32, j = k0 + lane;
-        bool seen = seen_word(a, place, w.block(i >> 2) * kN, i & 3) >> lane & 1u;
+        bool seen = seen_word(g, place, w.block(i >> 2) * kN, i & 3) >> lane & 1u;
         const int64_t at = seen ? key_at<KV>(a, it, kvh, j) : -1;
         seen = at >= 0;
         if (!__any_sync(0xFFFFFFFFu, seen)) continue;
@@ -233,7 +243,7 @@ __device__ __noinline__ void repair_row(const Args& g, const Item& it, int kvh, 
     const ChunkArgs& a = g.a;
     const int lane = threadIdx.x & 31, D = (int)a.D, place = it.s.len - it.s.n + token;
     const bool mine = lane * 4 < D;
-    const Walk w = walk(g, it, kN);
+    const Walk w = walk(g, it);
     uint32_t open = 0;  // entries that may have to be computed again
     if (mine) {
         if (it.splits > 1)
@@ -249,8 +259,8 @@ __device__ __noinline__ void repair_row(const Args& g, const Item& it, int kvh, 
         for (int i = (w.to - w.from) * 4 - 1; i >= 0; --i) {
             if (!__any_sync(0xFFFFFFFFu, until & ~bad)) break;
             const int k0 = w.block(w.from + (i >> 2)) * kN;
-            uint32_t keys = seen_word(a, place, k0, i & 3);
-            if (!seen) keys = ~keys & first_bits((int64_t)it.s.len - k0 - 32 * (i & 3));
+            uint32_t keys = seen_word(g, place, k0, i & 3);
+            if (!seen) keys = ~keys & first_bits(it.s.len - k0 - 32 * (i & 3));
             for (; keys; keys &= keys - 1) {
                 const int64_t at = key_at<KV>(a, it, kvh, k0 + 32 * (i & 3) + __ffs((int)keys) - 1);
                 if (at >= 0 && mine) bad |= not_finite(load_kv<KV, true>(a, kvh, at, lane * 4));
@@ -263,56 +273,33 @@ __device__ __noinline__ void repair_row(const Args& g, const Item& it, int kvh, 
     if (__any_sync(0xFFFFFFFFu, open)) exact_row<KV>(g, it, kvh, token, head);
 }
 
-// Work item `round` of this CTA: rounds go back and forth over the CTAs, so that
-// no CTA always gets the larger one.
-__device__ __forceinline__ uint64_t id_of(uint64_t round) {
-    return round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-}
-
 // After a wait that gave up: NaN in every row of this CTA's items, done or not.
 // By one warp.
 __device__ __noinline__ void give_up(const Args& g) {
     const ChunkArgs& a = g.a;
-    Finder finder(g);
-    for (uint64_t round = 0;; ++round) {
-        const uint64_t id = id_of(round);
-        const Item it = finder.find(id / (uint32_t)a.Hkv);
-        if (it.splits == 0) return;
-        const int kvh = (int)(id % (uint32_t)a.Hkv);
+    Source items(g, true);
+    Item it;
+    int kvh;
+    while (items.next(it, kvh))
         for (int r = threadIdx.x & 31; r < it.tiles * kM; r += 32) {
             const Row x = row_of(g, it, it.tile + r / kM, r % kM);
             if (!x.there) continue;
             const int head = kvh * g.group + x.head;
-            if (it.splits > 1)
-                g.part_ml[part_at(g, it, x.token, head)] = make_float2(0.0f, __uint_as_float(0x7FC00000u));
+            if (it.splits > 1) g.part_ml[part_at(g, it, x.token, head)] = make_float2(0.0f, __uint_as_float(0x7FC00000u));
             uint16_t* const out =
                 static_cast<uint16_t*>(a.out) + (it.s.begin + (int64_t)x.token) * a.out_stride + (int64_t)head * a.D;
             for (int d = 0; d < a.D; ++d) out[d] = 0x7FC0;
         }
-    }
 }
 
 // ---- an 8-bit cache's rows -----------------------------------------------------------
 
-// 16 bytes into shared memory, the first `from` of them from memory and zeros
-// behind them; rows off the 16-byte grid in two halves.
-__device__ __forceinline__ void copy_async(uint32_t to, const uint8_t* p, int from, bool grid16) {
-    if (grid16) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(from) : "memory");
-        return;
-    }
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(p), "r"(min(from, 8)) : "memory");
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + 8), "l"(from > 8 ? p + 8 : p),
-                 "r"(max(from - 8, 0))
-                 : "memory");
-}
-
 // Sixteen codes times 2^(byte - 127), exact in bf16 from 2^-126 on; byte 0:
 // zeros.  A code's bits, its exponent and mantissa moved to where bf16 has them,
-// are 2^-120 of its value; one product brings that and the scale.  Rows of byte
-// 135 and above (2^(byte - 7) is past bf16's range), and NaN codes, which that way
-// would come out as 480, go through f32.
-__device__ __forceinline__ void widen16(const Vec16& codes, uint32_t byte, Vec16& lo, Vec16& hi) {
+// are 2^-120 of its value; one product brings that and the scale.  False for what
+// has to go through f32: rows of byte 135 and above (2^(byte - 7) is past bf16's
+// range), and NaN codes, which that way come out as 480.
+__device__ __forceinline__ bool widen16(const Vec16& codes, uint32_t byte, Vec16& lo, Vec16& hi) {
     uint32_t nan = 0, w[8];
     const uint32_t field = byte == 0 ? 0u : (byte + 120u) << 7, scale = field | field << 16;
 #pragma unroll
@@ -325,157 +312,78 @@ __device__ __forceinline__ void widen16(const Vec16& codes, uint32_t byte, Vec16
             asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w[2 * x + h]) : "r"(z), "r"(scale));
         }
     }
-    if (byte != 0 && ((nan & 0x80808080u) || byte > 134u)) {
-        const float s = __uint_as_float(byte << 23);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            float f[4];
-            e4m3x4_to_f32(codes.w[x], f);
-            w[2 * x] = f32x2_to_bf16x2_bits(f[0] * s, f[1] * s);
-            w[2 * x + 1] = f32x2_to_bf16x2_bits(f[2] * s, f[3] * s);
-        }
-    }
 #pragma unroll
     for (int x = 0; x < 4; ++x) lo.w[x] = w[x], hi.w[x] = w[4 + x];
+    return byte == 0 || (!(nan & 0x80808080u) && byte <= 134u);
+}
+__device__ __forceinline__ void widen16_f32(const Vec16& codes, uint32_t byte, Vec16& lo, Vec16& hi) {
+    const float s = __uint_as_float(byte << 23);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        float f[4];
+        e4m3x4_to_f32(codes.w[x], f);
+        uint32_t* const w = x < 2 ? lo.w + 2 * x : hi.w + 2 * (x - 2);
+        w[0] = f32x2_to_bf16x2_bits(f[0] * s, f[1] * s);
+        w[1] = f32x2_to_bf16x2_bits(f[2] * s, f[3] * s);
+    }
 }
 
-// The warps that bring an 8-bit cache's rows into the ring as bf16.  Blocks are
-// counted over all items; of block B, k is load 2 B and v load 2 B + 1.  A thread
-// copies pieces of 16 codes into places of its own and widens them itself, so
-// that it waits for nobody but its own copies; two loads are on their way while
-// one is widened.  Where a block's rows lie is looked up by a thread a row, two
-// blocks ahead.
+// The warps that widen an 8-bit cache's rows, as the copying warp brings them,
+// into the ring.  Loads are counted over all items: k of block b is 2 b, v 2 b + 1.
 template <int DP>
-__device__ __forceinline__ void widen_rows(const Args& g, Control& ctl, uint8_t* const smem, uint32_t kv_smem) {
+__device__ __forceinline__ void widen_rows(Control& ctl, uint8_t* const smem) {
     using S = Shape<GBE_KV_E4M3, DP>;
     constexpr int kPieces = DP / 16, kRows = 128 / kPieces, kTurns = kN / kRows;
-    const ChunkArgs& a = g.a;
     const int tid = threadIdx.x - kWidenWarp * 32, lane = threadIdx.x & 31;
     volatile int* const abort = &ctl.abort;
-    uint8_t* const raw = smem + S::kTile * (2 + S::kStages) + S::kOut;
-    int64_t* const places = reinterpret_cast<int64_t*>(raw + S::kRaws * S::kRaw);  // [2][kN], of block B in B & 1
-    uint8_t* const scales = reinterpret_cast<uint8_t*>(places + 2 * kN);           // [4][k, v][kN], in B & 3
-    const int piece = tid % kPieces, r0 = tid / kPieces;
-    const int size = min(max((int)a.D - piece * 16, 0), 16);
-    const bool grid16 = a.D % 16 == 0 && a.c.page_stride % 16 == 0;
-    auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-
-    // the walk over all items' blocks
-    int todo = 0, x = 0, seq = 0, len = 0, kvh = 0;
-    Walk w = {};
-    bool end = false;
-    // the next block: false behind the last one.  Asks for the page of the thread's
-    // row of it; `locate` says where it lies and its scales' index, -1: nowhere.
-    int32_t page = -1;
-    int row = 0;
-    auto next = [&] {
-        page = -1;
-        while (!end && x == w.to) {
-            const bool ok = mbar_wait(smem_addr(&ctl.todo_full[todo % kTodos]), todo / kTodos & 1, abort);
-            end = !__all_sync(0xFFFFFFFFu, ok);
-            if (end) break;
-            const Item it = ctl.todo[todo % kTodos].item;
-            kvh = ctl.todo[todo % kTodos].kvh;
+    // Eight lanes have four pieces of 16 codes of two rows: what they read, and what
+    // they write, a piece's halves one after the other, meets eight bank groups.
+    const int panel = DP == 128 ? tid >> 3 & 1 : 0, piece = tid & 3;
+    const int r0 = DP == 128 ? (tid >> 2 & 1) | tid >> 4 << 1 : tid >> 2;
+    const uint8_t* const from = smem + S::kRawAt + panel * S::kRawPanel + r0 * 64 + piece * 16;
+    uint8_t* const to = smem + 2 * S::kTile + panel * S::kPanel + r0 * 128;
+    int load = 0;
+    for (int i = 0;; ++i) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.todo_full[i % kTodos]), i / kTodos & 1, abort))) return;
+        const int n = ctl.todo[i % kTodos].blocks(), slot = ctl.todo[i % kTodos].slot;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&ctl.todo_empty[i % kTodos]));
+        if (slot < 0) return;
+        for (const int end = load + 2 * n; load < end; ++load) {
+            const int raw = load % S::kRaws, stage = load % S::kStages;
+            bool ok = mbar_wait(smem_addr(&ctl.raw_full[raw]), load / S::kRaws & 1, abort);
+            ok = ok && mbar_wait(smem_addr(&ctl.kv_empty[stage]), (load / S::kStages & 1) ^ 1, abort);
+            if (!__all_sync(0xFFFFFFFFu, ok)) return;
+            const uint8_t* const scale = smem + S::kScaleAt + (load & 3) * kN + r0;
+            auto codes = [&](int x) { return *reinterpret_cast<const Vec16*>(from + raw * S::kRaw + x * (kRows * 64)); };
+            auto write = [&](int x, const Vec16& lo, const Vec16& hi) {
+                const int r = r0 + x * kRows, c = piece * 2;
+                uint8_t* const line = to + stage * S::kTile + x * (kRows * 128);
+                *reinterpret_cast<Vec16*>(line + ((c ^ (r & 7)) << 4)) = lo;
+                *reinterpret_cast<Vec16*>(line + (((c + 1) ^ (r & 7)) << 4)) = hi;
+            };
+            uint32_t again = 0;
+#pragma unroll 2
+            for (int x = 0; x < kTurns; ++x) {
+                Vec16 lo, hi;
+                if (!widen16(codes(x), scale[x * kRows], lo, hi)) again |= 1u << x;
+                write(x, lo, hi);
+            }
+#pragma unroll 1
+            for (; again; again &= again - 1) {
+                const int x = __ffs((int)again) - 1;
+                Vec16 lo, hi;
+                widen16_f32(codes(x), scale[x * kRows], lo, hi);
+                write(x, lo, hi);
+            }
+            async_proxy_fence();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&ctl.todo_empty[todo % kTodos]));
-            ++todo;
-            end = it.splits == 0;
-            if (end) break;
-            w = walk(g, it, kN);
-            x = w.from, seq = it.seq, len = it.s.len;
-        }
-        if (end) return false;
-        const int j = w.block(x++) * kN + tid;
-        if (j < len) {
-            const int page_i = j / a.c.page_size;
-            row = j - page_i * a.c.page_size;
-            page = a.table[seq * a.max_pages + page_i];
-        }
-        return true;
-    };
-    int64_t at = -1, scale_at = -1;
-    auto locate = [&] {
-        const bool there = page >= 0 && page < a.c.n_pages;
-        at = there ? page * a.c.page_stride + ((int64_t)kvh * a.c.page_size + row) * a.D : -1;
-        scale_at = there ? ((int64_t)page * a.c.Hkv + kvh) * a.c.page_size + row : -1;
-    };
-    auto keep_places = [&](int block) { places[(block & 1) * kN + tid] = at; };
-    uint32_t bytes = 0;
-    auto load_scales = [&] {
-        bytes = scale_at < 0 ? 0u : (uint32_t)a.c.k_scale[scale_at] | (uint32_t)a.c.v_scale[scale_at] << 8;
-    };
-    auto keep_scales = [&](int block) {
-        scales[((block & 3) * 2) * kN + tid] = (uint8_t)bytes;
-        scales[((block & 3) * 2 + 1) * kN + tid] = (uint8_t)(bytes >> 8);
-    };
-    auto fetch = [&](int load, bool there) {  // (an empty group behind the last one)
-        if (there) {
-            const uint8_t* const src = static_cast<const uint8_t*>(load & 1 ? a.c.v : a.c.k);
-            const uint32_t to = smem_addr(raw + load % S::kRaws * S::kRaw + tid * 16);
-            const int64_t* const place = places + (load >> 1 & 1) * kN + r0;
-#pragma unroll
-            for (int i = 0; i < kTurns; ++i) {
-                const int64_t p = place[i * kRows];
-                const bool here = p >= 0 && size > 0;
-                copy_async(to + i * 2048, src + (here ? p + piece * 16 : 0), here ? size : 0, grid16);
+            if (lane == 0) {
+                mbar_arrive(smem_addr(&ctl.kv_full[stage]));
+                mbar_arrive(smem_addr(&ctl.raw_empty[raw]));
             }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    auto widen = [&](int load) {
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-        const int stage = load % S::kStages;
-        const bool ok = mbar_wait(smem_addr(&ctl.kv_empty[stage]), (load / S::kStages & 1) ^ 1, abort);
-        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
-        const uint8_t* const from = raw + load % S::kRaws * S::kRaw + tid * 16;
-        const uint8_t* const scale = scales + ((load >> 1 & 3) * 2 + (load & 1)) * kN + r0;
-        uint8_t* const to = smem + (kv_smem - smem_addr(smem)) + stage * S::kTile + (piece >> 2) * S::kPanel;
-#pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-            const int r = i * kRows + r0, c = (piece & 3) * 2;
-            Vec16 lo, hi;
-            widen16(*reinterpret_cast<const Vec16*>(from + i * 2048), scale[i * kRows], lo, hi);
-            // (lanes of the second panel write their upper half first: eight lanes then meet eight bank groups)
-            const bool second = piece >> 2;
-            uint8_t* const line = to + r * 128;
-            *reinterpret_cast<Vec16*>(line + (((c + second) ^ (r & 7)) << 4)) = second ? hi : lo;
-            *reinterpret_cast<Vec16*>(line + (((c + !second) ^ (r & 7)) << 4)) = second ? lo : hi;
-        }
-        async_proxy_fence();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&ctl.kv_full[stage]));
-        return true;
-    };
-
-    bool have0 = next();
-    locate();
-    keep_places(0);
-    load_scales();
-    keep_scales(0);
-    bool have1 = next();
-    locate();
-    keep_places(1);
-    load_scales();
-    keep_scales(1);
-    sync();
-    fetch(0, have0);
-    fetch(1, have0);
-    fetch(2, have1);
-    for (int b = 0; have0; ++b) {
-        // (places of block b + 2 take those of block b, whose last use, the fetch of its v, was ahead of the last sync)
-        const bool have2 = next();
-        if (!widen(2 * b)) break;
-        fetch(2 * b + 3, have1);
-        locate();
-        keep_places(b + 2);
-        load_scales();
-        sync();
-        if (!widen(2 * b + 1)) break;
-        keep_scales(b + 2);
-        fetch(2 * b + 4, have2);
-        have0 = have1, have1 = have2;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <int KV, int DP>
@@ -492,13 +400,14 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
     volatile int* const abort = &ctl.abort;
 
     if (threadIdx.x == 0) {
-        mbar_init(smem_addr(&ctl.q_empty), 2);
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(smem_addr(&ctl.kv_full[i]), S::kE4 ? 4 : 1);
             mbar_init(smem_addr(&ctl.kv_empty[i]), 2);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_addr(&ctl.q_full[t]), 1);
+            mbar_init(smem_addr(&ctl.q_empty[t]), 1);
+            mbar_init(smem_addr(&ctl.s_last[t]), 4);
             mbar_init(smem_addr(&ctl.s_full[t]), 1);
             mbar_init(smem_addr(&ctl.p_ready[t]), 4);
             mbar_init(smem_addr(&ctl.s_free[t]), 4);
@@ -506,8 +415,13 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
             mbar_init(smem_addr(&ctl.o_free[t]), 4);
             mbar_init(smem_addr(&ctl.drained[t]), 1);
         }
+        for (int i = 0; i < S::kRaws; ++i) {
+            mbar_init(smem_addr(&ctl.raw_full[i]), 1);
+            mbar_init(smem_addr(&ctl.raw_empty[i]), 4);
+        }
         for (int i = 0; i < kTodos; ++i) {
             mbar_init(smem_addr(&ctl.todo_full[i]), 1);
+            mbar_init(smem_addr(&ctl.todo_checked[i]), 1);
             mbar_init(smem_addr(&ctl.todo_empty[i]), S::kReaders);
         }
         ctl.abort = 0;
@@ -528,61 +442,103 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
     auto todo_ready = [&](int i) { return mbar_wait(smem_addr(&ctl.todo_full[i % kTodos]), i / kTodos & 1, abort); };
     auto todo_read = [&](int i) { mbar_arrive(smem_addr(&ctl.todo_empty[i % kTodos])); };
 
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOtherRegs));
-        if (warp >= kWidenWarp) {
-            if constexpr (S::kE4) widen_rows<DP>(g, ctl, smem, kv_smem);
-        } else if (warp == kItemWarp) {
-            Finder finder(g);
-            bool ok = true;
-            for (int i = 0; ok; ++i) {
-                const uint64_t id = id_of(i);
-                const Item it = finder.find(id / (uint32_t)a.Hkv);
-                ok = __all_sync(0xFFFFFFFFu,
-                                mbar_wait(smem_addr(&ctl.todo_empty[i % kTodos]), (i / kTodos & 1) ^ 1, abort));
-                if (!ok) break;
-                if (lane == 0) {
-                    ctl.todo[i % kTodos].item = it;
-                    ctl.todo[i % kTodos].kvh = (int)(id % (uint32_t)a.Hkv);
-                    mbar_arrive(smem_addr(&ctl.todo_full[i % kTodos]));
-                }
-                if (it.splits == 0) break;
-            }
-        } else if (warp == kLoadWarp) {
-            int loads = 0, tiles[2] = {0, 0};  // of the ring and tiles of q so far
-            int items = 0;                     // with a block
-            bool ok = true;
-            const int boxes = kN / box;        // of a block; a power of two
-            for (int i = 0; ok; ++i) {
-                if (!(ok = __all_sync(0xFFFFFFFFu, todo_ready(i)))) break;
-                const Item it = ctl.todo[i % kTodos].item;
-                const int kvh = ctl.todo[i % kTodos].kvh;
-                __syncwarp();
-                if (lane == 0) todo_read(i);
-                if (it.splits == 0) break;
-                const Walk w = walk(g, it, kN);
-                if (w.from == w.to) continue;
-                auto load_q = [&] {  // once the last item's is done with
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.q_empty), (items & 1) ^ 1, abort));
-                    if (!ok) return;
-                    ++items;
-                    for (int t = 0; t < it.tiles; ++t) {
-                        const int u = it.tile + t;
+    if (S::kE4 && warp >= kWidenWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kWidenRegs));
+        if constexpr (S::kE4) widen_rows<DP>(ctl, smem);
+    } else if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kIssueRegs));
+        if (warp == kItemWarp) {
+            Source items(g, true);
+            bool ok = true, more = true;
+            int tiles[2] = {0, 0};  // of q so far
+            int last = 1;           // the slot that S was last for
+            Item q_item = {};       // whose q is to be fetched, once its slots' last one is done with
+            int q_kvh = 0, q_slot = -1;
+            auto load_q = [&](bool wait) {
+                if (q_slot < 0) return;
+                for (int t = 0; t < 2; ++t)
+                    if (q_item.tiles == 2 || t == q_slot) {
+                        const uint32_t bar = smem_addr(&ctl.q_empty[t]);
+                        if (!wait && !__all_sync(0xFFFFFFFFu, mbar_try(bar, (tiles[t] & 1) ^ 1))) return;
+                        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, (tiles[t] & 1) ^ 1, abort));
+                        if (!ok) return;
+                    }
+                for (int t = 0; t < 2; ++t)
+                    if (q_item.tiles == 2 || t == q_slot) {
+                        const int u = q_item.tile + (q_item.tiles == 2 ? t : 0);
                         if (lane == 0) {
                             const uint32_t qb = smem_addr(&ctl.q_full[t]);
                             mbar_arrive_tx(qb, (DP / 64) * 128 * g.heads * g.tokens);
 #pragma unroll
                             for (int p = 0; p < DP / 64; ++p)
                                 tma_load_3d(q_smem + t * S::kTile + p * S::kPanel, &maps.q, qb, p * 64,
-                                            kvh * g.group + u % g.parts * g.heads, it.s.begin + u / g.parts * g.tokens);
+                                            q_kvh * g.group + u % g.parts * g.heads,
+                                            q_item.s.begin + u / g.parts * g.tokens);
                         }
                         ++tiles[t];
                     }
-                };
-                if constexpr (S::kE4) {
-                    load_q();
-                    continue;
+                q_slot = -1;
+            };
+            for (int i = 0; ok && more; ++i) {
+                Todo todo;
+                more = items.next(todo.item, todo.kvh);
+                todo.slot = -1;
+                if (more) {
+                    todo.walk = walk(g, todo.item);
+                    todo.slot = todo.two() || todo.blocks() == 0 ? 0 : last ^ 1;
+                    if (todo.blocks() > 0) last = todo.two() ? 1 : todo.slot;
                 }
+                ok = __all_sync(0xFFFFFFFFu,
+                                mbar_wait(smem_addr(&ctl.todo_empty[i % kTodos]), (i / kTodos & 1) ^ 1, abort));
+                if (!ok) break;
+                if (lane == 0) {
+                    ctl.todo[i % kTodos] = todo;
+                    mbar_arrive(smem_addr(&ctl.todo_full[i % kTodos]));
+                }
+                load_q(true);  // the item's before
+                if (!more || !ok) break;
+                if (todo.blocks() > 0) q_item = todo.item, q_kvh = todo.kvh, q_slot = todo.slot;
+                load_q(false);
+                if constexpr (KV != kPacked) {
+                    const Walk& w = todo.walk;
+                    bool gone = false;
+                    auto check = [&](int from, int to) {  // pages that hold keys from .. to - 1
+                        to = min(to, todo.item.s.len);
+                        const int32_t* const pages = a.table + todo.item.seq * a.max_pages;
+                        for (int p = from / a.c.page_size + lane; p * (int64_t)a.c.page_size < to; p += 32)
+                            gone = gone || pages[p] < 0 || pages[p] >= a.c.n_pages;
+                    };
+                    if (w.from < w.sinks) check(w.from * kN, min(w.to, w.sinks) * kN);
+                    if (w.to > w.sinks) check(w.block(max(w.from, w.sinks)) * kN, w.block(w.to) * kN);
+                    gone = __any_sync(0xFFFFFFFFu, gone);
+                    if (lane == 0) {
+                        ctl.gone[i % kTodos] = gone;
+                        mbar_arrive(smem_addr(&ctl.todo_checked[i % kTodos]));
+                    }
+                }
+            }
+            if (*abort && lane == 0) {  // nothing may still be on its way when the CTA ends
+                int none = 0;
+                for (int t = 0; t < 2; ++t)
+                    if (tiles[t] > 0) mbar_wait(smem_addr(&ctl.q_full[t]), (tiles[t] - 1) & 1, &none);
+            }
+        } else if (warp == kLoadWarp) {
+            int loads = 0;               // of the ring so far; of an 8-bit cache, of the one ahead of it
+            bool ok = true;
+            const int boxes = kN / box;  // of a block; a power of two
+            for (int i = 0; ok; ++i) {
+                if (!(ok = __all_sync(0xFFFFFFFFu, todo_ready(i)))) break;
+                const Todo& todo = ctl.todo[i % kTodos];
+                const Walk w = todo.walk;
+                const int kvh = todo.kvh, slot = todo.slot;
+                const struct {
+                    Seq s;
+                    int seq;
+                } it = {todo.item.s, todo.item.seq};
+                __syncwarp();
+                if (lane == 0) todo_read(i);
+                if (slot < 0) break;
+                if (w.from == w.to) continue;
                 // box b of the walk's block x: the page (from n_pages on: zeros) and the row in it
                 auto look_up = [&](int x, int b, int& page, int& row) {
                     const int j = w.block(x) * kN + b * box;
@@ -597,67 +553,100 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                         }
                     }
                 };
+                constexpr int kPanel = S::kE4 ? S::kRawPanel : S::kPanel, kLine = S::kE4 ? 64 : 128;
                 auto copy = [&](uint32_t to, const CUtensorMap* m, uint32_t full, int page, int row) {
 #pragma unroll
                     for (int p = 0; p < DP / 64; ++p) {
                         if constexpr (KV == kPacked)
-                            tma_load_3d(to + p * S::kPanel, m, full, p * 64, kvh, row);
+                            tma_load_3d(to + p * kPanel, m, full, p * 64, kvh, row);
                         else
-                            tma_load_4d(to + p * S::kPanel, m, full, p * 64, row, kvh, page);
+                            tma_load_4d(to + p * kPanel, m, full, p * 64, row, kvh, page);
                     }
                 };
+                // An 8-bit cache's scales of rows 4 lane .. 4 lane + 3 of the walk's block x, a byte each; 0, which
+                // makes zeros of a row whatever its codes, behind the sequence's end and where there is no page.
+                uint32_t k_bytes = 0, v_bytes = 0;
+                auto ask = [&](int x) {
+                    k_bytes = v_bytes = 0;
+                    const int j = w.block(x) * kN + 4 * lane;
+                    int page = -1, row = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (x >= w.to || j + e >= it.s.len) break;
+                        if (e == 0 || ++row == a.c.page_size) {
+                            const int page_i = (j + e) / a.c.page_size;
+                            row = j + e - page_i * a.c.page_size;
+                            page = a.table[it.seq * a.max_pages + page_i];
+                        }
+                        if (page < 0 || page >= a.c.n_pages) continue;
+                        const int64_t at = ((int64_t)page * a.c.Hkv + kvh) * a.c.page_size + row;
+                        k_bytes |= (uint32_t)a.c.k_scale[at] << 8 * e;
+                        v_bytes |= (uint32_t)a.c.v_scale[at] << 8 * e;
+                    }
+                };
+                if constexpr (S::kE4) ask(w.from);
                 int page, row;
                 look_up(w.from, lane, page, row);
                 for (int x = w.from; ok && x < w.to; ++x) {
                     const int have0 = it.s.len - w.block(x) * kN;  // of the block's rows
                     for (int kv = 0; kv < 2; ++kv) {
-                        const int stage = loads % S::kStages;
-                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.kv_empty[stage]),
-                                                               (loads / S::kStages & 1) ^ 1, abort));
+                        constexpr int kRing = S::kE4 ? S::kRaws : S::kStages, kBytes = S::kE4 ? S::kRaw : S::kTile;
+                        const int stage = loads % kRing;
+                        ok = __all_sync(0xFFFFFFFFu,
+                                        mbar_wait(smem_addr(S::kE4 ? &ctl.raw_empty[stage] : &ctl.kv_empty[stage]),
+                                                  (loads / kRing & 1) ^ 1, abort));
                         if (!ok) break;
-                        const uint32_t full = smem_addr(&ctl.kv_full[stage]), to = kv_smem + stage * S::kTile;
-                        if (lane == 0) mbar_arrive_tx(full, S::kTile);
+                        const uint32_t full = smem_addr(S::kE4 ? &ctl.raw_full[stage] : &ctl.kv_full[stage]);
+                        const uint32_t to = S::kE4 ? smem_addr(smem) + S::kRawAt + stage * kBytes : kv_smem + stage * kBytes;
+                        if constexpr (S::kE4) {
+                            // (two blocks' are kept: the block before the last is done with when this load's place is)
+                            *reinterpret_cast<uint32_t*>(smem + S::kScaleAt + (loads & 3) * kN + 4 * lane) =
+                                kv == 0 ? k_bytes : v_bytes;
+                            if (kv == 1) ask(x + 1);
+                            __syncwarp();
+                        }
+                        if (lane == 0) mbar_arrive_tx(full, kBytes);
                         __syncwarp();
                         for (int b = lane; b < boxes; b += 32) {
                             if (b >= 32) look_up(x, b, page, row);
                             const int have = have0 - b * box;
-                            const uint32_t at = to + b * box * 128;
-                            if (kv == 0 || have >= box || (KV != kPacked && (have <= 0 || page == a.c.n_pages))) {
+                            const uint32_t at = to + b * box * kLine;
+                            // (widening makes zeros of what is behind the end)
+                            if (S::kE4 || kv == 0 || have >= box || (KV != kPacked && (have <= 0 || page == a.c.n_pages))) {
                                 copy(at, kv == 0 ? &maps.k : &maps.v, full, page, row);
                                 continue;
                             }
-                            // v where the sequence ends within the box: zeros from there on
-                            for (int r = 0; r < box;) {
-                                const int left = have - r;
-                                auto part = [&](const CUtensorMap* m, int rows) {
-                                    const bool zeros = left <= 0;
-                                    copy(at + r * 128, m, full, zeros ? (int)a.c.n_pages : page,
-                                         zeros && KV == kPacked ? (int)a.T : row + r);
-                                    r += rows;
-                                };
-                                if (r % 32 == 0 && box >= 32 && (left >= 32 || left <= 0))
-                                    part(&maps.v32, 32);
-                                else if (r % 8 == 0 && box >= 8 && (left >= 8 || left <= 0))
-                                    part(&maps.v8, 8);
-                                else
-                                    part(&maps.v1, 1);
+                            if constexpr (!S::kE4) {  // v where the sequence ends within the box: zeros from there on
+                                for (int r = 0; r < box;) {
+                                    const int left = have - r;
+                                    auto part = [&](const CUtensorMap* m, int rows) {
+                                        const bool zeros = left <= 0;
+                                        copy(at + r * 128, m, full, zeros ? (int)a.c.n_pages : page,
+                                             zeros && KV == kPacked ? (int)a.T : row + r);
+                                        r += rows;
+                                    };
+                                    if (r % 32 == 0 && box >= 32 && (left >= 32 || left <= 0))
+                                        part(&maps.v32, 32);
+                                    else if (r % 8 == 0 && box >= 8 && (left >= 8 || left <= 0))
+                                        part(&maps.v8, 8);
+                                    else
+                                        part(&maps.v1, 1);
+                                }
                             }
                         }
                         if (boxes > 32) look_up(x, lane, page, row);  // (the last one of these was looked up last)
                         ++loads;
-                        if (kv == 0 && x == w.from) load_q();
-                        if (!ok) break;
                     }
                     look_up(x + 1, lane, page, row);
                 }
             }
             __syncwarp();
-            if (*abort && lane == 0) {  // nothing may still be on its way when the CTA ends
+            if (*abort && lane == 0) {  // as above
                 int none = 0;
-                for (int t = 0; t < 2; ++t)
-                    if (tiles[t] > 0) mbar_wait(smem_addr(&ctl.q_full[t]), (tiles[t] - 1) & 1, &none);
-                for (int x = max(0, loads - S::kStages); x < loads; ++x)  // (0 of them over an 8-bit cache)
-                    mbar_wait(smem_addr(&ctl.kv_full[x % S::kStages]), x / S::kStages & 1, &none);
+                constexpr int kRing = S::kE4 ? S::kRaws : S::kStages;
+                for (int x = max(0, loads - kRing); x < loads; ++x)
+                    mbar_wait(smem_addr(S::kE4 ? &ctl.raw_full[x % kRing] : &ctl.kv_full[x % kRing]), x / kRing & 1,
+                              &none);
             }
         } else if (elect_one()) {
             const int t = warp - kMmaWarp;
@@ -668,31 +657,29 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
             const uint32_t o = tmem + 256 + t * 128, pw = tmem + 128 + t * 64;
             bool ok = true;
             int loads = 0;          // the ring's before this item: k of block j is load loads + 2 j
-            int done[2] = {0, 0};   // blocks of each tile before this item
-            int items = 0;          // items with a tile t and a block
-            int every = 0;          // items with a block
-            int last_t = -1;        // the tile that S was last written for in the item before
+            int done[2] = {0, 0};   // blocks of each slot before this item
+            int items = 0;          // items with blocks, of this slot
+            int every = 0;          // and of either
             for (int i = 0; ok; ++i) {
                 if (!(ok = todo_ready(i))) break;
-                const Item it = ctl.todo[i % kTodos].item;
+                const Todo& todo = ctl.todo[i % kTodos];
+                const int n = todo.blocks(), slot = todo.slot;
+                const bool two = todo.two(), mine = todo.has(t);
                 todo_read(i);
-                if (it.splits == 0) break;
-                const Walk w = walk(g, it, kN);
-                const int n = w.to - w.from;
+                if (slot < 0) break;
                 if (n == 0) continue;
-                const bool two = it.tiles == 2, mine = t == 0 || two;
                 auto loaded = [&](int x) {
                     ok = ok && mbar_wait(smem_addr(&ctl.kv_full[x % S::kStages]), x / S::kStages & 1, abort);
                 };
-                // S is free once the block before in the order (0, j), (1, j), (0, j + 1), ... has been read
+                // S is free for an item once the last block of the item before has been read.  Both threads wait for
+                // that at every item, so that neither passes over a phase (a wait by parity holds only where the phase
+                // before has completed); two barriers in turn, for a thread may be as far behind as the other's item.
+                if (every > 0)
+                    ok = mbar_wait(smem_addr(&ctl.s_last[(every - 1) & 1]), (every - 1) / 2 & 1, abort);
+                // and within it once the block before in the order (0, j), (1, j), (0, j + 1), ... has been
                 auto s_free = [&](int j) {
-                    const int pt = t == 1 ? 0 : j > 0 ? (two ? 1 : 0) : last_t, pj = t == 1 ? j : j - 1;
-                    // A wait by parity holds only where the phase before has completed.  The second tile's thread has
-                    // passed over the blocks of items before that have no second tile: S of this item's first block,
-                    // once it is there, says that those have been read.
-                    if (t == 1 && j == 0 && last_t == 0)
-                        ok = ok && mbar_wait(smem_addr(&ctl.s_full[0]), done[0] & 1, abort);
-                    if (pt >= 0) ok = ok && mbar_wait(smem_addr(&ctl.s_free[pt]), (done[pt] + pj) & 1, abort);
+                    const int pt = !two ? t : t ^ 1, pj = two && t == 1 ? j : j - 1;
+                    if (pj >= 0) ok = ok && mbar_wait(smem_addr(&ctl.s_free[pt]), (done[pt] + pj) & 1, abort);
                 };
                 auto scores = [&](int j) {
                     loaded(loads + 2 * j);
@@ -708,15 +695,12 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                     }
                     mma_commit(smem_addr(&ctl.s_full[t]));
                     mma_commit(smem_addr(&ctl.kv_empty[stage]));
-                    if (j + 1 == n) mma_commit(smem_addr(&ctl.q_empty));
+                    if (j + 1 == n) mma_commit(smem_addr(&ctl.q_empty[t]));
                 };
-                // (an item has a first tile always, a second one not)
-                ok = mine ? mbar_wait(smem_addr(&ctl.q_full[t]), items & 1, abort)
-                          : mbar_wait(smem_addr(&ctl.q_full[0]), every & 1, abort);
-                if (mine)
+                if (mine) {
+                    ok = ok && mbar_wait(smem_addr(&ctl.q_full[t]), items & 1, abort);
                     scores(0);
-                else if (ok)
-                    mbar_arrive(smem_addr(&ctl.q_empty));
+                }
                 for (int j = 0; ok && mine && j < n; ++j) {
                     if (j + 1 < n) scores(j + 1);
                     loaded(loads + 2 * j + 1);
@@ -733,17 +717,16 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                     mma_commit(smem_addr(&ctl.o_done[t]));
                     mma_commit(smem_addr(&ctl.kv_empty[stage]));
                 }
-                // blocks that only the other tile works on
+                // blocks that only the other slot works on
                 for (int x = 0; ok && !mine && x < 2 * n; ++x) {
                     loaded(loads + x);
                     if (ok) mbar_arrive(smem_addr(&ctl.kv_empty[(loads + x) % S::kStages]));
                 }
                 loads += 2 * n;
-                done[0] += n;
-                if (two) done[1] += n;
+                if (two || slot == 0) done[0] += n;
+                if (two || slot == 1) done[1] += n;
                 items += mine;
                 ++every;
-                last_t = two ? 1 : 0;
             }
             // every product is done before tensor memory is given back
             mma_commit(smem_addr(&ctl.drained[t]));
@@ -759,34 +742,68 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
         const float c = fmaxf(fabsf(a.scale) * kLog2e, __uint_as_float(1u));
         uint8_t* const stage = smem + S::kTile * (2 + S::kStages) + warp * (S::kOut / 8);
         bool ok = true;
-        int done = 0;  // blocks of this tile before this item
+        int done = 0;   // blocks of this slot before this item
+        int every = 0;  // items with blocks, of either
         for (int i = 0; ok; ++i) {
             ok = __all_sync(0xFFFFFFFFu, todo_ready(i));
             if (!ok) break;
-            const Item it = ctl.todo[i % kTodos].item;
-            const int kvh = ctl.todo[i % kTodos].kvh;
-            __syncwarp();
-            if (lane == 0) todo_read(i);
-            if (it.splits == 0) break;
-            if (t >= it.tiles) continue;
-            const Walk w = walk(g, it, kN);
-            const int u = it.tile + t;
-            const Row mine = row_of(g, it, u, threadIdx.x & 127);
-            const int place = it.s.len - it.s.n + mine.token;
-            // the places of the warp's rows: from .. to
-            const int place_from = __shfl_sync(0xFFFFFFFFu, place, 0), place_to = __shfl_sync(0xFFFFFFFFu, place, 31);
+            // (what an item is stays where it is until its rows are written: registers are for S)
+            const Todo& todo = ctl.todo[i % kTodos];
+            const int n = todo.blocks();
+            const bool end = todo.slot < 0;
+            if (end || !todo.has(t)) {
+                __syncwarp();
+                if (lane == 0) todo_read(i);
+                if (end) break;
+                every += n > 0;
+                continue;
+            }
+            bool gone = false;  // whether pages of the walk are not in the cache
+            if constexpr (KV != kPacked) {
+                ok = __all_sync(0xFFFFFFFFu,
+                                mbar_wait(smem_addr(&ctl.todo_checked[i % kTodos]), i / kTodos & 1, abort));
+                if (!ok) break;
+                gone = ctl.gone[i % kTodos];
+            }
+            // S has been read; for the item's last time?
+            auto s_read = [&](int j) {
+                if (lane != 0) return;
+                mbar_arrive(smem_addr(&ctl.s_free[t]));
+                if (j == n - 1 && (t == 1 || !todo.two())) mbar_arrive(smem_addr(&ctl.s_last[every & 1]));
+            };
+            int place;
+            bool idle;
+            {
+                const Row mine = row_of(g, todo.item, todo.tile(t), threadIdx.x & 127);
+                place = todo.item.s.len - todo.item.s.n + mine.token;
+                // a warp without a row that is there leaves its weights as they are: its rows of O are not looked at
+                idle = !__any_sync(0xFFFFFFFFu, mine.there);
+            }
+            // every row of the warp sees the keys of a block that are before `sure`, and under a window behind `low`
+            const int sure = __shfl_sync(0xFFFFFFFFu, place, 0) + 1;
+            const int low = g.window > 0 ? __shfl_sync(0xFFFFFFFFu, place, 31) - g.window : -1;
             float m = -INFINITY, l = 0.0f;
-            for (int x = w.from; x < w.to; ++x) {
-                const int j = x - w.from, k0 = w.block(x) * kN;
-                // pages of the block that are not in the cache
-                bool gone = false;
-                if constexpr (KV != kPacked) {
-                    const int first = k0 / a.c.page_size, last = min(k0 + kN, it.s.len) - 1;
-                    for (int p = first + lane; p * (int64_t)a.c.page_size <= last; p += 32) {
-                        const int32_t page = a.table[it.seq * a.max_pages + p];
-                        gone = gone || page < 0 || page >= a.c.n_pages;
+            for (int j = 0; idle && j < n; ++j) {
+                ok = mbar_wait(smem_addr(&ctl.s_full[t]), (done + j) & 1, abort);
+                s_read(j);
+                // (no sooner than the others: it would be counted for the weights before)
+                if (j > 0) ok = ok && mbar_wait(smem_addr(&ctl.o_done[t]), (done + j - 1) & 1, abort);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[t]));
+            }
+            for (int j = 0; !idle && j < n; ++j) {
+                const int k0 = todo.walk.block(todo.walk.from + j) * kN;
+                const bool whole = !gone && k0 + kN <= sure && (k0 > low || k0 + kN <= g.sinks);
+                if (KV != kPacked && gone) {  // (left where rows are written from: registers are for S)
+#pragma unroll 1
+                    for (int y = 0; y < 4; ++y) {
+                        const int key = k0 + 32 * y + lane;
+                        const bool here = key < todo.item.s.len && key_at<KV>(a, todo.item, todo.kvh, key) >= 0;
+                        const uint32_t word = __ballot_sync(0xFFFFFFFFu, here);
+                        if (lane == 0) reinterpret_cast<uint32_t*>(stage)[y] = word;
                     }
-                    gone = __any_sync(0xFFFFFFFFu, gone);
+                    __syncwarp();
                 }
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.s_full[t]), (done + j) & 1, abort));
                 if (!ok) break;
@@ -798,18 +815,12 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                 for (int y = 0; y < 4; ++y) tmem_wait_ld32(s + y * 32);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&ctl.s_free[t]));
-                // whether a row of the warp does not see a key of the block
-                if (gone || k0 + kN - 1 > place_from ||
-                    (a.window > 0 && k0 <= place_to - a.window && k0 + kN > a.sinks)) {
+                s_read(j);
+                if (!whole) {
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        uint32_t seen = seen_word(a, place, k0, y);
-                        if (KV != kPacked && gone) {
-                            const int key = k0 + 32 * y + lane;
-                            const bool here = key < it.s.len && key_at<KV>(a, it, kvh, key) >= 0;
-                            seen &= __ballot_sync(0xFFFFFFFFu, here);
-                        }
+                        uint32_t seen = seen_word(g, place, k0, y);
+                        if (KV != kPacked && gone) seen &= reinterpret_cast<const uint32_t*>(stage)[y];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) s[32 * y + e] = seen >> e & 1u ? s[32 * y + e] : 0xFF800000u;
                     }
@@ -870,7 +881,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[t]));
             }
-            const int n = w.to - w.from;
+            every += n > 0;
             done += n;
             if (n > 0) ok = ok && mbar_wait(smem_addr(&ctl.o_done[t]), (done - 1) & 1, abort);
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -878,11 +889,15 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
             tc_fence_after();
             // nothing but NaN: a finite maximum, so that it reaches the join
             if (m == -INFINITY && l != l) m = -3.0e38f;
-            const bool split = it.splits > 1;
+            const Item it = todo.item;
+            const int kvh = todo.kvh;
+            const Row mine = row_of(g, it, todo.tile(t), threadIdx.x & 127);
+            const bool is_part = it.splits > 1;
             // where the row lies, of the partial results or of out; -1: there is none
             const int head = kvh * g.group + mine.head;
+            const int64_t part = mine.there && is_part ? part_at(g, it, mine.token, head) : -1;
             const int64_t row = !mine.there ? -1
-                                : split     ? part_at(g, it, mine.token, head) * a.D
+                                : is_part   ? part * a.D
                                             : (it.s.begin + (int64_t)mine.token) * a.out_stride + (int64_t)head * a.D;
             float2 bad = make_float2(0.0f, 0.0f);
             // Some bytes of the warp's rows at a time by way of shared memory, so that
@@ -903,49 +918,48 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                     if (at >= 0 && d < a.D) *reinterpret_cast<Vec16*>(base + (at + d) * es) = v;
                 }
             };
-            constexpr int kCols = S::kOutRow >= 64 ? S::kOutRow / 2 : 32;  // of O at a time
-            if (split && mine.there) g.part_ml[row / a.D] = make_float2(m == -INFINITY || m == -3.0e38f ? m : m * c, l);
+            if (part >= 0) g.part_ml[part] = make_float2(m == -INFINITY || m == -3.0e38f ? m : m * c, l);
             const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
-#pragma unroll
-            for (int x = 0; x < DP / kCols; ++x) {
-                uint32_t o[kCols] = {};
+            // (rolled: code that runs once an item is fetched again each time)
+#pragma unroll 1
+            for (int x = 0; x < DP; x += 32) {
+                uint32_t o[32] = {};
                 if (n > 0) {
-#pragma unroll
-                    for (int y = 0; y < kCols / 32; ++y) tmem_ld32(to + x * kCols + y * 32, o + y * 32);
-#pragma unroll
-                    for (int y = 0; y < kCols / 32; ++y) tmem_wait_ld32(o + y * 32);
-                    if (x == DP / kCols - 1) {  // the next item may have O
+                    tmem_ld32(to + x, o);
+                    tmem_wait_ld32(o);
+                    if (x == DP - 32) {  // the next item may have O
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_addr(&ctl.o_free[t]));
                     }
                 }
-                if (split) {
+                const float by = is_part ? 1.0f : inv;
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 f = mul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
+                                             make_float2(by, by));
+                    bad = fma2_rn(f, make_float2(0.0f, 0.0f), bad);  // 0, or NaN
+                    o[e] = __float_as_uint(f.x), o[e + 1] = __float_as_uint(f.y);
+                }
+                if (is_part) {
                     constexpr int kEntries = S::kOutRow / 4;
 #pragma unroll
-                    for (int e = 0; e < kCols; e += 2)
-                        bad = fma2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
-                                      make_float2(0.0f, 0.0f), bad);  // 0, or NaN
-#pragma unroll
-                    for (int y = 0; y < kCols / kEntries; ++y)
-                        write(reinterpret_cast<char*>(g.part_o), 4, x * kCols + y * kEntries, [&](int e) {
-                            const uint32_t* const z = o + y * kEntries + 4 * e;
+                    for (int y = 0; y < 32; y += kEntries)
+                        write(reinterpret_cast<char*>(g.part_o), 4, x + y, [&](int e) {
+                            const uint32_t* const z = o + y + 4 * e;
                             return Vec16{{z[0], z[1], z[2], z[3]}};
                         });
                 } else {
                     constexpr int kEntries = S::kOutRow / 2;
 #pragma unroll
-                    for (int e = 0; e < kCols; e += 2) {
-                        const float2 f = mul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
-                                                 make_float2(inv, inv));
-                        bad = fma2_rn(f, make_float2(0.0f, 0.0f), bad);
-                        o[e / 2] = f32x2_to_bf16x2_bits(f.x, f.y);
-                    }
+                    for (int y = 0; y < 32; y += kEntries)
+                        write(static_cast<char*>(a.out), 2, x + y, [&](int e) {
+                            Vec16 v;
 #pragma unroll
-                    for (int y = 0; y < kCols / kEntries; ++y)
-                        write(static_cast<char*>(a.out), 2, x * kCols + y * kEntries, [&](int e) {
-                            const uint32_t* const z = o + y * kEntries / 2 + 4 * e;
-                            return Vec16{{z[0], z[1], z[2], z[3]}};
+                            for (int z = 0; z < 4; ++z)
+                                v.w[z] = f32x2_to_bf16x2_bits(__uint_as_float(o[y + 8 * e + 2 * z]),
+                                                              __uint_as_float(o[y + 8 * e + 2 * z + 1]));
+                            return v;
                         });
                 }
             }
@@ -957,6 +971,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                 repair_row<KV>(g, it, kvh, __shfl_sync(0xFFFFFFFFu, mine.token, r),
                                __shfl_sync(0xFFFFFFFFu, mine.head, r));
             }
+            if (lane == 0) todo_read(i);
         }
     }
     tc_fence_before();
@@ -975,41 +990,39 @@ bool encode_kv(CUtensorMap* m, const ChunkArgs& a, bool second, cuuint32_t rows)
         return encode_bf16(m, second ? a.v : a.k, 3, dims, strides, box);
     }
     const KvCacheArgs& c = a.c;
-    const cuuint64_t page = (cuuint64_t)c.page_size * c.D * 2;
+    const cuuint64_t es = c.dtype == GBE_KV_E4M3 ? 1 : 2, page = (cuuint64_t)c.page_size * c.D * es;
     const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.page_size, (cuuint64_t)c.Hkv, (cuuint64_t)c.n_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)c.D * 2, page,
-                                   c.n_pages > 1 ? (cuuint64_t)c.page_stride * 2 : page * c.Hkv};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.D * es, page,
+                                   c.n_pages > 1 ? (cuuint64_t)c.page_stride * es : page * c.Hkv};
     const cuuint32_t box[4] = {64, rows, 1, 1};
+    if (es == 1) return encode_bytes(m, second ? c.v : c.k, 4, dims, strides, box);
     return encode_bf16(m, second ? c.v : c.k, 4, dims, strides, box);
 }
 
 template <int KV, int DP>
 cudaError_t go(const ChunkArgs& a, cudaStream_t st) {
     using S = Shape<KV, DP>;
-    const Args g = make_args(a, kM, 2);
+    const Args g = make_args(a, kM, 2, kN);
     cuuint32_t box = kN;  // keys of a copy: the largest power of two that divides a page, and at most a block
-    if (KV == GBE_KV_BF16)
+    if (KV != kPacked)
         while (a.c.page_size % box) box /= 2;
     Maps maps;
     const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
     const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.q_stride * 2};
     const cuuint32_t q_box[3] = {64, (cuuint32_t)g.heads, (cuuint32_t)g.tokens};
     if (!encode_bf16(&maps.q, a.q, 3, dims, strides, q_box)) return cudaErrorNotSupported;
-    if constexpr (S::kE4) {
-        maps.k = maps.v = maps.v32 = maps.v8 = maps.v1 = maps.q;  // (not used)
-    } else if (!encode_kv(&maps.k, a, false, box) || !encode_kv(&maps.v, a, true, box) ||
-               !encode_kv(&maps.v32, a, true, box < 32 ? box : 32) || !encode_kv(&maps.v8, a, true, box < 8 ? box : 8) ||
-               !encode_kv(&maps.v1, a, true, 1)) {
+    if (!encode_kv(&maps.k, a, false, box) || !encode_kv(&maps.v, a, true, box) ||
+        !encode_kv(&maps.v32, a, true, box < 32 ? box : 32) || !encode_kv(&maps.v8, a, true, box < 8 ? box : 8) ||
+        !encode_kv(&maps.v1, a, true, 1))
         return cudaErrorNotSupported;
-    }
     constexpr int smem = S::kBytes;
     static_assert(smem <= 227 * 1024);
     static FunctionLimit limit;
     const cudaError_t e = limit.raise(reinterpret_cast<const void*>(chunk_tc<KV, DP>), smem);
     if (e != cudaSuccess) return e;
     const int64_t seqs = a.n_seqs < a.T ? a.n_seqs : a.T, sms = sm_count();
-    const int64_t items = (a.T / g.tokens + seqs) * g.parts * g.most * a.Hkv;
-    const cudaError_t f = launch(chunk_tc<KV, DP>, dim3((unsigned)(items < sms ? items : sms)), dim3(S::kThreads), smem,
+    const int64_t pieces = (a.T / g.tokens + seqs) * g.parts * a.Hkv * g.most;
+    const cudaError_t f = launch(chunk_tc<KV, DP>, dim3((unsigned)(pieces < sms ? pieces : sms)), dim3(S::kThreads), smem,
                                  st, maps, g, (int)box);
     return f != cudaSuccess ? f : launch_join(g, kBF16, st);
 }

@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // [T, H, D] bf16 with a token stride, copied in boxes of `rows` tokens of one
 // head and 64 entries (128 bytes, swizzled by the place in shared memory, so
 // that a box may begin at any row of a tile); zeros outside.
-bool encode(CUtensorMap* m, const void* p, int64_t T, int64_t H, int64_t D, int64_t stride, cuuint32_t rows) {
+bool encode_rows(CUtensorMap* m, const void* p, int64_t T, int64_t H, int64_t D, int64_t stride, cuuint32_t rows) {
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
     const cuuint32_t box[3] = {64, 1, rows};
@@ -655,9 +655,9 @@ bool encode(CUtensorMap* m, const void* p, int64_t T, int64_t H, int64_t D, int6
 template <int DP>
 cudaError_t go(const PromptArgs& a, cudaStream_t st) {
     CUtensorMap mq, mk, mv, mv32, mv8, mv1;
-    if (!encode(&mq, a.q, a.T, a.Hq, a.D, a.q_stride, kM) || !encode(&mk, a.k, a.T, a.Hkv, a.D, a.k_stride, kN) ||
-        !encode(&mv, a.v, a.T, a.Hkv, a.D, a.v_stride, kN) || !encode(&mv32, a.v, a.T, a.Hkv, a.D, a.v_stride, 32) ||
-        !encode(&mv8, a.v, a.T, a.Hkv, a.D, a.v_stride, 8) || !encode(&mv1, a.v, a.T, a.Hkv, a.D, a.v_stride, 1))
+    if (!encode_rows(&mq, a.q, a.T, a.Hq, a.D, a.q_stride, kM) || !encode_rows(&mk, a.k, a.T, a.Hkv, a.D, a.k_stride, kN) ||
+        !encode_rows(&mv, a.v, a.T, a.Hkv, a.D, a.v_stride, kN) || !encode_rows(&mv32, a.v, a.T, a.Hkv, a.D, a.v_stride, 32) ||
+        !encode_rows(&mv8, a.v, a.T, a.Hkv, a.D, a.v_stride, 8) || !encode_rows(&mv1, a.v, a.T, a.Hkv, a.D, a.v_stride, 1))
         return cudaErrorNotSupported;
     constexpr int smem = Shape<DP>::kBytes;
     static FunctionLimit limit;

@@ -104,7 +104,7 @@ def test_chunk_workspace_sizes(L):
     one = W(1, 1, 32, 8, 128, 64, 2048, 0, 0)
     assert one > 0 and W(1, 2, 32, 8, 128, 64, 2048, 0, 0) == 2 * one
     # never more than a few rounds of CTAs of 256 rows leave for a sequence, however long its chunk
-    assert W(1, 1 << 20, 32, 8, 128, 64, 1 << 14, 0, 0) <= 4 * 152 * 256 * 130 * 4
+    assert W(1, 1 << 20, 32, 8, 128, 64, 1 << 14, 0, 0) <= 8 * 152 * 256 * 130 * 4
     for bad in ((-1, 1, 32, 8, 128, 64, 10, 0, 0), (1, -1, 32, 8, 128, 64, 10, 0, 0), (1, 1, 33, 8, 128, 64, 10, 0, 0),
                 (1, 1, 32, 8, 100, 64, 10, 0, 0), (1, 1, 32, 8, 128, 0, 10, 0, 0), (1, 1, 32, 8, 128, 64, 1 << 25, 0, 0),
                 (1, 1, 32, 8, 128, 64, 10, -1, 0), (1, 1, 32, 8, 128, 64, 10, 1, -1)):
