@@ -6,12 +6,16 @@
 //
 // over the keys that row i sees (attn_chunk.cuh).  On the CUDA cores, f32
 // throughout.  A CTA goes from item to item: 32 rows -- tokens and the query
-// heads of a kv head -- and their keys, or a part of these, in tiles of 64 with the running maximum and sum of the softmax (base 2: scale * log2(e) is folded
-// into q).  Eight by sixteen threads, a thread holding 4 x 4 logits and 4 x D/16
-// of the output, two multiply-adds an instruction; up to D = 128 two groups of
-// threads take every other tile and join their sums.  f32 rows come by
-// asynchronous copies, v while the logits are formed and the next k while the
-// output is; where a row lies is looked up a tile ahead.
+// heads of a kv head -- and their keys, or a part of these, in tiles of 64 with the
+// running maximum and sum of the softmax (base 2: scale * log2(e) is folded into q).
+// Eight by sixteen threads, a thread holding 4 x 4 logits and 4 x D/16 of the
+// output, two multiply-adds an instruction; up to D = 128 two groups of threads
+// take every other tile and join their sums.  f32 rows come by asynchronous
+// copies, v while the logits are formed and the next k while the output is; where
+// a row lies is looked up a tile ahead.  The multiply-adds and their operands'
+// loads from shared memory bound it: five sequences of up to 100 rows behind up to
+// 900, 14 heads over 2 of D 64, window 500: 51 us; three prompts of up to 1000, 8
+// heads of D 64, window 129: 51 us.
 #include <new>
 #include <type_traits>
 
@@ -25,7 +29,6 @@ namespace {
 
 constexpr int kThreads = 128;  // of a group
 constexpr int kN = 64, kM = 32, R = kM / 8;
-constexpr int kPacked = -1;    // KV of rows that are not in a cache
 
 template <int DP>
 constexpr int kGroups = DP <= 128 ? 2 : 1;
@@ -405,58 +408,103 @@ __global__ void __launch_bounds__(kThreads* kGroups<DP>, 1) chunk_rows(const __g
     }
 }
 
-// A warp a row, its partial results in order, four entries a lane; 0 where nothing
-// was seen (a weight of 0 still carries NaN on).
-constexpr int kJoinWarps = 8;
-template <int DT>
+// A warp two rows at a time, their partial results in order, four of each on
+// their way, four entries a lane: a row has few of them, so that the latency of one
+// behind the other is what it would cost.  0 where nothing was seen; a weight of 0
+// still carries NaN on.
+constexpr int kJoinWarps = 8, kJoinRows = 2, kJoinDepth = 4;
+template <int DT, int DP>
 __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join(const __grid_constant__ Args g) {
+    constexpr int kPieces = DP / 128;  // of four entries, of a lane
     pdl_begin();
     const ChunkArgs& a = g.a;
     const int lane = threadIdx.x & 31, D = (int)a.D;
+    constexpr int kFour = DT == kF32 ? 16 : 8;  // bytes; where rows lie on their grid
+    const bool fours = reinterpret_cast<uintptr_t>(a.out) % kFour == 0 && a.out_stride % 4 == 0;
     for (int64_t b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
         Item it = {};
         it.s = sequence(a, b);
         it.seq = (int)b;
         it.splits = cut_of(g, it.s).splits;
         if (it.splits == 1) continue;
-        const int Hq = (int)a.Hq, rows = it.s.n * Hq;  // (of fewer than kWave kRounds units)
-        for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < rows; r += gridDim.y * kJoinWarps) {
-            const int token = r / Hq, head = r - token * Hq;
-            const int n = it.splits;
-            const int64_t at = parts_at(g, it, token, head);
-            const float2* const ml = g.part_ml + at;
-            float mx = -INFINITY;
-            for (int s = lane; s < n; s += 32) mx = fmaxf(mx, ml[s].x);
+        const int Hq = (int)a.Hq, rows = it.s.n * Hq, n = it.splits;  // (of fewer than kWave kRounds units)
+        const int step = gridDim.y * kJoinWarps;
+        for (int r0 = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r0 < rows; r0 += kJoinRows * step) {
+            int64_t at[kJoinRows];
+            float m[kJoinRows], l[kJoinRows];
+            float4 o[kJoinRows][kPieces] = {};
 #pragma unroll
-            for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
-            float l = 0.0f;
-            float4 o[2] = {};
-            const float* const from = g.part_o + at * D + lane * 4;
-#pragma unroll 4
-            for (int s = 0; s < n; ++s) {
-                const float2 v = ml[s];
-                const bool any = v.x != -INFINITY;
-                const float w = any ? ex2(v.x - mx) : 0.0f;
-                if (any) l = fmaf(v.y, w, l);
+            for (int i = 0; i < kJoinRows; ++i) {
+                const int r = min(r0 + i * step, rows - 1), token = r / Hq;
+                at[i] = parts_at(g, it, token, r - token * Hq);
+                m[i] = -INFINITY, l[i] = 0.0f;
+            }
+            for (int s0 = 0; s0 < n; s0 += kJoinDepth) {
+                float2 ml[kJoinRows][kJoinDepth];
+                float4 y[kJoinRows][kJoinDepth][kPieces];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (lane * 4 + x * 128 >= D) continue;
-                    const float4 y = *reinterpret_cast<const float4*>(from + (int64_t)s * D + x * 128);
-                    if (!any) continue;
-                    o[x].x = fmaf(y.x, w, o[x].x);
-                    o[x].y = fmaf(y.y, w, o[x].y);
-                    o[x].z = fmaf(y.z, w, o[x].z);
-                    o[x].w = fmaf(y.w, w, o[x].w);
+                for (int i = 0; i < kJoinRows; ++i)
+#pragma unroll
+                    for (int s = 0; s < kJoinDepth; ++s) {
+                        const bool there = s0 + s < n;
+                        ml[i][s] = there ? g.part_ml[at[i] + s0 + s] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+                        for (int x = 0; x < kPieces; ++x) {
+                            const int d = lane * 4 + x * 128;
+                            y[i][s][x] = there && d < D
+                                             ? *reinterpret_cast<const float4*>(g.part_o + (at[i] + s0 + s) * D + d)
+                                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        }
+                    }
+#pragma unroll
+                for (int i = 0; i < kJoinRows; ++i) {
+                    float top = m[i];
+#pragma unroll
+                    for (int s = 0; s < kJoinDepth; ++s) top = fmaxf(top, ml[i][s].x);
+                    const float back = m[i] == -INFINITY ? 0.0f : ex2(m[i] - top);
+                    m[i] = top;
+                    l[i] *= back;
+#pragma unroll
+                    for (int x = 0; x < kPieces; ++x)
+                        o[i][x].x *= back, o[i][x].y *= back, o[i][x].z *= back, o[i][x].w *= back;
+#pragma unroll
+                    for (int s = 0; s < kJoinDepth; ++s) {
+                        if (ml[i][s].x == -INFINITY) continue;
+                        const float w = ex2(ml[i][s].x - top);
+                        l[i] = fmaf(ml[i][s].y, w, l[i]);
+#pragma unroll
+                        for (int x = 0; x < kPieces; ++x) {
+                            const float4 z = y[i][s][x];
+                            o[i][x].x = fmaf(z.x, w, o[i][x].x);
+                            o[i][x].y = fmaf(z.y, w, o[i][x].y);
+                            o[i][x].z = fmaf(z.z, w, o[i][x].z);
+                            o[i][x].w = fmaf(z.w, w, o[i][x].w);
+                        }
+                    }
                 }
             }
-            const int64_t out = (it.s.begin + (int64_t)token) * a.out_stride + (int64_t)head * D + lane * 4;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (lane * 4 + x * 128 >= D) continue;
-                const float y[4] = {o[x].x, o[x].y, o[x].z, o[x].w};
+            for (int i = 0; i < kJoinRows; ++i) {
+                const int r = r0 + i * step, token = r / Hq;
+                if (r >= rows) continue;
+                const int64_t out = (it.s.begin + (int64_t)token) * a.out_stride + (int64_t)(r - token * Hq) * D + lane * 4;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    Store<DT>::store1(a.out, out + x * 128 + e, mx == -INFINITY ? 0.0f : y[e] / l);
+                for (int x = 0; x < kPieces; ++x) {
+                    if (lane * 4 + x * 128 >= D) continue;
+                    float z[4] = {o[i][x].x, o[i][x].y, o[i][x].z, o[i][x].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[e] = m[i] == -INFINITY ? 0.0f : z[e] / l[i];
+                    const int64_t to = out + x * 128;
+                    if (!fours) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) Store<DT>::store1(a.out, to + e, z[e]);
+                    } else if constexpr (DT == kF32) {
+                        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = make_float4(z[0], z[1], z[2], z[3]);
+                    } else {
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
+                            make_uint2(f32x2_to_bf16x2_bits(z[0], z[1]), f32x2_to_bf16x2_bits(z[2], z[3]));
+                    }
+                }
             }
         }
     }
@@ -472,9 +520,8 @@ cudaError_t go(const ChunkArgs& a, cudaStream_t st) {
     const int64_t seqs = a.n_seqs < a.T ? a.n_seqs : a.T;
     const int64_t pieces = (a.T / g.tokens + seqs) * g.parts * a.Hkv * g.most;
     const int64_t most = 2 * (int64_t)sm_count();
-    const cudaError_t f = launch(chunk_rows<DT, KV, DP, VEC>, dim3((unsigned)(pieces < most ? pieces : most)),
-                                 dim3(kThreads * kGroups<DP>), smem, st, g);
-    return f != cudaSuccess ? f : launch_join(g, DT, st);
+    return launch(chunk_rows<DT, KV, DP, VEC>, dim3((unsigned)(pieces < most ? pieces : most)),
+                  dim3(kThreads * kGroups<DP>), smem, st, g);
 }
 
 template <int DT, int KV, bool VEC>
@@ -486,13 +533,18 @@ cudaError_t pick(const ChunkArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+template <int DT>
+static cudaError_t join(const Args& g, cudaStream_t st) {
+    const int64_t ctas = 6 * (int64_t)sm_count(), x = g.a.n_seqs < ctas ? g.a.n_seqs : ctas;
+    const int64_t rows = (g.a.T * g.a.Hq + kJoinWarps - 1) / kJoinWarps, share = (ctas + x - 1) / x;
+    const dim3 grid((unsigned)x, (unsigned)(rows < share ? rows : share)), threads(kJoinWarps * 32);
+    return g.a.D <= 128 ? launch(chunk_join<DT, 128>, grid, threads, 0, st, g)
+                        : launch(chunk_join<DT, 256>, grid, threads, 0, st, g);
+}
+
 cudaError_t launch_join(const Args& g, int dtype, cudaStream_t st) {
     if (g.most == 1) return cudaSuccess;
-    const int64_t ctas = 8 * (int64_t)sm_count(), x = g.a.n_seqs < ctas ? g.a.n_seqs : ctas;
-    const int64_t rows = (g.a.T * g.a.Hq + kJoinWarps - 1) / kJoinWarps, share = ctas / x;
-    const dim3 grid((unsigned)x, (unsigned)(rows < share ? rows : share));
-    return dtype == GBE_F32 ? launch(chunk_join<kF32>, grid, dim3(kJoinWarps * 32), 0, st, g)
-                            : launch(chunk_join<kBF16>, grid, dim3(kJoinWarps * 32), 0, st, g);
+    return dtype == GBE_F32 ? join<kF32>(g, st) : join<kBF16>(g, st);
 }
 
 }  // namespace chunk
@@ -515,17 +567,21 @@ ChunkRoom chunk_room(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t
 
 cudaError_t launch_attn_chunk(const ChunkArgs& a, int dtype, bool vec, bool tensor, cudaStream_t st) {
     using namespace chunk;
-    if (tensor && vec && dtype == GBE_BF16 && a.D <= 128 &&
-        (a.table == nullptr || (a.c.n_pages > 0 && (a.c.dtype == GBE_KV_BF16 ||
-                                                    (a.D % 16 == 0 && a.c.page_stride % 16 == 0)))))
-        return launch_tc(a, st);
-    if (a.table == nullptr) {
-        if (dtype == GBE_F32) return vec ? pick<kF32, kPacked, true>(a, st) : pick<kF32, kPacked, false>(a, st);
-        return vec ? pick<kBF16, kPacked, true>(a, st) : pick<kBF16, kPacked, false>(a, st);
-    }
-    if (dtype == GBE_F32)
-        return a.c.dtype == GBE_KV_E4M3 ? pick<kF32, GBE_KV_E4M3, true>(a, st) : pick<kF32, GBE_KV_F32, true>(a, st);
-    return a.c.dtype == GBE_KV_E4M3 ? pick<kBF16, GBE_KV_E4M3, true>(a, st) : pick<kBF16, GBE_KV_BF16, true>(a, st);
+    const bool paged = a.table != nullptr, e4m3 = paged && a.c.dtype == GBE_KV_E4M3, bf16 = dtype == GBE_BF16;
+    const bool tc = bf16 && vec && tensor && a.D <= 128 &&
+                    (!paged || (a.c.n_pages > 0 && (!e4m3 || (a.D % 16 == 0 && a.c.page_stride % 16 == 0))));
+    cudaError_t e = cudaSuccess;
+    if (tc)
+        e = launch_tc(a, st);
+    else if (!paged && bf16)
+        e = vec ? pick<kBF16, kPacked, true>(a, st) : pick<kBF16, kPacked, false>(a, st);
+    else if (!paged)
+        e = vec ? pick<kF32, kPacked, true>(a, st) : pick<kF32, kPacked, false>(a, st);
+    else if (bf16)
+        e = e4m3 ? pick<kBF16, GBE_KV_E4M3, true>(a, st) : pick<kBF16, GBE_KV_BF16, true>(a, st);
+    else
+        e = e4m3 ? pick<kF32, GBE_KV_E4M3, true>(a, st) : pick<kF32, GBE_KV_F32, true>(a, st);
+    return e != cudaSuccess ? e : launch_join(tc ? make_args(a, 128, 2, 128) : make_args(a, kM, 1, kN), dtype, st);
 }
 
 }  // namespace gbe

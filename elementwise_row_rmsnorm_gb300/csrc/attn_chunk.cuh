@@ -31,6 +31,7 @@ constexpr int kRounds = 8;       // once at least, and at most as often
 constexpr int kLeast = 1024;     // keys of a split at least
 constexpr int kEnds = 4;         // what an item's first copies, last rows and join cost, in blocks of 128 keys
 constexpr int kUnitRows = 256;   // at most
+constexpr int kPacked = -1;      // the type of keys that are not in a cache
 
 struct Args {
     ChunkArgs a;
@@ -94,7 +95,7 @@ static __device__ __noinline__ Cut cut_of(const Args& g, const Seq& s) {
     c.units = ((s.n + g.tokens - 1) / g.tokens * g.parts + g.tiles - 1) / g.tiles;
     if (g.most == 1 || c.units >= kWave * kRounds) return c;
     int64_t keys = s.len;
-    if (a.window > 0) keys = min(keys, a.window + a.sinks + g.tiles * g.tokens);
+    if (a.window > 0) keys = min(keys, a.window + a.sinks + min(s.n, g.tiles * g.tokens));
     const int blocks = (int)((keys + 127) / 128), all = c.units * Hkv;
     const int cap = min(g.most, blocks / (kLeast / 128));
     if (all >= kWave * kRounds || cap < 2) return c;

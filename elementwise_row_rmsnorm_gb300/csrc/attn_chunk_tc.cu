@@ -17,6 +17,11 @@
 //
 //   S0 = q0 k(j+1)^T, O0 += p0 v(j), S1 = q1 k(j+1)^T, O1 += p1 v(j)
 //
+// Over an 8-bit cache two more warpgroups widen codes and scales to bf16, exactly.
+// What their registers leave to the softmax warps does not hold a row of S, so S is
+// not free early; each tile has one of its own, the weights take its place, and
+// S(j+1) follows O += p v(j).
+//
 // Both tiles of an item walk the same blocks, so the one with the earlier rows
 // may meet a block that none of them sees: its weights are zeros.
 //
@@ -30,7 +35,19 @@
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 over the
 // one in use, as in attn_prompt_tc.cu.
+//
+// Measured, with 32 heads over 8 of D 128 and pages of 64: 2048 tokens behind 30720
+// 715 us, 1480 TFLOP/s (softmax and products take turns on what the SM issues);
+// 24 sequences of up to 200 behind up to 8000 264 us; 64 of 5 behind 8000 412 us,
+// 5.1 TB/s of keys; a prompt of 8192 under a window of 1024 127 us.  Over an 8-bit
+// cache the widening bounds it: 2048 behind 30720 1.17 ms, 64 of 5 behind 8000 535 us
+// (eight warps take 1.2 to 1.5 thousand clocks for a block's k, as many for its v;
+// with four 650 us, and one warp that waited for each block's pages and then for its
+// scales 620).  Not kept: slots that share one tile's blocks, every other one each (545
+// us), four warps for k alone and four for v (580), and pages asked into L2 a block
+// ahead (bf16, 64 of 5: 426 us for 411).
 #include "attn_chunk.cuh"
+#include "attn_chunk_row.cuh"
 #include "gbe_elementwise.h"
 #include "kv_cache.cuh"
 #include "tensor_core.cuh"
@@ -42,9 +59,8 @@ namespace {
 
 constexpr int kM = 128, kN = 128;
 constexpr int kLoadWarp = 8, kItemWarp = 9, kMmaWarp = 10;  // products: a warp for each tile
-constexpr int kWidenWarp = 12;   // over an 8-bit cache, and the three after it
+constexpr int kWidenWarp = 12, kWidenWarps = 8;  // over an 8-bit cache
 constexpr float kGrowth = 8.0f;  // a maximum may lag this many powers of two
-constexpr int kPacked = -1;      // KV of rows that are not in a cache
 
 // What the item warp hands out.  Of two tiles, tile t goes to slot t -- its
 // softmax warpgroup, its thread of products and their tensor memory --; one alone
@@ -75,22 +91,28 @@ struct Control {
 template <int KV, int DP>
 struct Shape {
     static constexpr bool kE4 = KV == GBE_KV_E4M3;
-    static constexpr int kThreads = kE4 ? 512 : 384;
+    static constexpr int kThreads = kE4 ? 640 : 384;
     // Registers of a thread: 384 threads were launched with 168 each (64512), the
-    // softmax warpgroups take 208 and the issuing one keeps 80 (63488); 512 threads
-    // with 128 (65536): 200, and 56 of the issuing and the widening one (65536).
-    static constexpr int kSoftmaxRegs = kE4 ? 200 : 208, kIssueRegs = kE4 ? 56 : 80, kWidenRegs = 56;
-    static constexpr int kReaders = kE4 ? 15 : 11;        // warps that read an item: all but the one that finds it
+    // softmax warpgroups take 208 and the issuing one keeps 80 (63488); of 640 with
+    // 96 (61440), 144, 64 and the widening ones 64 (61440).
+    static constexpr int kSoftmaxRegs = kE4 ? 144 : 208, kIssueRegs = kE4 ? 64 : 80, kWidenRegs = 64;
+    static constexpr int kReaders = kE4 ? 19 : 11;        // warps that read an item: all but the one that finds it
     static constexpr int kPanel = 128 * 128;              // 128 rows of 64 bf16
     static constexpr int kTile = kPanel * (DP / 64);      // 128 rows of DP
     static constexpr int kStages = (kE4 ? 3 : 4) * (128 / DP);
     static constexpr int kOutRow = kE4 ? 32 : 64;         // bytes of a row on their way out
     static constexpr int kOut = 8 * 32 * kOutRow;         // 32 rows for each softmax warp
-    // 8-bit rows on their way in, 64 bytes of each in a panel, and the scales of two blocks
+    // 8-bit rows on their way in, 64 bytes of each in a panel, and the scales and the pages of kAhead blocks
+    static constexpr int kAhead = 8;
     static constexpr int kRaw = kE4 ? kN * DP : 0, kRaws = 3, kRawPanel = kN * 64;
     static constexpr int kRawAt = kTile * (2 + kStages) + kOut, kScaleAt = kRawAt + kRaws * kRaw;
-    static constexpr int kControlAt = kScaleAt + (kE4 ? 2 * 2 * kN : 0);
+    static constexpr int kPageAt = kScaleAt + (kE4 ? kAhead * 2 * kN : 0);
+    static constexpr int kControlAt = kPageAt + (kE4 ? kAhead * 32 * 4 : 0);
     static constexpr int kBytes = kControlAt + 1024 + (int)sizeof(Control);
+    // Tensor memory of slot t: O behind 256.  One S for both and weights of each; over an
+    // 8-bit cache an S for each, of which the weights take the place.
+    __host__ __device__ static constexpr int s_at(int t) { return kE4 ? 128 * t : 0; }
+    __host__ __device__ static constexpr int p_at(int t) { return kE4 ? 128 * t : 128 + 64 * t; }
     // where piece c (16 bytes) of row r of a warp's rows lies on its way out
     __device__ static __forceinline__ int out_at(int r, int c) {
         constexpr int kPieces = kOutRow / 16, kSide = 8 / kPieces;  // rows side by side
@@ -116,161 +138,6 @@ __device__ __forceinline__ Row row_of(const Args& g, const Item& it, int u, int 
     x.head = head0 + r % g.heads;
     x.there = r < g.tokens * g.heads && x.token < it.s.n && x.head < g.group;
     return x;
-}
-
-// The row of key j in k and v; -1: it lies on no page of the cache.
-template <int KV>
-__device__ __forceinline__ int64_t key_at(const ChunkArgs& a, const Item& it, int kvh, int j) {
-    if constexpr (KV == kPacked) return it.s.begin + (int64_t)j;
-    const int page_i = j / a.c.page_size, row = j - page_i * a.c.page_size;
-    const int32_t page = a.table[it.seq * a.max_pages + page_i];
-    if (page < 0 || page >= a.c.n_pages) return -1;
-    return page * a.c.page_stride + ((int64_t)kvh * a.c.page_size + row) * a.D;
-}
-
-// Four consecutive values of a bf16 row, widened.
-__device__ __forceinline__ float4 load4(const void* base, int64_t i) {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xFFFF0000u));
-}
-template <int KV, bool V>
-__device__ __forceinline__ float4 load_kv(const ChunkArgs& a, int kvh, int64_t at, int d) {
-    if constexpr (KV == kPacked) {
-        return load4(V ? a.v : a.k, at * (V ? a.v_stride : a.k_stride) + (int64_t)kvh * a.D + d);
-    } else if constexpr (KV == GBE_KV_E4M3) {
-        const int64_t page = at / a.c.page_stride, row = (at - page * a.c.page_stride) / a.D;
-        const uint8_t byte = (V ? a.c.v_scale : a.c.k_scale)[page * a.c.Hkv * a.c.page_size + row];
-        float f[4] = {};
-        if (byte != 0) {  // (0: zeros, whatever the codes)
-            e4m3x4_to_f32(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(V ? a.c.v : a.c.k) + at + d), f);
-            const float scale = __uint_as_float((uint32_t)byte << 23);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] *= scale;
-        }
-        return make_float4(f[0], f[1], f[2], f[3]);
-    } else {
-        return load4(V ? a.c.v : a.c.k, at + d);
-    }
-}
-
-__device__ __forceinline__ uint32_t not_finite(float4 x) {
-    auto bad = [](float f) { return (__float_as_uint(f) & 0x7F800000u) == 0x7F800000u; };
-    return (bad(x.x) ? 1u : 0u) | (bad(x.y) ? 2u : 0u) | (bad(x.z) ? 4u : 0u) | (bad(x.w) ? 8u : 0u);
-}
-
-// Which keys of a block, as bits, a row at `place` sees: word x is of keys
-// k0 + 32 x and on.  (Places, windows and sinks are 2^30 at most.)
-__device__ __forceinline__ uint32_t first_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
-__device__ __forceinline__ uint32_t seen_word(const Args& g, int place, int k0, int x) {
-    const int at = k0 + 32 * x;
-    uint32_t m = first_bits(place + 1 - at);
-    if (g.window > 0) m &= ~first_bits(place + 1 - g.window - at) | first_bits(g.sinks - at);
-    return m;
-}
-
-// One row of an item in f32 from the keys that it sees alone, by a whole warp: 32
-// keys at a time, a lane a key for the logits, a lane four entries for the output.
-template <int KV>
-__device__ __noinline__ void exact_row(const Args& g, const Item& it, int kvh, int token, int head) {
-    const ChunkArgs& a = g.a;
-    const int lane = threadIdx.x & 31, D = (int)a.D, place = it.s.len - it.s.n + token;
-    const float c = a.scale * kLog2e;
-    const Walk w = walk(g, it);
-    const int64_t row = (it.s.begin + (int64_t)token) * a.q_stride + ((int64_t)kvh * g.group + head) * D;
-    float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f), o = q;
-    if (lane * 4 < D) q = load4(a.q, row + lane * 4);
-    float m = -INFINITY, l = 0.0f;
-    for (int i = w.from * 4; i < w.to * 4; ++i) {
-        const int k0 = w.block(i >> 2) * kN + (i & 3) * 32, j = k0 + lane;
-        bool seen = seen_word(g, place, w.block(i >> 2) * kN, i & 3) >> lane & 1u;
-        const int64_t at = seen ? key_at<KV>(a, it, kvh, j) : -1;
-        seen = at >= 0;
-        if (!__any_sync(0xFFFFFFFFu, seen)) continue;
-        float s = 0.0f;
-        for (int d = 0; d < D; d += 4) {
-            const float4 k = seen ? load_kv<KV, false>(a, kvh, at, d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            s = fmaf(__shfl_sync(0xFFFFFFFFu, q.x, d >> 2), k.x, s);
-            s = fmaf(__shfl_sync(0xFFFFFFFFu, q.y, d >> 2), k.y, s);
-            s = fmaf(__shfl_sync(0xFFFFFFFFu, q.z, d >> 2), k.z, s);
-            s = fmaf(__shfl_sync(0xFFFFFFFFu, q.w, d >> 2), k.w, s);
-        }
-        s *= c;
-        // a NaN logit leaves a finite maximum, so that its NaN weight reaches the result
-        float mx = seen ? fmaxf(m, s == s ? s : -3.0e38f) : m;
-#pragma unroll
-        for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
-        const float r = m == -INFINITY ? 0.0f : ex2(m - mx);
-        const float p = !seen || s == -INFINITY ? 0.0f : ex2(s - mx);
-        m = mx;
-        float sum = p;
-#pragma unroll
-        for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
-        l = fmaf(l, r, sum);
-        o.x *= r, o.y *= r, o.z *= r, o.w *= r;
-        for (uint32_t left = __ballot_sync(0xFFFFFFFFu, seen); left; left &= left - 1) {
-            const int t = __ffs((int)left) - 1;
-            const float weight = __shfl_sync(0xFFFFFFFFu, p, t);
-            const int64_t from = __shfl_sync(0xFFFFFFFFu, at, t);
-            if (lane * 4 < D) {
-                const float4 v = load_kv<KV, true>(a, kvh, from, lane * 4);
-                o.x = fmaf(weight, v.x, o.x);
-                o.y = fmaf(weight, v.y, o.y);
-                o.z = fmaf(weight, v.z, o.z);
-                o.w = fmaf(weight, v.w, o.w);
-            }
-        }
-    }
-    const float y[4] = {o.x, o.y, o.z, o.w};
-    if (it.splits > 1) {
-        const int64_t part = part_at(g, it, token, kvh * g.group + head);
-        if (lane * 4 < D) *reinterpret_cast<float4*>(g.part_o + part * D + lane * 4) = o;
-        if (lane == 0) g.part_ml[part] = make_float2(m, l);
-    } else if (lane * 4 < D) {
-        const int64_t at = (it.s.begin + (int64_t)token) * a.out_stride + ((int64_t)kvh * g.group + head) * D + lane * 4;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) Store<kBF16>::store1(a.out, at + e, m == -INFINITY ? 0.0f : y[e] / l);
-    }
-}
-
-// A row that came out not finite: right as it is where the keys that it sees
-// made it so, but a weight of zero may also have met an infinity or a NaN of v
-// in a key of its blocks that it does not see.  Computed again only if an entry
-// is not finite, has such a value there, and has none among the keys that it
-// sees.  By a whole warp; the row has been written.
-template <int KV>
-__device__ __noinline__ void repair_row(const Args& g, const Item& it, int kvh, int token, int head) {
-    const ChunkArgs& a = g.a;
-    const int lane = threadIdx.x & 31, D = (int)a.D, place = it.s.len - it.s.n + token;
-    const bool mine = lane * 4 < D;
-    const Walk w = walk(g, it);
-    uint32_t open = 0;  // entries that may have to be computed again
-    if (mine) {
-        if (it.splits > 1)
-            open = not_finite(*reinterpret_cast<const float4*>(
-                g.part_o + part_at(g, it, token, kvh * g.group + head) * D + lane * 4));
-        else
-            open = not_finite(load4(a.out, (it.s.begin + (int64_t)token) * a.out_stride +
-                                               ((int64_t)kvh * g.group + head) * D + lane * 4));
-    }
-    // entries that a key of the blocks, seen or not, has no finite value in
-    auto among = [&](bool seen, uint32_t until) {
-        uint32_t bad = 0;
-        for (int i = (w.to - w.from) * 4 - 1; i >= 0; --i) {
-            if (!__any_sync(0xFFFFFFFFu, until & ~bad)) break;
-            const int k0 = w.block(w.from + (i >> 2)) * kN;
-            uint32_t keys = seen_word(g, place, k0, i & 3);
-            if (!seen) keys = ~keys & first_bits(it.s.len - k0 - 32 * (i & 3));
-            for (; keys; keys &= keys - 1) {
-                const int64_t at = key_at<KV>(a, it, kvh, k0 + 32 * (i & 3) + __ffs((int)keys) - 1);
-                if (at >= 0 && mine) bad |= not_finite(load_kv<KV, true>(a, kvh, at, lane * 4));
-            }
-        }
-        return bad;
-    };
-    open &= among(false, open);
-    open &= ~among(true, open);
-    if (__any_sync(0xFFFFFFFFu, open)) exact_row<KV>(g, it, kvh, token, head);
 }
 
 // After a wait that gave up: NaN in every row of this CTA's items, done or not.
@@ -305,12 +172,10 @@ __device__ __forceinline__ bool widen16(const Vec16& codes, uint32_t byte, Vec16
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
         nan |= (codes.w[x] & 0x7F7F7F7Fu) + 0x01010101u;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t y = __byte_perm(codes.w[x], 0, h == 0 ? 0x1404 : 0x3424);
-            const uint32_t z = (y >> 4 & 0x07F007F0u) | (y & 0x80008000u);
-            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w[2 * x + h]) : "r"(z), "r"(scale));
-        }
+        // the upper and the lower bytes of four results
+        const uint32_t up = (codes.w[x] >> 4 & 0x07070707u) | (codes.w[x] & 0x80808080u), low = codes.w[x] << 4 & 0xF0F0F0F0u;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w[2 * x]) : "r"(__byte_perm(low, up, 0x5140)), "r"(scale));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w[2 * x + 1]) : "r"(__byte_perm(low, up, 0x7362)), "r"(scale));
     }
 #pragma unroll
     for (int x = 0; x < 4; ++x) lo.w[x] = w[x], hi.w[x] = w[4 + x];
@@ -333,7 +198,7 @@ __device__ __forceinline__ void widen16_f32(const Vec16& codes, uint32_t byte, V
 template <int DP>
 __device__ __forceinline__ void widen_rows(Control& ctl, uint8_t* const smem) {
     using S = Shape<GBE_KV_E4M3, DP>;
-    constexpr int kPieces = DP / 16, kRows = 128 / kPieces, kTurns = kN / kRows;
+    constexpr int kPieces = DP / 16, kRows = kWidenWarps * 32 / kPieces, kTurns = kN / kRows;
     const int tid = threadIdx.x - kWidenWarp * 32, lane = threadIdx.x & 31;
     volatile int* const abort = &ctl.abort;
     // Eight lanes have four pieces of 16 codes of two rows: what they read, and what
@@ -354,7 +219,7 @@ __device__ __forceinline__ void widen_rows(Control& ctl, uint8_t* const smem) {
             bool ok = mbar_wait(smem_addr(&ctl.raw_full[raw]), load / S::kRaws & 1, abort);
             ok = ok && mbar_wait(smem_addr(&ctl.kv_empty[stage]), (load / S::kStages & 1) ^ 1, abort);
             if (!__all_sync(0xFFFFFFFFu, ok)) return;
-            const uint8_t* const scale = smem + S::kScaleAt + (load & 3) * kN + r0;
+            const uint8_t* const scale = smem + S::kScaleAt + load % (2 * S::kAhead) * kN + r0;
             auto codes = [&](int x) { return *reinterpret_cast<const Vec16*>(from + raw * S::kRaw + x * (kRows * 64)); };
             auto write = [&](int x, const Vec16& lo, const Vec16& hi) {
                 const int r = r0 + x * kRows, c = piece * 2;
@@ -363,7 +228,7 @@ __device__ __forceinline__ void widen_rows(Control& ctl, uint8_t* const smem) {
                 *reinterpret_cast<Vec16*>(line + (((c + 1) ^ (r & 7)) << 4)) = hi;
             };
             uint32_t again = 0;
-#pragma unroll 2
+#pragma unroll
             for (int x = 0; x < kTurns; ++x) {
                 Vec16 lo, hi;
                 if (!widen16(codes(x), scale[x * kRows], lo, hi)) again |= 1u << x;
@@ -386,6 +251,82 @@ __device__ __forceinline__ void widen_rows(Control& ctl, uint8_t* const smem) {
     }
 }
 
+// An item's rows and their scales on their way in, by the copying warp: pages that
+// hold four rows of which the scales lie on the 4-byte grid.  A lane has rows
+// 4 lane .. 4 lane + 3 of each block.  What one needs of another is asked for
+// blocks ahead, into shared memory: a block's pages four, its scales, of which the
+// pages have come by then, two.
+template <int DP>
+__device__ __forceinline__ bool load_codes(Control& ctl, uint8_t* const smem, const Maps& maps, const Args& g,
+                                           const Walk& w, int len, int seq, int kvh, int box, int& loads) {
+    using S = Shape<GBE_KV_E4M3, DP>;
+    const KvCacheArgs& c = g.a.c;
+    const int lane = threadIdx.x & 31, size = c.page_size, boxes = kN / box;
+    const int32_t* const table = g.a.table + seq * g.a.max_pages;
+    volatile int* const abort = &ctl.abort;
+    const uint32_t pages = smem_addr(smem) + S::kPageAt, scales = smem_addr(smem) + S::kScaleAt;
+    const int base = loads / 2 - w.from;  // block x of the walk is block base + x of all
+    auto ask_page = [&](int x) {
+        const int j = w.block(x) * kN + 4 * lane;
+        const bool here = x < w.to && j < len;
+        cp_async4(pages + ((base + x) % S::kAhead * 32 + lane) * 4, table + (here ? j / size : 0), here ? 4 : 0);
+    };
+    auto page_of = [&](int x, int l) {
+        return *reinterpret_cast<const volatile int32_t*>(smem + S::kPageAt + ((base + x) % S::kAhead * 32 + l) * 4);
+    };
+    // 0, which makes zeros of a row whatever its codes, behind the sequence's end and where there is no page
+    auto ask_scales = [&](int x) {
+        const int j = w.block(x) * kN + 4 * lane, page = page_of(x, lane);
+        const bool here = x < w.to && j < len && page >= 0 && page < c.n_pages;
+        const int64_t at = here ? ((int64_t)page * c.Hkv + kvh) * size + j % size : 0;
+        const uint32_t to = scales + (base + x) % S::kAhead * (2 * kN) + 4 * lane;
+        cp_async4(to, c.k_scale + at, here ? min(4, len - j) : 0);
+        cp_async4(to + kN, c.v_scale + at, here ? min(4, len - j) : 0);
+    };
+    __syncwarp();
+    for (int x = 0; x < 4; ++x) ask_page(w.from + x);
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncwarp();
+    for (int x = 0; x < 2; ++x) {
+        ask_scales(w.from + x);
+        cp_async_commit();
+    }
+    bool ok = true;
+    for (int x = w.from; x < w.to; ++x) {
+        const int j = w.block(x) * kN + lane * box;
+        int page = (int)c.n_pages, row = 0;  // (from n_pages on: zeros)
+        if (lane < boxes && j < len) {
+            const int32_t p = page_of(x, lane * box / 4);
+            if (p >= 0 && p < c.n_pages) page = p, row = j % size;
+        }
+        for (int kv = 0; kv < 2; ++kv, ++loads) {
+            const int stage = loads % S::kRaws;
+            ok = __all_sync(0xFFFFFFFFu,
+                            mbar_wait(smem_addr(&ctl.raw_empty[stage]), (loads / S::kRaws & 1) ^ 1, abort));
+            if (!ok) return false;
+            const uint32_t full = smem_addr(&ctl.raw_full[stage]);
+            const uint32_t to = smem_addr(smem) + S::kRawAt + stage * S::kRaw + lane * box * 64;
+            if (lane < boxes) {
+#pragma unroll
+                for (int p = 0; p < DP / 64; ++p)
+                    tma_load_4d(to + p * S::kRawPanel, kv == 0 ? &maps.k : &maps.v, full, p * 64, row, kvh, page);
+            }
+            if (kv == 0) {
+                cp_async_wait<1>();  // this block's scales, the pages of the block after the next
+                __syncwarp();
+                ask_page(x + 4);
+                ask_scales(x + 2);
+                cp_async_commit();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_tx(full, S::kRaw);
+        }
+    }
+    cp_async_wait<0>();
+    return true;
+}
+
 template <int KV, int DP>
 __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
     chunk_tc(const __grid_constant__ Maps maps, const __grid_constant__ Args g, int box) {
@@ -401,7 +342,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(smem_addr(&ctl.kv_full[i]), S::kE4 ? 4 : 1);
+            mbar_init(smem_addr(&ctl.kv_full[i]), S::kE4 ? kWidenWarps : 1);
             mbar_init(smem_addr(&ctl.kv_empty[i]), 2);
         }
         for (int t = 0; t < 2; ++t) {
@@ -417,7 +358,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
         }
         for (int i = 0; i < S::kRaws; ++i) {
             mbar_init(smem_addr(&ctl.raw_full[i]), 1);
-            mbar_init(smem_addr(&ctl.raw_empty[i]), 4);
+            mbar_init(smem_addr(&ctl.raw_empty[i]), kWidenWarps);
         }
         for (int i = 0; i < kTodos; ++i) {
             mbar_init(smem_addr(&ctl.todo_full[i]), 1);
@@ -526,6 +467,8 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
             int loads = 0;               // of the ring so far; of an 8-bit cache, of the one ahead of it
             bool ok = true;
             const int boxes = kN / box;  // of a block; a power of two
+            // four rows' scales lie together, on the 4-byte grid
+            const bool fours = S::kE4 && box >= 4 && ((uintptr_t)a.c.k_scale | (uintptr_t)a.c.v_scale) % 4 == 0;
             for (int i = 0; ok; ++i) {
                 if (!(ok = __all_sync(0xFFFFFFFFu, todo_ready(i)))) break;
                 const Todo& todo = ctl.todo[i % kTodos];
@@ -539,6 +482,12 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                 if (lane == 0) todo_read(i);
                 if (slot < 0) break;
                 if (w.from == w.to) continue;
+                if constexpr (S::kE4) {
+                    if (fours) {
+                        ok = load_codes<DP>(ctl, smem, maps, g, w, it.s.len, it.seq, kvh, box, loads);
+                        continue;
+                    }
+                }
                 // box b of the walk's block x: the page (from n_pages on: zeros) and the row in it
                 auto look_up = [&](int x, int b, int& page, int& row) {
                     const int j = w.block(x) * kN + b * box;
@@ -599,8 +548,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                         const uint32_t full = smem_addr(S::kE4 ? &ctl.raw_full[stage] : &ctl.kv_full[stage]);
                         const uint32_t to = S::kE4 ? smem_addr(smem) + S::kRawAt + stage * kBytes : kv_smem + stage * kBytes;
                         if constexpr (S::kE4) {
-                            // (two blocks' are kept: the block before the last is done with when this load's place is)
-                            *reinterpret_cast<uint32_t*>(smem + S::kScaleAt + (loads & 3) * kN + 4 * lane) =
+                            *reinterpret_cast<uint32_t*>(smem + S::kScaleAt + loads % (2 * S::kAhead) * kN + 4 * lane) =
                                 kv == 0 ? k_bytes : v_bytes;
                             if (kv == 1) ask(x + 1);
                             __syncwarp();
@@ -654,7 +602,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
             constexpr uint32_t idesc_o = bf16_idesc(kM, DP, true), hi = smem_desc_hi(1024);
             const uint32_t q_lo = smem_desc_lo(q_smem + t * S::kTile, 16), k_lo = smem_desc_lo(kv_smem, 16);
             const uint32_t v_lo = smem_desc_lo(kv_smem, S::kPanel);
-            const uint32_t o = tmem + 256 + t * 128, pw = tmem + 128 + t * 64;
+            const uint32_t o = tmem + 256 + t * 128;
             bool ok = true;
             int loads = 0;          // the ring's before this item: k of block j is load loads + 2 j
             int done[2] = {0, 0};   // blocks of each slot before this item
@@ -674,24 +622,30 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                 // S is free for an item once the last block of the item before has been read.  Both threads wait for
                 // that at every item, so that neither passes over a phase (a wait by parity holds only where the phase
                 // before has completed); two barriers in turn, for a thread may be as far behind as the other's item.
-                if (every > 0)
+                if (!S::kE4 && every > 0)
                     ok = mbar_wait(smem_addr(&ctl.s_last[(every - 1) & 1]), (every - 1) / 2 & 1, abort);
-                // and within it once the block before in the order (0, j), (1, j), (0, j + 1), ... has been
+                // And within it once the block before in the order (0, j), (1, j), (0, j + 1), ... has been.  (Over an
+                // 8-bit cache it is free once the weights that took its place have met v.)
                 auto s_free = [&](int j) {
-                    const int pt = !two ? t : t ^ 1, pj = two && t == 1 ? j : j - 1;
-                    if (pj >= 0) ok = ok && mbar_wait(smem_addr(&ctl.s_free[pt]), (done[pt] + pj) & 1, abort);
+                    if constexpr (S::kE4) {
+                        if (done[t] + j > 0)
+                            ok = ok && mbar_wait(smem_addr(&ctl.o_done[t]), (done[t] + j - 1) & 1, abort);
+                    } else {
+                        const int pt = !two ? t : t ^ 1, pj = two && t == 1 ? j : j - 1;
+                        if (pj >= 0) ok = ok && mbar_wait(smem_addr(&ctl.s_free[pt]), (done[pt] + pj) & 1, abort);
+                    }
                 };
                 auto scores = [&](int j) {
-                    loaded(loads + 2 * j);
+                    const int x = loads + 2 * j, stage = x % S::kStages;
+                    loaded(x);
                     s_free(j);
                     if (!ok) return;
                     tc_fence_after();
-                    const int stage = (loads + 2 * j) % S::kStages;
                     const uint32_t k0 = k_lo + stage * (S::kTile >> 4);
 #pragma unroll
-                    for (int x = 0; x < DP / 16; ++x) {
-                        const uint32_t off = ((x / 4) * S::kPanel + (x % 4) * 32) >> 4;
-                        mma_ss(tmem, q_lo + off, hi, k0 + off, hi, idesc_s, x > 0);
+                    for (int y = 0; y < DP / 16; ++y) {
+                        const uint32_t off = ((y / 4) * S::kPanel + (y % 4) * 32) >> 4;
+                        mma_ss(tmem + S::s_at(t), q_lo + off, hi, k0 + off, hi, idesc_s, y > 0);
                     }
                     mma_commit(smem_addr(&ctl.s_full[t]));
                     mma_commit(smem_addr(&ctl.kv_empty[stage]));
@@ -699,28 +653,31 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                 };
                 if (mine) {
                     ok = ok && mbar_wait(smem_addr(&ctl.q_full[t]), items & 1, abort);
-                    scores(0);
+                    if (!S::kE4) scores(0);
                 }
                 for (int j = 0; ok && mine && j < n; ++j) {
-                    if (j + 1 < n) scores(j + 1);
-                    loaded(loads + 2 * j + 1);
+                    if (S::kE4)
+                        scores(j);
+                    else if (j + 1 < n)
+                        scores(j + 1);
+                    const int x = loads + 2 * j + 1, stage = x % S::kStages;
+                    loaded(x);
                     ok = ok && mbar_wait(smem_addr(&ctl.p_ready[t]), (done[t] + j) & 1, abort);
                     // O has been read for the last item
                     if (j == 0 && items > 0) ok = ok && mbar_wait(smem_addr(&ctl.o_free[t]), (items - 1) & 1, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    const int stage = (loads + 2 * j + 1) % S::kStages;
                     const uint32_t v0 = v_lo + stage * (S::kTile >> 4);
 #pragma unroll
-                    for (int x = 0; x < kN / 16; ++x)
-                        mma_ts(o, pw + x * 8, v0 + x * (2048 >> 4), hi, idesc_o, j > 0 || x > 0);
+                    for (int y = 0; y < kN / 16; ++y)
+                        mma_ts(o, tmem + S::p_at(t) + y * 8, v0 + y * (2048 >> 4), hi, idesc_o, j > 0 || y > 0);
                     mma_commit(smem_addr(&ctl.o_done[t]));
                     mma_commit(smem_addr(&ctl.kv_empty[stage]));
                 }
                 // blocks that only the other slot works on
-                for (int x = 0; ok && !mine && x < 2 * n; ++x) {
-                    loaded(loads + x);
-                    if (ok) mbar_arrive(smem_addr(&ctl.kv_empty[(loads + x) % S::kStages]));
+                for (int x = loads; ok && !mine && x < loads + 2 * n; ++x) {
+                    loaded(x);
+                    if (ok) mbar_arrive(smem_addr(&ctl.kv_empty[x % S::kStages]));
                 }
                 loads += 2 * n;
                 if (two || slot == 0) done[0] += n;
@@ -737,7 +694,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftmaxRegs));
         const int t = warp >> 2;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
-        const uint32_t ts = tmem + lanes, tp = tmem + 128 + t * 64 + lanes, to = tmem + 256 + t * 128 + lanes;
+        const uint32_t ts = tmem + S::s_at(t) + lanes, tp = tmem + S::p_at(t) + lanes, to = tmem + 256 + t * 128 + lanes;
         // (never 0, so that c times the -inf of a masked place stays -inf)
         const float c = fmaxf(fabsf(a.scale) * kLog2e, __uint_as_float(1u));
         uint8_t* const stage = smem + S::kTile * (2 + S::kStages) + warp * (S::kOut / 8);
@@ -785,7 +742,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; idle && j < n; ++j) {
                 ok = mbar_wait(smem_addr(&ctl.s_full[t]), (done + j) & 1, abort);
-                s_read(j);
+                if (!S::kE4) s_read(j);
                 // (no sooner than the others: it would be counted for the weights before)
                 if (j > 0) ok = ok && mbar_wait(smem_addr(&ctl.o_done[t]), (done + j - 1) & 1, abort);
                 ok = __all_sync(0xFFFFFFFFu, ok);
@@ -808,74 +765,141 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.s_full[t]), (done + j) & 1, abort));
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t s[128];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) tmem_ld32(ts + y * 32, s + y * 32);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) tmem_wait_ld32(s + y * 32);
-                tc_fence_before();
-                __syncwarp();
-                s_read(j);
-                if (!whole) {
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        uint32_t seen = seen_word(g, place, k0, y);
-                        if (KV != kPacked && gone) seen &= reinterpret_cast<const uint32_t*>(stage)[y];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) s[32 * y + e] = seen >> e & 1u ? s[32 * y + e] : 0xFF800000u;
-                    }
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int y = 0; y < 128; y += 8)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[y + e]), __uint_as_float(s[y + 4 + e])));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                const bool grow = m == -INFINITY ? top > m : (top - m) * c > kGrowth;
+                // a word's bits: which of 32 keys of the block are seen; the maximum of some logits, what is in use moved up
+                auto seen = [&](int y) {
+                    uint32_t word = seen_word(g, place, k0, y);
+                    if (KV != kPacked && gone) word &= reinterpret_cast<const uint32_t*>(stage)[y];
+                    return word;
+                };
                 auto last_done = [&] {  // the product with the last weights is done
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.o_done[t]), (done + j - 1) & 1, abort));
                     tc_fence_after();
                 };
-                if (__any_sync(0xFFFFFFFFu, grow)) {
+                auto move_up = [&](float top) {
+                    const bool grow = m == -INFINITY ? top > m : (top - m) * c > kGrowth;
+                    if (!__any_sync(0xFFFFFFFFu, grow)) return;
                     const float m2 = grow ? top : m;
                     if (j > 0) {
-                        last_done();
-                        if (!ok) break;
+                        if (!S::kE4) last_done();
+                        if (!ok) return;
                         const float r = m == -INFINITY ? 0.0f : ex2((m - m2) * c);
                         l *= r;
 #pragma unroll
-                        for (int y = 0; y < DP / 32; ++y) {
-                            uint32_t o[32];
-                            tmem_ld32(to + y * 32, o);
-                            tmem_wait_ld32(o);
+                        for (int y = 0; y < DP; y += S::kE4 ? 16 : 32) {
+                            uint32_t o[S::kE4 ? 16 : 32];
+                            if constexpr (S::kE4)
+                                tmem_ld16(to + y, o), tmem_wait_ld16(o);
+                            else
+                                tmem_ld32(to + y, o), tmem_wait_ld32(o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
-                            tmem_st32(to + y * 32, o);
+                            for (uint32_t& e : o) e = __float_as_uint(__uint_as_float(e) * r);
+                            if constexpr (S::kE4)
+                                tmem_st16(to + y, o);
+                            else
+                                tmem_st32(to + y, o);
                         }
                     }
                     m = m2;
-                }
-                const float shift = m == -INFINITY ? 0.0f : -m * c;
-                const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
-                float2 sum[4] = {};
-                uint32_t p[64];
+                };
+                if constexpr (!S::kE4) {
+                    // all of a row's logits in registers, and S given up at once
+                    uint32_t s[128];
 #pragma unroll
-                for (int e = 0; e < 64; ++e) {
-                    float2 y = fma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2,
-                                       shift2);
-                    y.x = ex2(y.x), y.y = ex2(y.y);
-                    sum[e & 3] = add2_rn(sum[e & 3], y);
-                    p[e] = f32x2_to_bf16x2_bits(y.x, y.y);
-                }
-                const float2 add = add2_rn(add2_rn(sum[0], sum[1]), add2_rn(sum[2], sum[3]));
-                l += add.x + add.y;
-                if (j > 0) {
-                    last_done();
+                    for (int y = 0; y < 4; ++y) tmem_ld32(ts + y * 32, s + y * 32);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) tmem_wait_ld32(s + y * 32);
+                    tc_fence_before();
+                    __syncwarp();
+                    s_read(j);
+                    if (!whole) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const uint32_t word = seen(y);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s[32 * y + e] = word >> e & 1u ? s[32 * y + e] : 0xFF800000u;
+                        }
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int y = 0; y < 128; y += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[y + e]), __uint_as_float(s[y + 4 + e])));
+                    move_up(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
                     if (!ok) break;
+                    const float shift = m == -INFINITY ? 0.0f : -m * c;
+                    const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+                    float2 sum[4] = {};
+                    uint32_t p[64];
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) {
+                        float2 y = fma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2,
+                                           shift2);
+                        y.x = ex2(y.x), y.y = ex2(y.y);
+                        sum[e & 3] = add2_rn(sum[e & 3], y);
+                        p[e] = f32x2_to_bf16x2_bits(y.x, y.y);
+                    }
+                    const float2 add = add2_rn(add2_rn(sum[0], sum[1]), add2_rn(sum[2], sum[3]));
+                    l += add.x + add.y;
+                    if (j > 0) {
+                        last_done();
+                        if (!ok) break;
+                    }
+                    tmem_st32(tp, p);
+                    tmem_st32(tp + 32, p + 32);
+                } else {
+                    // The registers are the widening warps' too: keys 64 .. 95 are read once more.  (The product before
+                    // this one was done with the weights before S took their place.)
+                    uint32_t s[64], b[32];
+                    auto read = [&](int y, uint32_t* to) { tmem_ld32(ts + 32 * y, to); };
+                    auto there = [&](int y, uint32_t* to) {
+                        tmem_wait_ld32(to);
+                        if (whole) return;
+                        const uint32_t word = seen(y);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) to[e] = word >> e & 1u ? to[e] : 0xFF800000u;
+                    };
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto top = [&](const uint32_t* of) {
+#pragma unroll
+                        for (int y = 0; y < 32; y += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(of[y + e]), __uint_as_float(of[y + 4 + e])));
+                    };
+                    read(2, b), read(0, s), read(1, s + 32);
+                    there(2, b);
+                    top(b);
+                    there(0, s), there(1, s + 32);
+                    read(3, b);
+                    top(s), top(s + 32);
+                    there(3, b);
+                    top(b);
+                    move_up(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    if (!ok) break;
+                    const float shift = m == -INFINITY ? 0.0f : -m * c;
+                    const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+                    float2 sum[2] = {};
+                    auto weigh = [&](int y, const uint32_t* of) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float2 z = fma2_rn(make_float2(__uint_as_float(of[2 * e]), __uint_as_float(of[2 * e + 1])),
+                                               c2, shift2);
+                            z.x = ex2(z.x), z.y = ex2(z.y);
+                            sum[e & 1] = add2_rn(sum[e & 1], z);
+                            p[e] = f32x2_to_bf16x2_bits(z.x, z.y);
+                        }
+                        tmem_st16(tp + 16 * y, p);
+                    };
+                    weigh(3, b);
+                    read(2, b);
+                    weigh(0, s), weigh(1, s + 32);
+                    there(2, b);
+                    weigh(2, b);
+                    const float2 add = add2_rn(sum[0], sum[1]);
+                    l += add.x + add.y;
                 }
-                tmem_st32(tp, p);
-                tmem_st32(tp + 32, p + 32);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -1022,9 +1046,8 @@ cudaError_t go(const ChunkArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int64_t seqs = a.n_seqs < a.T ? a.n_seqs : a.T, sms = sm_count();
     const int64_t pieces = (a.T / g.tokens + seqs) * g.parts * a.Hkv * g.most;
-    const cudaError_t f = launch(chunk_tc<KV, DP>, dim3((unsigned)(pieces < sms ? pieces : sms)), dim3(S::kThreads), smem,
-                                 st, maps, g, (int)box);
-    return f != cudaSuccess ? f : launch_join(g, kBF16, st);
+    return launch(chunk_tc<KV, DP>, dim3((unsigned)(pieces < sms ? pieces : sms)), dim3(S::kThreads), smem, st, maps, g,
+                  (int)box);
 }
 
 }  // namespace
