@@ -609,8 +609,11 @@ int gbe_attn_prompt_window(const void *q, int64_t q_stride, const void *k, int64
  * A row's bits depend on its own sequence, on Hq, Hkv, D, page_size, max_pages,
  * window and sinks: the same in a batch of any size and at any place in it.
  * bf16 with D up to 128, q and out on the 16-byte grid, everything in device
- * memory, goes through the tensor cores, the weights rounded to bf16 for the
- * second product; other calls do not, and bf16 ones differ within that rounding.
+ * memory, goes through the tensor cores (over an 8-bit cache with D and the page
+ * stride multiples of 16 and an even page_size), the weights rounded to bf16 for
+ * the second product; a row that shares a block of 128 keys with an infinity or a
+ * NaN that it does not see is computed again without that rounding.  Other calls
+ * do not, and bf16 ones differ within that rounding.
  * Errors : as for gbe_attn_decode.  Hq is a multiple of Hkv, at most 65536; T at
  * most 2^28, n_seqs at most 2^24, max_pages * page_size at most 2^30.
  */
