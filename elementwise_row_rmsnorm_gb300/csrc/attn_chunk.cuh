@@ -158,6 +158,7 @@ class Source {
 #pragma unroll
             for (int step = 16; step >= 1; step >>= 1)
                 if (__shfl_sync(0xFFFFFFFFu, upto_, who + step - 1) <= at) who += step;
+            who = min(who, 31);
             const uint32_t before = __shfl_sync(0xFFFFFFFFu, upto_, who == 0 ? 0 : who - 1);
             const Seq s = {__shfl_sync(0xFFFFFFFFu, group_.begin, who), __shfl_sync(0xFFFFFFFFu, group_.n, who),
                            __shfl_sync(0xFFFFFFFFu, group_.len, who)};
@@ -168,8 +169,9 @@ class Source {
                 // what runs at a time reads the same keys
                 const uint32_t x = at - (who == 0 ? 0u : before), y = x / (uint32_t)g_.a.Hkv;
                 kvh_ = (int)(x - y * (uint32_t)g_.a.Hkv);
-                split_ = (int)(y / (uint32_t)units);
-                unit_ = units - 1 - (int)(y - (uint32_t)split_ * (uint32_t)units);
+                split_ = (int)(y / (uint32_t)max(units, 1));
+                unit_ = max(units, 1) - 1 - (int)(y - (uint32_t)split_ * (uint32_t)max(units, 1));
+                split_ = min(split_, splits - 1);  // (starts that decrease may have more pieces than 32 bits count)
                 s_ = s, splits_ = splits, seq_ = (int)first_ + who;
             }
             const bool past = splits_ == 0 && index >= base_ + total;

@@ -322,3 +322,22 @@ def test_buffers_past_2_31_entries(dtype, kind):
         attn_ref.assert_within(out, want, tol, (window, sinks))
         one = gbe.attn_decode_window(q[2:], cache, table, i32([n]), window, sinks, 0.1)
         attn_ref.assert_within(one, want[2:], tol[2:], (window, sinks))
+
+
+@pytest.mark.parametrize("dtype,kind", KINDS)
+def test_starts_that_decrease_stay_within_the_buffers(dtype, kind):
+    """Rows that one sequence has are right, rows that two have are one's or the other's, no others are written."""
+    Hq, H, D, P = 4, 2, 64, 16
+    starts, lens = [5, 50, 20, 60, -7, 2 ** 30], [3000, 40, 90, 7, 200]
+    cache, table = filled(lens, P, H, D, dtype, kind, 51)
+    q = rand((64, Hq, D), dtype, 52)
+    out = torch.full_like(q, 9.0)
+    _into(out, q, cache, starts[:4], table[:3], lens[:3], 0.1)
+    one, tol, _ = chunk_ref.chunk(q, cache, starts[:2], table[:1], lens[:1], 0.1, rounded=dtype == BF)
+    two, e, _ = chunk_ref.chunk(q, cache, starts[2:4], table[2:3], lens[2:3], 0.1, rounded=dtype == BF)
+    attn_ref.assert_within(out[5:20], one[5:20], tol[5:20])
+    attn_ref.assert_within(out[50:60], two[50:60], e[50:60])
+    assert bool((((out[20:50] - one[20:50]).abs() <= tol[20:50]) | ((out[20:50] - two[20:50]).abs() <= e[20:50])).all())
+    assert bool((out[:5] == 9.0).all()) and bool((out[60:] == 9.0).all())
+    _into(out, q, cache, starts, table, lens, 0.1)  # ends outside the buffers count as these
+    assert bool(out.isfinite().all()) and bool((out != 9.0).any(-1).all())
