@@ -17,9 +17,10 @@
 // of its token, all loads ahead of the first store.  Angles are formed once a CTA,
 // into shared memory: formed by the lanes, each its own, they bounded the kernel.
 //
-// Measured: 8192 tokens of 32 + 8 + 8 heads of 128 into 8 bits 53 us, 3.5 TB/s (the
-// latency of a CTA's positions, angles and rows, one behind the other, bounds it);
-// 64 tokens of them into bf16 2.8 us a call in a graph.
+// Measured: 8192 tokens of 32 + 8 + 8 heads of 128 into 8 bits 43 us, 4.3 TB/s, into
+// bf16 35 us, 5.7 TB/s; 64 tokens 2.6 us a call in a graph.  A CTA's positions, angles
+// and rows come one behind the other, so what hides them is more CTAs: three an SM
+// (85 registers), where two (100) took 52 us; two heads a lane in four of them 44.
 #include "gbe_elementwise.h"
 #include "kv_cache.cuh"
 #include "launch.h"
@@ -54,7 +55,7 @@ __device__ __forceinline__ float row_max(float m, int G, uint32_t mask) {
 }
 
 template <int DT, int KV, int LAYOUT, int HEADS>
-__global__ void __launch_bounds__(kThreads) rope_kv_rows(RopeKvArgs a, Shape sh, Divisor by_token, Divisor by_page,
+__global__ void __launch_bounds__(kThreads, 3) rope_kv_rows(RopeKvArgs a, Shape sh, Divisor by_token, Divisor by_page,
                                                          Divisor by_half) {
     __shared__ float2 angles[kAngles];
     pdl_begin();
