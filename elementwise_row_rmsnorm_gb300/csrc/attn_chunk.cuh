@@ -28,7 +28,12 @@ namespace chunk {
 
 constexpr int kWave = 152;       // items at a time, which a sequence's splits are to fill
 constexpr int kRounds = 8;       // once at least, and at most as often
-constexpr int kLeast = 1024;     // keys of a split at least
+// Keys of a split at least; twice as many where a sequence has more rows of a kv head than kFewRows, for every split
+// writes and reads partial results of all of them.  A sequence alone is best cut short, a batch best left whole
+// (bf16, 32 heads over 8 of 128): 24 sequences of up to 200 behind up to 8000 264 us with 1024 for all and 222 with
+// 2048, 16 of 60 behind 8000 182 and 163, one of 100 behind 4000 33 and 42; 64 of 5 behind 8000 411 and 390, but one
+// of 5 25 and 38, where so few rows are a user who waits.
+constexpr int kLeast = 1024, kFewRows = 128;
 constexpr int kEnds = 4;         // what an item's first copies, last rows and join cost, in blocks of 128 keys
 constexpr int kUnitRows = 256;   // at most
 constexpr int kPacked = -1;      // the type of keys that are not in a cache
@@ -97,7 +102,7 @@ static __device__ __noinline__ Cut cut_of(const Args& g, const Seq& s) {
     int64_t keys = s.len;
     if (a.window > 0) keys = min(keys, a.window + a.sinks + min(s.n, g.tiles * g.tokens));
     const int blocks = (int)((keys + 127) / 128), all = c.units * Hkv;
-    const int cap = min(g.most, blocks / (kLeast / 128));
+    const int cap = min(g.most, blocks / (kLeast / 128 * ((int64_t)s.n * g.group > kFewRows ? 2 : 1)));
     if (all >= kWave * kRounds || cap < 2) return c;
     // what one round, two, ... make possible; worth it from a 16th on
     float cost = (float)((all + kWave - 1) / kWave * (blocks + kEnds)) * 0.9375f;

@@ -38,7 +38,7 @@
 //
 // Measured, with 32 heads over 8 of D 128 and pages of 64: 2048 tokens behind 30720
 // 715 us, 1480 TFLOP/s (softmax and products take turns on what the SM issues);
-// 24 sequences of up to 200 behind up to 8000 264 us; 64 of 5 behind 8000 412 us,
+// 24 sequences of up to 200 behind up to 8000 227 us; 64 of 5 behind 8000 412 us,
 // 5.1 TB/s of keys; a prompt of 8192 under a window of 1024 127 us.  Over an 8-bit
 // cache the widening bounds it: 2048 behind 30720 1.17 ms, 64 of 5 behind 8000 535 us
 // (eight warps take 1.2 to 1.5 thousand clocks for a block's k, as many for its v;
