@@ -17,10 +17,10 @@
 // of its token, all loads ahead of the first store.  Angles are formed once a CTA,
 // into shared memory: formed by the lanes, each its own, they bounded the kernel.
 //
-// Measured: 8192 tokens of 32 + 8 + 8 heads of 128 into 8 bits 43 us, 4.3 TB/s, into
-// bf16 35 us, 5.7 TB/s; 64 tokens 2.6 us a call in a graph.  A CTA's positions, angles
-// and rows come one behind the other, so what hides them is more CTAs: three an SM
-// (85 registers), where two (100) took 52 us; two heads a lane in four of them 44.
+// Measured: 8192 tokens of 32 + 8 + 8 heads of 128 into 8 bits and read back from
+// there (which takes 10 us) 50 us, 4.7 TB/s; 64 tokens 2.6 us a call in a graph.  A
+// CTA's positions, angles and rows come one behind the other, so what hides them is
+// more CTAs: three an SM, where two took 60 us; two heads a lane in four of them 51.
 #include "gbe_elementwise.h"
 #include "kv_cache.cuh"
 #include "launch.h"
