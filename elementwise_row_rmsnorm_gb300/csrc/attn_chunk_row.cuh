@@ -21,15 +21,11 @@ __device__ __forceinline__ int64_t key_at(const ChunkArgs& a, const Item& it, in
     return page * a.c.page_stride + ((int64_t)kvh * a.c.page_size + row) * a.D;
 }
 
-// Four consecutive values of a bf16 row, widened; on the 8-byte grid, or anywhere.
+// Four consecutive values of a bf16 row, widened; on the 8-byte grid.
 __device__ __forceinline__ float4 load4(const void* base, int64_t i) {
     const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
     return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
                        __uint_as_float(w.y & 0xFFFF0000u));
-}
-__device__ __forceinline__ float4 load4_anywhere(const void* base, int64_t i) {
-    return make_float4(Store<kBF16>::load1(base, i), Store<kBF16>::load1(base, i + 1), Store<kBF16>::load1(base, i + 2),
-                       Store<kBF16>::load1(base, i + 3));
 }
 template <int KV, bool V>
 __device__ __forceinline__ float4 load_kv(const ChunkArgs& a, int kvh, int64_t at, int d) {
@@ -76,7 +72,7 @@ static __device__ __noinline__ void exact_row(const Args& g, const Item& it, int
     const Walk w = walk(g, it);
     const int64_t row = (it.s.begin + (int64_t)token) * a.q_stride + ((int64_t)kvh * g.group + head) * D;
     float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f), o = q;
-    if (lane * 4 < D) q = load4_anywhere(a.q, row + lane * 4);
+    if (lane * 4 < D) q = load4(a.q, row + lane * 4);
     float m = -INFINITY, l = 0.0f;
     for (int i = w.from * 4; i < w.to * 4; ++i) {
         const int k0 = w.block(i >> 2) * kKeys + (i & 3) * 32, j = k0 + lane;
@@ -147,7 +143,7 @@ static __device__ __noinline__ void repair_row(const Args& g, const Item& it, in
             open = not_finite(*reinterpret_cast<const float4*>(
                 g.part_o + part_at(g, it, token, kvh * g.group + head) * D + lane * 4));
         else
-            open = not_finite(load4_anywhere(a.out, (it.s.begin + (int64_t)token) * a.out_stride +
+            open = not_finite(load4(a.out, (it.s.begin + (int64_t)token) * a.out_stride +
                                                ((int64_t)kvh * g.group + head) * D + lane * 4));
     }
     // entries that a key of the blocks, seen or not, has no finite value in

@@ -79,8 +79,8 @@ struct Todo {
 constexpr int kTodos = 4;  // in hand
 
 struct Control {
-    uint64_t q_full[2], q_empty[2], s_last[2], kv_full[8], kv_empty[8], s_full[2], s_free[2], p_ready[2], o_done[2], o_free[2];
-    uint64_t drained[2], raw_full[3], raw_empty[3];
+    uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], s_full[2], s_free[2], s_last[2];
+    uint64_t p_ready[2], o_done[2], o_free[2], drained[2], raw_full[3], raw_empty[3];
     uint64_t todo_full[kTodos], todo_empty[kTodos], todo_checked[kTodos];
     Todo todo[kTodos];
     int gone[kTodos];  // (once checked) whether a page of the item's walk is not in the cache
@@ -173,7 +173,8 @@ __device__ __forceinline__ bool widen16(const Vec16& codes, uint32_t byte, Vec16
     for (int x = 0; x < 4; ++x) {
         nan |= (codes.w[x] & 0x7F7F7F7Fu) + 0x01010101u;
         // the upper and the lower bytes of four results
-        const uint32_t up = (codes.w[x] >> 4 & 0x07070707u) | (codes.w[x] & 0x80808080u), low = codes.w[x] << 4 & 0xF0F0F0F0u;
+        const uint32_t up = (codes.w[x] >> 4 & 0x07070707u) | (codes.w[x] & 0x80808080u);
+        const uint32_t low = codes.w[x] << 4 & 0xF0F0F0F0u;
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w[2 * x]) : "r"(__byte_perm(low, up, 0x5140)), "r"(scale));
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w[2 * x + 1]) : "r"(__byte_perm(low, up, 0x7362)), "r"(scale));
     }
