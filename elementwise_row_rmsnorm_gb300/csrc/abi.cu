@@ -931,6 +931,7 @@ int gbe_attn_prompt_window(const void* q, int64_t q_stride, const void* k, int64
     if (T == 1) q_stride = out_stride = Hq * D, k_stride = v_stride = Hkv * D;
     if (window > 0) {
         gbe::ChunkArgs a = {};
+        a.packed = true;
         a.q = q, a.k = k, a.v = v, a.out = out;
         a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride, a.out_stride = out_stride;
         a.starts = starts;

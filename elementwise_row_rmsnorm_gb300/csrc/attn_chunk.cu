@@ -589,7 +589,7 @@ ChunkRoom chunk_room(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t
 
 cudaError_t launch_attn_chunk(const ChunkArgs& a, int dtype, bool vec, bool tensor, cudaStream_t st) {
     using namespace chunk;
-    const bool paged = a.table != nullptr, e4m3 = paged && a.c.dtype == GBE_KV_E4M3, bf16 = dtype == GBE_BF16;
+    const bool paged = !a.packed, e4m3 = paged && a.c.dtype == GBE_KV_E4M3, bf16 = dtype == GBE_BF16;
     // Tensor copies start on 16 bytes in memory and on 128 in shared memory: over an 8-bit cache rows of a multiple of 16,
     // and pages of an even number of them, for a copy of one row would be of 64 bytes.
     const bool tc = bf16 && vec && tensor && a.D <= 128 &&

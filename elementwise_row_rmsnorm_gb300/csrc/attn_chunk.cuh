@@ -63,7 +63,7 @@ inline Args make_args(const ChunkArgs& a, int rows, int tiles, int width) {
     g.tiles = tiles;
     g.width = width;
     g.window = (int)a.window, g.sinks = (int)a.sinks;  // (2^30 at most)
-    const int64_t keys = a.table == nullptr ? 0 : a.max_pages * a.c.page_size;
+    const int64_t keys = a.packed ? 0 : a.max_pages * a.c.page_size;
     const ChunkRoom r = chunk_room(a.n_seqs, a.T, a.Hq, a.Hkv, keys, a.window, a.sinks);
     g.most = r.most;
     g.per_seq = r.per_seq;
@@ -78,13 +78,12 @@ struct Seq {
 
 // starts are brought into [0, T] and lens into the table's capacity, so that no
 // row and no page outside the buffers is reached whatever they hold.
-__device__ __forceinline__ Seq sequence(const ChunkArgs& a, int64_t b) {
+__host__ __device__ __forceinline__ Seq sequence(const ChunkArgs& a, int64_t b) {
     Seq s = {0, 0, 0};
     if (b >= a.n_seqs) return s;
     s.begin = (int)min(max((int64_t)a.starts[b], (int64_t)0), a.T);
     s.n = (int)max(min(max((int64_t)a.starts[b + 1], (int64_t)0), a.T) - s.begin, (int64_t)0);
-    s.len = a.table == nullptr ? s.n
-                               : (int)min(max((int64_t)a.lens[b], (int64_t)0), a.max_pages * a.c.page_size);
+    s.len = a.packed ? s.n : (int)min(max((int64_t)a.lens[b], (int64_t)0), a.max_pages * a.c.page_size);
     return s;
 }
 

@@ -1008,7 +1008,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
 
 // k or v: pages of a cache, or packed rows; in boxes of `rows` keys of one head.
 bool encode_kv(CUtensorMap* m, const ChunkArgs& a, bool second, cuuint32_t rows) {
-    if (a.table == nullptr) {
+    if (a.packed) {
         const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hkv, (cuuint64_t)a.T};
         const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)(second ? a.v_stride : a.k_stride) * 2};
         const cuuint32_t box[3] = {64, 1, rows};
@@ -1054,7 +1054,7 @@ cudaError_t go(const ChunkArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_tc(const ChunkArgs& a, cudaStream_t st) {
-    if (a.table == nullptr) return a.D <= 64 ? go<kPacked, 64>(a, st) : go<kPacked, 128>(a, st);
+    if (a.packed) return a.D <= 64 ? go<kPacked, 64>(a, st) : go<kPacked, 128>(a, st);
     if (a.c.dtype == GBE_KV_E4M3) return a.D <= 64 ? go<GBE_KV_E4M3, 64>(a, st) : go<GBE_KV_E4M3, 128>(a, st);
     return a.D <= 64 ? go<GBE_KV_BF16, 64>(a, st) : go<GBE_KV_BF16, 128>(a, st);
 }

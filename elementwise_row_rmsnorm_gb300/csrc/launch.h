@@ -178,8 +178,10 @@ cudaError_t launch_attn_prompt(const PromptArgs& a, int dtype, bool vec, cudaStr
 cudaError_t launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t st);
 
 // New rows of each sequence against the keys that they see: of a paged cache, or
-// (table == nullptr) of packed rows k and v of their own.
+// (packed) of packed rows k and v of their own.  (A table of no columns may be at
+// NULL, so the table does not tell.)
 struct ChunkArgs {
+    bool packed;
     const void* q;
     void* out;
     int64_t q_stride, out_stride;

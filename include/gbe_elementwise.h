@@ -598,8 +598,9 @@ int gbe_attn_prompt_window(const void *q, int64_t q_stride, const void *k, int64
  *   outside [starts[0], starts[n_seqs]) are left as they were.
  * table  : device int32[n_seqs, max_pages]; lens : device int32[n_seqs].  As for
  *   gbe_attn_decode: a token on a page outside the cache takes no part, a length
- *   outside [0, max_pages * page_size] counts as the nearer end.  Rows at places
- *   below 0 (a sequence of fewer cached than new tokens) see nothing: zeros.
+ *   outside [0, max_pages * page_size] counts as the nearer end (max_pages 0: no
+ *   keys, and table may be NULL).  Rows at places below 0 (a sequence of fewer
+ *   cached than new tokens) see nothing: zeros.
  * window, sinks : as for gbe_attn_decode_window; 0, 0: none.
  * workspace : device memory of gbe_attn_chunk_workspace bytes at least, 16-byte
  *   aligned, as for gbe_attn_decode.  May be NULL when 0 bytes are needed.
