@@ -47,11 +47,6 @@ __device__ __forceinline__ float4 load_kv(const ChunkArgs& a, int kvh, int64_t a
     }
 }
 
-__device__ __forceinline__ uint32_t not_finite(float4 x) {
-    auto bad = [](float f) { return (__float_as_uint(f) & 0x7F800000u) == 0x7F800000u; };
-    return (bad(x.x) ? 1u : 0u) | (bad(x.y) ? 2u : 0u) | (bad(x.z) ? 4u : 0u) | (bad(x.w) ? 8u : 0u);
-}
-
 // Which keys of a block, as bits, a row at `place` sees: word x is of keys
 // k0 + 32 x and on.  (Places, windows and sinks are 2^30 at most.)
 __device__ __forceinline__ uint32_t first_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
@@ -128,41 +123,45 @@ static __device__ __noinline__ void exact_row(const Args& g, const Item& it, int
 
 // A row that came out not finite: right as it is where the keys that it sees
 // made it so, but a weight of zero may also have met an infinity or a NaN of v
-// in a key of its blocks that it does not see.  Computed again only if an entry
-// is not finite, has such a value there, and has none among the keys that it
-// sees.  By a whole warp; the row has been written.
+// in a key of its blocks that it does not see, which makes NaN of the entry.
+// Computed again only if an entry is NaN, has such a value there, and the values
+// that it sees do not make NaN of it by themselves: a NaN among them or
+// infinities of both signs.  (Of one sign they do not: the entry is that
+// infinity.)  By a whole warp; the row has been written.
 template <int KV>
 static __device__ __noinline__ void repair_row(const Args& g, const Item& it, int kvh, int token, int head) {
     const ChunkArgs& a = g.a;
     const int lane = threadIdx.x & 31, D = (int)a.D, place = it.s.len - it.s.n + token;
     const bool mine = lane * 4 < D;
     const Walk w = walk(g, it);
-    uint32_t open = 0;  // entries that may have to be computed again
+    Odd now;
     if (mine) {
         if (it.splits > 1)
-            open = not_finite(*reinterpret_cast<const float4*>(
+            now.meet(*reinterpret_cast<const float4*>(
                 g.part_o + part_at(g, it, token, kvh * g.group + head) * D + lane * 4));
         else
-            open = not_finite(load4(a.out, (it.s.begin + (int64_t)token) * a.out_stride +
-                                               ((int64_t)kvh * g.group + head) * D + lane * 4));
+            now.meet(load4(a.out, (it.s.begin + (int64_t)token) * a.out_stride +
+                                      ((int64_t)kvh * g.group + head) * D + lane * 4));
     }
-    // entries that a key of the blocks, seen or not, has no finite value in
-    auto among = [&](bool seen, uint32_t until) {
-        uint32_t bad = 0;
+    uint32_t open = now.nan;  // entries that may have to be computed again
+    // what they meet in the keys of the blocks, seen or not: an odd value, or of those seen ones that make NaN
+    auto among = [&](bool seen) {
+        Odd bad;
+        auto found = [&] { return seen ? bad.lost() : bad.any(); };
         for (int i = (w.to - w.from) * 4 - 1; i >= 0; --i) {
-            if (!__any_sync(0xFFFFFFFFu, until & ~bad)) break;
+            if (!__any_sync(0xFFFFFFFFu, open & ~found())) break;
             const int k0 = w.block(w.from + (i >> 2)) * kKeys;
             uint32_t keys = seen_word(g, place, k0, i & 3);
             if (!seen) keys = ~keys & first_bits(it.s.len - k0 - 32 * (i & 3));
             for (; keys; keys &= keys - 1) {
                 const int64_t at = key_at<KV>(a, it, kvh, k0 + 32 * (i & 3) + __ffs((int)keys) - 1);
-                if (at >= 0 && mine) bad |= not_finite(load_kv<KV, true>(a, kvh, at, lane * 4));
+                if (at >= 0 && mine) bad.meet(load_kv<KV, true>(a, kvh, at, lane * 4));
             }
         }
-        return bad;
+        return found();
     };
-    open &= among(false, open);
-    open &= ~among(true, open);
+    open &= among(false);
+    open &= ~among(true);
     if (__any_sync(0xFFFFFFFFu, open)) exact_row<KV>(g, it, kvh, token, head);
 }
 

@@ -25,6 +25,22 @@ __device__ __forceinline__ float2 fma2_rn(float2 a, float2 b, float2 c) {
     return d;
 }
 
+// Which of four entries have met a NaN, an infinity, one of the other sign; a bit each.
+struct Odd {
+    uint32_t nan = 0, up = 0, down = 0;
+    __device__ __forceinline__ void meet(float4 x) {
+        auto bits = [&](auto is) {
+            return (is(x.x) ? 1u : 0u) | (is(x.y) ? 2u : 0u) | (is(x.z) ? 4u : 0u) | (is(x.w) ? 8u : 0u);
+        };
+        nan |= bits([](float f) { return f != f; });
+        up |= bits([](float f) { return f == INFINITY; });
+        down |= bits([](float f) { return f == -INFINITY; });
+    }
+    __device__ __forceinline__ uint32_t any() const { return nan | up | down; }
+    // of which a weighted sum is NaN whatever the weights
+    __device__ __forceinline__ uint32_t lost() const { return nan | (up & down); }
+};
+
 // Dynamic shared memory past 48 KB is granted to a kernel once a device; one of
 // these for each kernel remembers on which devices that has been done.
 class FunctionLimit {
