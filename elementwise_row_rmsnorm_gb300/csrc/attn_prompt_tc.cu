@@ -170,39 +170,33 @@ __device__ __noinline__ void exact_row(const PromptArgs& a, int begin, int row, 
     }
 }
 
-// Which of four consecutive values are infinite or NaN, a bit each.
-__device__ __forceinline__ uint32_t not_finite4(const void* base, int64_t i) {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
-    return ((w.x & 0x7F80u) == 0x7F80u ? 1u : 0u) | ((w.x >> 16 & 0x7F80u) == 0x7F80u ? 2u : 0u) |
-           ((w.y & 0x7F80u) == 0x7F80u ? 4u : 0u) | ((w.y >> 16 & 0x7F80u) == 0x7F80u ? 8u : 0u);
-}
-
 // A row that came out not finite: right as it is where the keys that it attends
 // to made it so, but a weight of zero may also have met an infinity or a NaN of
-// v behind the mask, in rows row + 1 .. end - 1, the sequence's in the tile.
-// Computed again only if an entry is not finite, has such a value behind the
-// mask, and has none before it.  By a whole warp; the row has been written.
+// v behind the mask, in rows row + 1 .. end - 1, the sequence's in the tile,
+// which makes NaN of the entry.  Computed again only if an entry is NaN, has such
+// a value behind the mask, and the values before it do not make NaN of it by
+// themselves: a NaN among them or infinities of both signs.  (Of one sign they do
+// not: the entry is that infinity.)  By a whole warp; the row has been written.
 __device__ __noinline__ void repair_row(const PromptArgs& a, int begin, int row, int end, int head) {
     const int lane = threadIdx.x & 31, D = (int)a.D, kvh = head / (int)(a.Hq / a.Hkv);
     const bool mine = lane * 4 < D;
     const int64_t v0 = (int64_t)begin * a.v_stride + (int64_t)kvh * D + lane * 4;
     const int64_t out0 = (begin + (int64_t)row) * a.out_stride + (int64_t)head * D + lane * 4;
-    uint32_t open = mine ? not_finite4(a.out, out0) : 0u;  // entries that may have to be computed again
-    uint32_t behind = 0;
-    for (int j = row + 1; j < end && __any_sync(0xFFFFFFFFu, open & ~behind); j += 8)
+    Odd now, behind, before;
+    if (mine) now.meet(load4(a.out, out0));
+    uint32_t open = now.nan;  // entries that may have to be computed again
+    for (int j = row + 1; j < end && __any_sync(0xFFFFFFFFu, open & ~behind.any()); j += 8)
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-            if (mine && j + x < end) behind |= not_finite4(a.v, v0 + (int64_t)(j + x) * a.v_stride);
-    open &= behind;
+            if (mine && j + x < end) behind.meet(load4(a.v, v0 + (int64_t)(j + x) * a.v_stride));
+    open &= behind.any();
     for (int j = row; j >= 0; j -= 8) {
-        if (!__any_sync(0xFFFFFFFFu, open)) return;
-        uint32_t before = 0;
+        if (!__any_sync(0xFFFFFFFFu, open & ~before.lost())) return;
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-            if (mine && j - x >= 0) before |= not_finite4(a.v, v0 + (int64_t)(j - x) * a.v_stride);
-        open &= ~before;
+            if (mine && j - x >= 0) before.meet(load4(a.v, v0 + (int64_t)(j - x) * a.v_stride));
     }
-    if (__any_sync(0xFFFFFFFFu, open)) exact_row(a, begin, row, head);
+    if (__any_sync(0xFFFFFFFFu, open & ~before.lost())) exact_row(a, begin, row, head);
 }
 
 // Work item `round` of this CTA: rounds go back and forth over the CTAs, so that

@@ -72,6 +72,23 @@ def test_prompt_window(dtype, n, window, sinks, D):
             _check(got, want, tol, 0, entry, odd, window, sinks, (seen, hidden, a, b))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("n,D", [(150, 64), (300, 128), (200, 72), (150, 136)])
+def test_prompt(dtype, n, D):
+    H, Hq, entry = 2, 4, 9
+    q, k, v = (rand((n, h, D), dtype, 17 + i) for i, h in enumerate((Hq, H, H)))
+    want, tol, _ = attn_ref.prompt(q, k, v, [0, n], 0.1, dtype == BF)
+    for seen, hidden in PAIRS:
+        for a, b in ((0, n - 1), (60, 61), (100, 70), (70, 100), (n - 2, n - 1)):
+            vv, odd = v.clone(), [(b, hidden)]
+            vv[b, :, entry] = hidden
+            if seen is not None:
+                vv[a, :, entry] = seen
+                odd.append((a, seen))
+            got = gbe.attn_prompt(q, k, vv, i32([0, n]), 0.1)
+            _check(got, want, tol, 0, entry, odd, 0, 0, (seen, hidden, a, b))
+
+
 def test_chunk_over_e4m3():
     """A NaN code that a row does not see, next to rows whose own keys hold none: bf16's infinities have no code."""
     P, H, Hq, D, n, m, entry = 16, 2, 4, 64, 200, 30, 5
