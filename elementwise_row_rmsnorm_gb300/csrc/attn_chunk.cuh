@@ -22,6 +22,7 @@
 #include "attn_common.cuh"
 #include "gbe_elementwise.h"
 #include "launch.h"
+#include "patience.h"
 
 namespace gbe {
 namespace chunk {
@@ -47,6 +48,7 @@ struct Args {
     int width;             // keys of a block
     int window, sinks;     // a's
     int most;              // splits at most; 1: nothing is cut
+    uint32_t patience;     // of waits that may last for an item
     int64_t per_seq;       // places for each sequence's; 0: `most` for each row
     float* part_o;         // [places, D]
     float2* part_ml;       // [places]: running maximum (base 2), running sum
@@ -62,6 +64,7 @@ inline Args make_args(const ChunkArgs& a, int rows, int tiles, int width) {
     g.tokens = rows / g.heads;
     g.tiles = tiles;
     g.width = width;
+    g.patience = patience_for((a.packed ? a.T : a.max_pages * a.c.page_size) / width);
     g.window = (int)a.window, g.sinks = (int)a.sinks;  // (2^30 at most)
     const int64_t keys = a.packed ? 0 : a.max_pages * a.c.page_size;
     const ChunkRoom r = chunk_room(a.n_seqs, a.T, a.Hq, a.Hkv, keys, a.window, a.sinks);

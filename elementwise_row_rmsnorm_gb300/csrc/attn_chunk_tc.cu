@@ -85,7 +85,7 @@ struct Control {
     Todo todo[kTodos];
     int gone[kTodos];  // (once checked) whether a page of the item's walk is not in the cache
     uint32_t tmem;
-    int abort;
+    int state;  // of the CTA (patience.h)
 };
 
 template <int KV, int DP>
@@ -197,11 +197,13 @@ __device__ __forceinline__ void widen16_f32(const Vec16& codes, uint32_t byte, V
 // The warps that widen an 8-bit cache's rows, as the copying warp brings them,
 // into the ring.  Loads are counted over all items: k of block b is 2 b, v 2 b + 1.
 template <int DP>
-__device__ __forceinline__ void widen_rows(Control& ctl, uint8_t* const smem) {
+__device__ __forceinline__ void widen_rows(Control& ctl, uint8_t* const smem, const Args& g) {
     using S = Shape<GBE_KV_E4M3, DP>;
     constexpr int kPieces = DP / 16, kRows = kWidenWarps * 32 / kPieces, kTurns = kN / kRows;
     const int tid = threadIdx.x - kWidenWarp * 32, lane = threadIdx.x & 31;
-    volatile int* const abort = &ctl.abort;
+    volatile int* const state = &ctl.state;
+    auto until = [&](uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity, state); };
+    auto until_item = [&](uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity, state, g.patience); };
     // Eight lanes have four pieces of 16 codes of two rows: what they read, and what
     // they write, a piece's halves one after the other, meets eight bank groups.
     const int panel = DP == 128 ? tid >> 3 & 1 : 0, piece = tid & 3;
@@ -210,15 +212,15 @@ __device__ __forceinline__ void widen_rows(Control& ctl, uint8_t* const smem) {
     uint8_t* const to = smem + 2 * S::kTile + panel * S::kPanel + r0 * 128;
     int load = 0;
     for (int i = 0;; ++i) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.todo_full[i % kTodos]), i / kTodos & 1, abort))) return;
+        if (!__all_sync(0xFFFFFFFFu, until_item(smem_addr(&ctl.todo_full[i % kTodos]), i / kTodos & 1))) return;
         const int n = ctl.todo[i % kTodos].blocks(), slot = ctl.todo[i % kTodos].slot;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&ctl.todo_empty[i % kTodos]));
         if (slot < 0) return;
         for (const int end = load + 2 * n; load < end; ++load) {
             const int raw = load % S::kRaws, stage = load % S::kStages;
-            bool ok = mbar_wait(smem_addr(&ctl.raw_full[raw]), load / S::kRaws & 1, abort);
-            ok = ok && mbar_wait(smem_addr(&ctl.kv_empty[stage]), (load / S::kStages & 1) ^ 1, abort);
+            bool ok = until(smem_addr(&ctl.raw_full[raw]), load / S::kRaws & 1);
+            ok = ok && until(smem_addr(&ctl.kv_empty[stage]), (load / S::kStages & 1) ^ 1);
             if (!__all_sync(0xFFFFFFFFu, ok)) return;
             const uint8_t* const scale = smem + S::kScaleAt + load % (2 * S::kAhead) * kN + r0;
             auto codes = [&](int x) { return *reinterpret_cast<const Vec16*>(from + raw * S::kRaw + x * (kRows * 64)); };
@@ -264,7 +266,8 @@ __device__ __forceinline__ bool load_codes(Control& ctl, uint8_t* const smem, co
     const KvCacheArgs& c = g.a.c;
     const int lane = threadIdx.x & 31, size = c.page_size, boxes = kN / box;
     const int32_t* const table = g.a.table + seq * g.a.max_pages;
-    volatile int* const abort = &ctl.abort;
+    volatile int* const state = &ctl.state;
+    auto until = [&](uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity, state); };
     const uint32_t pages = smem_addr(smem) + S::kPageAt, scales = smem_addr(smem) + S::kScaleAt;
     const int base = loads / 2 - w.from;  // block x of the walk is block base + x of all
     auto ask_page = [&](int x) {
@@ -304,7 +307,7 @@ __device__ __forceinline__ bool load_codes(Control& ctl, uint8_t* const smem, co
         for (int kv = 0; kv < 2; ++kv, ++loads) {
             const int stage = loads % S::kRaws;
             ok = __all_sync(0xFFFFFFFFu,
-                            mbar_wait(smem_addr(&ctl.raw_empty[stage]), (loads / S::kRaws & 1) ^ 1, abort));
+                            until(smem_addr(&ctl.raw_empty[stage]), (loads / S::kRaws & 1) ^ 1));
             if (!ok) return false;
             const uint32_t full = smem_addr(&ctl.raw_full[stage]);
             const uint32_t to = smem_addr(smem) + S::kRawAt + stage * S::kRaw + lane * box * 64;
@@ -339,7 +342,11 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
     Control& ctl = *reinterpret_cast<Control*>(smem + S::kControlAt);
     const uint32_t q_smem = base, kv_smem = base + 2 * S::kTile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    volatile int* const abort = &ctl.abort;
+    volatile int* const state = &ctl.state;
+    // for what a block's copies, products and weights take, and for an item (of which each slot may have another: the
+    // first S of one comes behind the last keys of the other)
+    auto until = [&](uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity, state); };
+    auto until_item = [&](uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity, state, g.patience); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
@@ -366,7 +373,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
             mbar_init(smem_addr(&ctl.todo_checked[i]), 1);
             mbar_init(smem_addr(&ctl.todo_empty[i]), S::kReaders);
         }
-        ctl.abort = 0;
+        ctl.state = 0;
         mbar_init_fence();
         tma_prefetch(&maps.q);
         tma_prefetch(&maps.k);
@@ -381,12 +388,12 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
     const uint32_t tmem = ctl.tmem;
 
     // false: a wait gave up
-    auto todo_ready = [&](int i) { return mbar_wait(smem_addr(&ctl.todo_full[i % kTodos]), i / kTodos & 1, abort); };
+    auto todo_ready = [&](int i) { return until_item(smem_addr(&ctl.todo_full[i % kTodos]), i / kTodos & 1); };
     auto todo_read = [&](int i) { mbar_arrive(smem_addr(&ctl.todo_empty[i % kTodos])); };
 
     if (S::kE4 && warp >= kWidenWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kWidenRegs));
-        if constexpr (S::kE4) widen_rows<DP>(ctl, smem);
+        if constexpr (S::kE4) widen_rows<DP>(ctl, smem, g);
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kIssueRegs));
         if (warp == kItemWarp) {
@@ -402,7 +409,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                     if (q_item.tiles == 2 || t == q_slot) {
                         const uint32_t bar = smem_addr(&ctl.q_empty[t]);
                         if (!wait && !__all_sync(0xFFFFFFFFu, mbar_try(bar, (tiles[t] & 1) ^ 1))) return;
-                        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, (tiles[t] & 1) ^ 1, abort));
+                        ok = ok && __all_sync(0xFFFFFFFFu, until_item(bar, (tiles[t] & 1) ^ 1));
                         if (!ok) return;
                     }
                 for (int t = 0; t < 2; ++t)
@@ -431,7 +438,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                     if (todo.blocks() > 0) last = todo.two() ? 1 : todo.slot;
                 }
                 ok = __all_sync(0xFFFFFFFFu,
-                                mbar_wait(smem_addr(&ctl.todo_empty[i % kTodos]), (i / kTodos & 1) ^ 1, abort));
+                                until_item(smem_addr(&ctl.todo_empty[i % kTodos]), (i / kTodos & 1) ^ 1));
                 if (!ok) break;
                 if (lane == 0) {
                     ctl.todo[i % kTodos] = todo;
@@ -459,7 +466,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                     }
                 }
             }
-            if (*abort && lane == 0) {  // nothing may still be on its way when the CTA ends
+            if (*state > 0 && lane == 0) {  // nothing may still be on its way when the CTA ends
                 int none = 0;
                 for (int t = 0; t < 2; ++t)
                     if (tiles[t] > 0) mbar_wait(smem_addr(&ctl.q_full[t]), (tiles[t] - 1) & 1, &none);
@@ -543,8 +550,8 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                         constexpr int kRing = S::kE4 ? S::kRaws : S::kStages, kBytes = S::kE4 ? S::kRaw : S::kTile;
                         const int stage = loads % kRing;
                         ok = __all_sync(0xFFFFFFFFu,
-                                        mbar_wait(smem_addr(S::kE4 ? &ctl.raw_empty[stage] : &ctl.kv_empty[stage]),
-                                                  (loads / kRing & 1) ^ 1, abort));
+                                        until(smem_addr(S::kE4 ? &ctl.raw_empty[stage] : &ctl.kv_empty[stage]),
+                                              (loads / kRing & 1) ^ 1));
                         if (!ok) break;
                         const uint32_t full = smem_addr(S::kE4 ? &ctl.raw_full[stage] : &ctl.kv_full[stage]);
                         const uint32_t to = S::kE4 ? smem_addr(smem) + S::kRawAt + stage * kBytes : kv_smem + stage * kBytes;
@@ -590,7 +597,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                 }
             }
             __syncwarp();
-            if (*abort && lane == 0) {  // as above
+            if (*state > 0 && lane == 0) {  // as above
                 int none = 0;
                 constexpr int kRing = S::kE4 ? S::kRaws : S::kStages;
                 for (int x = max(0, loads - kRing); x < loads; ++x)
@@ -618,22 +625,22 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                 if (slot < 0) break;
                 if (n == 0) continue;
                 auto loaded = [&](int x) {
-                    ok = ok && mbar_wait(smem_addr(&ctl.kv_full[x % S::kStages]), x / S::kStages & 1, abort);
+                    ok = ok && until(smem_addr(&ctl.kv_full[x % S::kStages]), x / S::kStages & 1);
                 };
                 // S is free for an item once the last block of the item before has been read.  Both threads wait for
                 // that at every item, so that neither passes over a phase (a wait by parity holds only where the phase
                 // before has completed); two barriers in turn, for a thread may be as far behind as the other's item.
                 if (!S::kE4 && every > 0)
-                    ok = mbar_wait(smem_addr(&ctl.s_last[(every - 1) & 1]), (every - 1) / 2 & 1, abort);
+                    ok = until(smem_addr(&ctl.s_last[(every - 1) & 1]), (every - 1) / 2 & 1);
                 // And within it once the block before in the order (0, j), (1, j), (0, j + 1), ... has been.  (Over an
                 // 8-bit cache it is free once the weights that took its place have met v.)
                 auto s_free = [&](int j) {
                     if constexpr (S::kE4) {
                         if (done[t] + j > 0)
-                            ok = ok && mbar_wait(smem_addr(&ctl.o_done[t]), (done[t] + j - 1) & 1, abort);
+                            ok = ok && until(smem_addr(&ctl.o_done[t]), (done[t] + j - 1) & 1);
                     } else {
                         const int pt = !two ? t : t ^ 1, pj = two && t == 1 ? j : j - 1;
-                        if (pj >= 0) ok = ok && mbar_wait(smem_addr(&ctl.s_free[pt]), (done[pt] + pj) & 1, abort);
+                        if (pj >= 0) ok = ok && until(smem_addr(&ctl.s_free[pt]), (done[pt] + pj) & 1);
                     }
                 };
                 auto scores = [&](int j) {
@@ -653,7 +660,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                     if (j + 1 == n) mma_commit(smem_addr(&ctl.q_empty[t]));
                 };
                 if (mine) {
-                    ok = ok && mbar_wait(smem_addr(&ctl.q_full[t]), items & 1, abort);
+                    ok = ok && until(smem_addr(&ctl.q_full[t]), items & 1);
                     if (!S::kE4) scores(0);
                 }
                 for (int j = 0; ok && mine && j < n; ++j) {
@@ -663,9 +670,9 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                         scores(j + 1);
                     const int x = loads + 2 * j + 1, stage = x % S::kStages;
                     loaded(x);
-                    ok = ok && mbar_wait(smem_addr(&ctl.p_ready[t]), (done[t] + j) & 1, abort);
+                    ok = ok && until(smem_addr(&ctl.p_ready[t]), (done[t] + j) & 1);
                     // O has been read for the last item
-                    if (j == 0 && items > 0) ok = ok && mbar_wait(smem_addr(&ctl.o_free[t]), (items - 1) & 1, abort);
+                    if (j == 0 && items > 0) ok = ok && until(smem_addr(&ctl.o_free[t]), (items - 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t v0 = v_lo + stage * (S::kTile >> 4);
@@ -719,7 +726,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
             bool gone = false;  // whether pages of the walk are not in the cache
             if constexpr (KV != kPacked) {
                 ok = __all_sync(0xFFFFFFFFu,
-                                mbar_wait(smem_addr(&ctl.todo_checked[i % kTodos]), i / kTodos & 1, abort));
+                                until_item(smem_addr(&ctl.todo_checked[i % kTodos]), i / kTodos & 1));
                 if (!ok) break;
                 gone = ctl.gone[i % kTodos];
             }
@@ -742,10 +749,10 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
             const int low = g.window > 0 ? __shfl_sync(0xFFFFFFFFu, place, 31) - g.window : -1;
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; idle && j < n; ++j) {
-                ok = mbar_wait(smem_addr(&ctl.s_full[t]), (done + j) & 1, abort);
+                ok = until_item(smem_addr(&ctl.s_full[t]), (done + j) & 1);
                 if (!S::kE4) s_read(j);
                 // (no sooner than the others: it would be counted for the weights before)
-                if (j > 0) ok = ok && mbar_wait(smem_addr(&ctl.o_done[t]), (done + j - 1) & 1, abort);
+                if (j > 0) ok = ok && until(smem_addr(&ctl.o_done[t]), (done + j - 1) & 1);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[t]));
@@ -763,7 +770,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                     }
                     __syncwarp();
                 }
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.s_full[t]), (done + j) & 1, abort));
+                ok = __all_sync(0xFFFFFFFFu, until_item(smem_addr(&ctl.s_full[t]), (done + j) & 1));
                 if (!ok) break;
                 tc_fence_after();
                 // a word's bits: which of 32 keys of the block are seen; the maximum of some logits, what is in use moved up
@@ -773,7 +780,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                     return word;
                 };
                 auto last_done = [&] {  // the product with the last weights is done
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.o_done[t]), (done + j - 1) & 1, abort));
+                    ok = __all_sync(0xFFFFFFFFu, until(smem_addr(&ctl.o_done[t]), (done + j - 1) & 1));
                     tc_fence_after();
                 };
                 auto move_up = [&](float top) {
@@ -908,7 +915,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
             }
             every += n > 0;
             done += n;
-            if (n > 0) ok = ok && mbar_wait(smem_addr(&ctl.o_done[t]), (done - 1) & 1, abort);
+            if (n > 0) ok = ok && until(smem_addr(&ctl.o_done[t]), (done - 1) & 1);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -990,11 +997,14 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
             }
             uint32_t again = __ballot_sync(0xFFFFFFFFu, mine.there && bad.x + bad.y != 0.0f);
             __syncwarp();
-            while (again) {
-                const int r = __ffs((int)again) - 1;
-                again &= again - 1;
-                repair_row<KV>(g, it, kvh, __shfl_sync(0xFFFFFFFFu, mine.token, r),
-                               __shfl_sync(0xFFFFFFFFu, mine.head, r));
+            if (again) {
+                if (lane == 0) long_work_begins(state);
+                for (; again; again &= again - 1) {
+                    const int r = __ffs((int)again) - 1;
+                    repair_row<KV>(g, it, kvh, __shfl_sync(0xFFFFFFFFu, mine.token, r),
+                                   __shfl_sync(0xFFFFFFFFu, mine.head, r));
+                }
+                if (lane == 0) long_work_ends(state);
             }
             if (lane == 0) todo_read(i);
         }
@@ -1003,7 +1013,7 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == kMmaWarp) tmem_free(tmem, 512);
-    if (*abort && warp == 0) give_up(g);
+    if (*state > 0 && warp == 0) give_up(g);
 }
 
 // k or v: pages of a cache, or packed rows; in boxes of `rows` keys of one head.

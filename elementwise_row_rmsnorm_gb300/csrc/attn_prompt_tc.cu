@@ -86,7 +86,7 @@ struct Control {
     uint64_t item_full[kItems], item_empty[kItems];
     Item item[kItems];
     uint32_t tmem;
-    int abort;
+    int state;  // of the CTA (patience.h)
 };
 
 template <int DP>
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t q_smem = base, kv_smem = base + 2 * S::kTile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = (int)(a.Hq / a.Hkv);
-    volatile int* const abort = &ctl.abort;
+    volatile int* const state = &ctl.state;
 
     if (threadIdx.x == 0) {
         mbar_init(smem_addr(&ctl.q_full[0]), 1);
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(smem_addr(&ctl.drained[0]), 1);
         mbar_init(smem_addr(&ctl.drained[1]), 1);
-        ctl.abort = 0;
+        ctl.state = 0;
         mbar_init_fence();
         tma_prefetch(&mq);
         tma_prefetch(&mk);
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return w;
     };
     // false: a wait gave up
-    auto item_ready = [&](int i) { return mbar_wait(smem_addr(&ctl.item_full[i % kItems]), i / kItems & 1, abort); };
+    auto item_ready = [&](int i) { return mbar_wait(smem_addr(&ctl.item_full[i % kItems]), i / kItems & 1, state); };
     auto item_read = [&](int i) { mbar_arrive(smem_addr(&ctl.item_empty[i % kItems])); };
 
     // Registers: 384 threads were launched with 168 each (64512); the softmax
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (it.p.units == 0) continue;
                 }
                 ok = __all_sync(0xFFFFFFFFu,
-                                mbar_wait(smem_addr(&ctl.item_empty[i % kItems]), (i / kItems & 1) ^ 1, abort));
+                                mbar_wait(smem_addr(&ctl.item_empty[i % kItems]), (i / kItems & 1) ^ 1, state));
                 if (!ok) break;
                 if (lane == 0) {
                     ctl.item[i % kItems] = it;
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (w.units < 0) break;
                     for (int x = 0; ok && x < 2 * w.most; ++x) {  // k and v of each block in turn
                         const int stage = g % S::kStages;
-                        ok = mbar_wait(smem_addr(&ctl.kv_empty[stage]), (g / S::kStages & 1) ^ 1, abort);
+                        ok = mbar_wait(smem_addr(&ctl.kv_empty[stage]), (g / S::kStages & 1) ^ 1, state);
                         if (!ok) break;
                         const uint32_t full = smem_addr(&ctl.kv_full[stage]);
                         mbar_arrive_tx(full, S::kTile);
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         ++g;
                         if (x == 0) {  // q, once the last item's is done with
-                            ok = mbar_wait(smem_addr(&ctl.q_empty), (i & 1) ^ 1, abort);
+                            ok = mbar_wait(smem_addr(&ctl.q_empty), (i & 1) ^ 1, state);
                             if (!ok) break;
                             for (int t = 0; t < w.units; ++t) {
                                 const uint32_t qb = smem_addr(&ctl.q_full[t]);
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (*abort) {  // nothing may still be on its way when the CTA ends
+                if (*state > 0) {  // nothing may still be on its way when the CTA ends
                     int none = 0;
                     for (int t = 0; t < 2; ++t)
                         if (tiles[t] > 0) mbar_wait(smem_addr(&ctl.q_full[t]), (tiles[t] - 1) & 1, &none);
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (w.units < 0) break;
                 const int mine = w.blocks[t], theirs = w.blocks[t ^ 1];
                 auto loaded = [&](int x) {
-                    ok = ok && mbar_wait(smem_addr(&ctl.kv_full[x % S::kStages]), x / S::kStages & 1, abort);
+                    ok = ok && mbar_wait(smem_addr(&ctl.kv_full[x % S::kStages]), x / S::kStages & 1, state);
                 };
                 // S is free once the block before in the order (0, j), (1, j), (0, j + 1), ... has been read
                 auto s_free = [&](int j) {
@@ -405,9 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // passed over the first one's blocks of an item before that has no second tile: S of this item's
                     // first block, once it is there, says that those have been read.
                     if (t == 1 && j == 0 && last_t == 0)
-                        ok = ok && mbar_wait(smem_addr(&ctl.s_full[0]), done[0] & 1, abort);
+                        ok = ok && mbar_wait(smem_addr(&ctl.s_full[0]), done[0] & 1, state);
                     if (pt >= 0)
-                        ok = ok && mbar_wait(smem_addr(&ctl.s_free[pt]), (done[pt] + pj) & 1, abort);
+                        ok = ok && mbar_wait(smem_addr(&ctl.s_free[pt]), (done[pt] + pj) & 1, state);
                 };
                 auto scores = [&](int j) {
                     loaded(g + 2 * j);
@@ -426,8 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j + 1 == mine) mma_commit(smem_addr(&ctl.q_empty));
                 };
                 // (an item has a first tile always, a second one not)
-                ok = mine > 0 ? mbar_wait(smem_addr(&ctl.q_full[t]), items & 1, abort)
-                              : mbar_wait(smem_addr(&ctl.q_full[0]), i & 1, abort);
+                ok = mine > 0 ? mbar_wait(smem_addr(&ctl.q_full[t]), items & 1, state)
+                              : mbar_wait(smem_addr(&ctl.q_full[0]), i & 1, state);
                 if (mine > 0)
                     scores(0);
                 else if (ok)
@@ -435,10 +435,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; ok && j < mine; ++j) {
                     if (j + 1 < mine) scores(j + 1);
                     loaded(g + 2 * j + 1);
-                    ok = ok && mbar_wait(smem_addr(&ctl.p_ready[t]), (done[t] + j) & 1, abort);
+                    ok = ok && mbar_wait(smem_addr(&ctl.p_ready[t]), (done[t] + j) & 1, state);
                     // O has been read for the last item
                     if (j == 0 && items > 0)
-                        ok = ok && mbar_wait(smem_addr(&ctl.o_free[t]), (items - 1) & 1, abort);
+                        ok = ok && mbar_wait(smem_addr(&ctl.o_free[t]), (items - 1) & 1, state);
                     if (!ok) break;
                     tc_fence_after();
                     const int stage = (g + 2 * j + 1) % S::kStages;
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = u / group * kM + (threadIdx.x & 127);
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < n; ++j) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.s_full[t]), (done + j) & 1, abort));
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.s_full[t]), (done + j) & 1, state));
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t s[128];
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const bool grow = m == -INFINITY ? top > m : (top - m) * c > kGrowth;
                 auto last_done = [&] {  // the product with the last weights is done
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.o_done[t]), (done + j - 1) & 1, abort));
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&ctl.o_done[t]), (done + j - 1) & 1, state));
                     tc_fence_after();
                 };
                 if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[t]));
             }
             done += n;
-            ok = ok && mbar_wait(smem_addr(&ctl.o_done[t]), (done - 1) & 1, abort);
+            ok = ok && mbar_wait(smem_addr(&ctl.o_done[t]), (done - 1) & 1, state);
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
             const int head = it.kvh * group + u % group;
@@ -612,10 +612,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             uint32_t again = __ballot_sync(0xFFFFFFFFu, ok && live && bad.x + bad.y != 0.0f);
             __syncwarp();
-            while (again) {
-                const int r = __ffs((int)again) - 1;
-                again &= again - 1;
-                repair_row(a, it.p.begin, row0 + r, min(u / group * kM + kM, it.p.len), head);
+            if (again) {
+                if (lane == 0) long_work_begins(state);
+                for (; again; again &= again - 1)
+                    repair_row(a, it.p.begin, row0 + __ffs((int)again) - 1, min(u / group * kM + kM, it.p.len), head);
+                if (lane == 0) long_work_ends(state);
             }
         }
         // a wait that gave up: NaN in every row of this CTA's tiles, done or not

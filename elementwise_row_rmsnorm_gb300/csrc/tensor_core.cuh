@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <stdint.h>
 
+#include "patience.h"
+
 namespace gbe {
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -33,25 +35,31 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Waits for the phase of this parity to complete; gives up after ten seconds,
-// or when another thread of the CTA has (*abort), so that no wait is without
-// an end.  Returns whether the phase completed.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+// Waits for the phase of this parity to complete; gives up after `limit` ticks in
+// which no warp of the CTA was at long work, or when another of its threads has, so
+// that no wait is without an end (patience.h).  Returns whether the phase completed.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* state,
+                                          uint32_t limit = kPatience) {
     if (mbar_try(bar, parity)) return true;
-    unsigned long long t0 = 0, t;
+    Patience patience;
     for (int i = 1;; ++i) {
         if (mbar_try(bar, parity)) return true;
         if ((i & 63) == 0) {
-            if (*abort) return false;
+            const int now = *state;
+            if (now > 0) return false;
+            unsigned long long t;
             asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-            if (t0 == 0) t0 = t;
-            if (t - t0 > 10000000000ull) {
-                *abort = 1;
+            if (patience.over((uint32_t)(t >> 20), now, limit)) {
+                *state = kGaveUp;
                 return false;
             }
         }
     }
 }
+
+// Around work that has an end but may take long, by one thread.
+__device__ __forceinline__ void long_work_begins(volatile int* state) { atomicSub(const_cast<int*>(state), 1); }
+__device__ __forceinline__ void long_work_ends(volatile int* state) { atomicAdd(const_cast<int*>(state), 1); }
 
 // True in one thread of a converged warp.  The compiler knows that a branch on
 // it runs a single thread, and so keeps the operands of the instructions in it
