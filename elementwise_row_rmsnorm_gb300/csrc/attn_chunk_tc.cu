@@ -596,8 +596,9 @@ __global__ void __launch_bounds__(Shape<KV, DP>::kThreads, 1)
                     look_up(x + 1, lane, page, row);
                 }
             }
+            if constexpr (S::kE4) cp_async_wait<0>();  // as above
             __syncwarp();
-            if (*state > 0 && lane == 0) {  // as above
+            if (*state > 0 && lane == 0) {
                 int none = 0;
                 constexpr int kRing = S::kE4 ? S::kRaws : S::kStages;
                 for (int x = max(0, loads - kRing); x < loads; ++x)
