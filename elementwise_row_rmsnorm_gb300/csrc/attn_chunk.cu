@@ -44,7 +44,7 @@ struct Places {
 
 // 64 rows into shared memory as f32; zeros where there is none and behind D.
 // SRC: the type that memory holds.
-template <int SRC, int DP, bool VEC>
+template <int SRC, int DP>
 __device__ __forceinline__ void stage(float* dst, const void* src, const uint8_t* scales, const Places& pl, int D) {
     constexpr int W = DP + 4;
     for (int i = threadIdx.x & (kThreads - 1); i < kN * (DP / 8); i += kThreads) {
@@ -61,7 +61,7 @@ __device__ __forceinline__ void stage(float* dst, const void* src, const uint8_t
 #pragma unroll
                     for (int e = 0; e < 8; ++e) f[e] *= s;
                 }
-            } else if constexpr (VEC) {
+            } else {
                 constexpr int V = Store<SRC>::V;
 #pragma unroll
                 for (int p = 0; p < 8 / V; ++p) {
@@ -71,9 +71,6 @@ __device__ __forceinline__ void stage(float* dst, const void* src, const uint8_t
 #pragma unroll
                     for (int e = 0; e < V; ++e) f[p * V + e] = g[e];
                 }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = Store<SRC>::load1(src, at + d + e);
             }
         }
         float4* o = reinterpret_cast<float4*>(dst + r * W + d);
@@ -237,7 +234,7 @@ __global__ void __launch_bounds__(kThreads* kGroups<DP>, 1) chunk_rows(const __g
             } else if constexpr (ASYNC) {
                 stage_async<DP>(dst, static_cast<const float*>(src), pl, D);
             } else {
-                stage<SRC, DP, true>(dst, src, scales, pl, D);
+                stage<SRC, DP>(dst, src, scales, pl, D);
                 asm volatile("cp.async.commit_group;" ::: "memory");
             }
         };
