@@ -1011,7 +1011,8 @@ int gbe_attn_chunk(const void* q, int64_t q_stride, void* out, int64_t out_strid
     const bool vec = aligned16(q) && aligned16(out) && (q_stride * es) % 16 == 0 && (out_stride * es) % 16 == 0;
     if (T == 1) q_stride = out_stride = Hq * D;
     a.q = q, a.out = out, a.q_stride = q_stride, a.out_stride = out_stride;
-    a.table = table, a.lens = lens, a.max_pages = max_pages;
+    // (a cache of no pages, which may be at NULL, holds no keys: no copy of no bytes from there either)
+    a.table = table, a.lens = lens, a.max_pages = a.c.n_pages > 0 ? max_pages : 0;
     a.starts = starts, a.n_seqs = n_seqs, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.D = D;
     a.window = window, a.sinks = sinks, a.scale = scale;
     a.workspace = workspace;

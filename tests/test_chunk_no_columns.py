@@ -66,3 +66,18 @@ def test_zeros(dtype, kind, D):
                 assert bool((view[:2] == 9.0).all()) and bool((view[38:] == 9.0).all())
                 one = gbe.attn_decode_window(q[:3].contiguous(), cache, table, i32([70, 9, -4]), window, sinks)
                 assert bool((one == 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,kind", [(F32, F32), (F32, F8), (BF, BF), (BF, F8)])
+@pytest.mark.parametrize("D", [64, 136])
+def test_a_cache_of_no_pages(dtype, kind, D):
+    """Every token lies on a page that is not there."""
+    P, H, Hq, T = 16, 2, 8, 40
+    cache = gbe.kv_cache(0, H, P, D, kind)
+    table, lens = torch.zeros(2, 200, dtype=torch.int32, device="cuda"), i32([3000, 9])
+    q = rand((T, Hq, D), dtype, 6)
+    for window, sinks in ((0, 0), (5, 2)):
+        out = gbe.attn_chunk(q, cache, i32([0, 35, T]), table, lens, 0.1, window, sinks)
+        assert bool((out == 0).all())
+        assert bool((gbe.attn_decode_window(q[:2], cache, table, lens, window, sinks) == 0).all())
