@@ -608,7 +608,8 @@ def gbe_attn_decode_window(q, out, cache: KvCache, table, lens, window: int, sin
 
 def attn_chunk_workspace(n_seqs: int, T: int, Hq: int, cache: KvCache, max_pages: int, window: int = 0,
                          sinks: int = 0) -> int:
-    """Bytes of workspace of gbe_attn_chunk for T new tokens of n_seqs sequences of at most max_pages pages."""
+    """Bytes of workspace of gbe_attn_chunk for T new tokens of n_seqs sequences of at most max_pages pages: they go by
+    max_pages, not by lengths, so a table cut to the longest sequence's pages needs fewer."""
     _, H, P, D = cache.shape
     n = lib().gbe_attn_chunk_workspace(n_seqs, T, Hq, H, D, P, max_pages, window, sinks)
     if n < 0:
@@ -766,7 +767,8 @@ def attn_prompt_window(q, k, v, starts, window: int, sinks: int = 0, scale: floa
 def attn_chunk(q, cache: KvCache, starts, table, lens, scale: float | None = None, window: int = 0, sinks: int = 0,
                workspace=None, stream=None):
     """[T, Hq, D] of the new tokens packed in q; rows outside [starts[0], starts[-1]) are not written; allocates the
-    workspace unless one is given."""
+    workspace (attn_chunk_workspace bytes, many for a wide table) unless one is given.  The scale comes ahead of window
+    and sinks here and behind them in attn_decode_window and attn_prompt_window: name them."""
     out = _like(q, stream)
     if workspace is None:
         n = attn_chunk_workspace(lens.numel(), q.shape[0], q.shape[1], cache, table.shape[1], window, sinks)

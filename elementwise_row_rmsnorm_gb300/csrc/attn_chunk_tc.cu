@@ -36,11 +36,19 @@
 // O is rescaled only when a row's maximum has grown by more than 2^8 over the
 // one in use, as in attn_prompt_tc.cu.
 //
+// Weights are one bf16, 8 bits, as there and for the same reason: it is what a
+// product with bf16 keys takes, and tensor memory is full (S, two tiles' weights, two
+// O).  Results are 1.25 to 1.4 times as far from the definition as their own rounding
+// leaves them (0.0021 to 0.0023 of their norm, 0.0016 to 0.0017); a single token's
+// decode, which adds the rest of each weight as a second bf16, 1.0 times.  Sums of
+// weights and of products are f32.
+//
 // Measured, with 32 heads over 8 of D 128 and pages of 64: 2048 tokens behind 30720
-// 715 us, 1480 TFLOP/s (softmax and products take turns on what the SM issues);
-// 24 sequences of up to 200 behind up to 8000 227 us; 64 of 5 behind 8000 412 us,
-// 5.1 TB/s of keys; a prompt of 8192 under a window of 1024 127 us.  Over an 8-bit
-// cache the widening bounds it: 2048 behind 30720 1.17 ms, 64 of 5 behind 8000 535 us
+// 720 to 780 us, 1.37 to 1.46 PFLOP/s (softmax and products take turns on what the SM
+// issues; the longer a GPU is kept at it, the slower); 24 sequences of up to 200 behind
+// up to 8000 228 us; 64 of 5 behind 8000 412 us, 5.1 TB/s of keys; a prompt of 8192
+// under a window of 1024 131 to 136 us.  Over an 8-bit cache the widening bounds it:
+// 2048 behind 30720 1.17 ms, 64 of 5 behind 8000 530 to 545 us
 // (eight warps take 1.2 to 1.5 thousand clocks for a block's k, as many for its v;
 // with four 650 us, and one warp that waited for each block's pages and then for its
 // scales 620).  Not kept: slots that share one tile's blocks, every other one each (545

@@ -623,7 +623,11 @@ int gbe_attn_chunk(const void *q, int64_t q_stride, void *out, int64_t out_strid
                    int64_t max_pages, const int32_t *lens, int64_t window, int64_t sinks, float scale,
                    void *workspace, int64_t workspace_bytes, int dtype, gbe_stream stream);
 
-/* The bytes of workspace that gbe_attn_chunk needs; -1 when it would refuse the sizes. */
+/* The bytes of workspace that gbe_attn_chunk needs; -1 when it would refuse the
+ * sizes.  They go by the table's width, not by lengths: up to 4 (D + 2) bytes for
+ * each row, query head and 1024 tokens of max_pages * page_size, or 1245184 (D + 2)
+ * for each sequence, whichever is less in all (0 below 2048 tokens).  A table no wider
+ * than the longest sequence keeps them small. */
 int64_t gbe_attn_chunk_workspace(int64_t n_seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,
                                  int64_t max_pages, int64_t window, int64_t sinks);
 
